@@ -90,6 +90,13 @@ _SIGS = {
     "dflash_stamps_arm": (ctypes.c_int, [_vp, _vp, ctypes.c_int32]),
     "dflash_harness_verify": (ctypes.c_int, [_vp, _vp, ctypes.c_int32, _vp, _vp, _vp, ctypes.c_int32, _vp,
                                              _vp, _vp, ctypes.c_int32, _vp, _vp]),
+    # operators of the caller's own target model (ops.py); structs are passed packed
+    "dflash_rope_init": (ctypes.c_int, [_vp, _vp]),
+    "dflash_rope": (ctypes.c_int, [_vp, ctypes.c_char_p, _vp]),
+    "dflash_paged_append": (ctypes.c_int, [ctypes.c_char_p, _vp, ctypes.c_char_p, _vp]),
+    "dflash_paged_attention_workspace": (ctypes.c_size_t, [ctypes.c_char_p, ctypes.c_int32, ctypes.c_int32,
+                                                           ctypes.c_int32]),
+    "dflash_paged_attention": (ctypes.c_int, [ctypes.c_char_p, ctypes.c_char_p, _vp]),
 }
 
 _LIB = None

@@ -220,3 +220,34 @@ cudaError_t launch_harness_verify(const int* slots, int batch, int S, const int*
                                   const bf16* feat_stream, int stream_rows, bf16* feats_out, int F,
                                   const int* ctx_len, int max_slots, unsigned long long* stamp,
                                   unsigned* blocks_done, cudaStream_t s);
+
+// ---- operators of the caller's own target model (rope.cu, paged_attention.cu)
+
+// Makes `device` current for a call and gives the caller's back.
+struct DeviceGuard {
+  int before = -1;
+  bool ok;
+  explicit DeviceGuard(int device) {
+    ok = cudaGetDevice(&before) == cudaSuccess;
+    if (ok && before == device) before = -1;  // nothing to give back
+    else if (ok) ok = cudaSetDevice(device) == cudaSuccess;
+  }
+  ~DeviceGuard() {
+    if (before >= 0) cudaSetDevice(before);
+  }
+};
+
+inline int page_shift(int page_size) {
+  int s = 0;
+  while ((1 << s) < page_size) ++s;
+  return s;
+}
+
+// DFLASH_OK, or why a paged cache cannot be used by any call.
+inline int paged_cache_check(const dflash_paged_cache* c) {
+  if (!c || !c->k || !c->v || !c->page_table || !c->status || (c->dtype != DFLASH_F16 && c->dtype != DFLASH_BF16) ||
+      c->n_pages < 1 || c->max_pages < 1 || c->kv_heads < 1 || c->table_stride < c->max_pages || c->device < 0)
+    return DFLASH_ERR_INVALID_ARG;
+  if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1))) return DFLASH_ERR_SHAPE;
+  return DFLASH_OK;
+}

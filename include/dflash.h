@@ -420,6 +420,151 @@ DFLASH_API int dflash_harness_verify(dflash_handle* h, const int32_t* slots, int
                           const void* feat_stream, int32_t stream_rows, void* feats_out,
                           void* stream);
 
+/* ---- operators of the caller's own target model --------------------------
+ * The verify step belongs to the caller's target ("DFlash原理深度剖析…", §三 第2步:
+ * the target's own forward over the block), of any depth and in the caller's
+ * own engine.  These calls are the attention half of such a model's layers:
+ * rotary positions, the append of new keys and values to a paged cache, and
+ * the attention of the new tokens -- single tokens, verify blocks, prompt
+ * chunks, in one ragged batch -- over that cache.  They need no handle.
+ *
+ * A batch is ragged: row t of q/k/v belongs to the sequence b with
+ * cu_rows[b] <= t < cu_rows[b+1] (DEVICE int32 [batch+1], non-decreasing, from
+ * 0); its position is ctx_len[b] + t - cu_rows[b].  Rows from cu_rows[batch]
+ * on are padding: nothing is read or written for them.  Values are f16 or
+ * bf16, one type for all tensors of a call.  A tensor of rows is given by its
+ * pointer and the strides, in elements, of its rows and heads; the head
+ * dimension is contiguous.  `device` is the ordinal that every pointer and
+ * the stream belong to; the caller's current device is left as it was.
+ * Calls keep nothing between them and may overlap on different streams, each
+ * with a workspace of its own; they are legal inside stream capture. */
+#define DFLASH_F16 0
+#define DFLASH_BF16 1
+
+typedef struct dflash_rows {
+  void* data;          /* [rows, heads, head_dim] */
+  int64_t row_stride;  /* elements */
+  int64_t head_stride; /* elements */
+} dflash_rows;
+
+/* Long-context scalings of the rotary frequencies w_i = theta^(-2i/rotary_dim),
+ * i < rotary_dim/2 (angle of pair i at position p: p * w_i). */
+#define DFLASH_ROPE_PLAIN 0   /* w_i */
+#define DFLASH_ROPE_LINEAR 1  /* w_i / factor */
+#define DFLASH_ROPE_NTK 2     /* theta -> theta * factor^(rotary_dim / (rotary_dim - 2)) */
+#define DFLASH_ROPE_YARN 3    /* w_i / factor where a pair makes fewer than beta_slow turns over original_len
+                                 positions, w_i where more than beta_fast, a linear ramp over the pair index
+                                 between; cos and sin times 0.1 ln(factor) + 1 (attention_factor > 0: that) */
+#define DFLASH_ROPE_LLAMA3 4  /* by turns over original_len: w_i / factor below low_freq, w_i above high_freq,
+                                 their linear mix between */
+#define DFLASH_ROPE_FACTORS 5 /* w_i / factors[i]; cos and sin times attention_factor (0: 1) */
+
+typedef struct dflash_rope_config {
+  int32_t rotary_dim;    /* leading dimensions of a head that are rotated: even, 2..256 */
+  int32_t interleaved;   /* pair i is dims (2i, 2i+1) if 1, (i, i + rotary_dim/2) if 0 */
+  int32_t scaling;       /* DFLASH_ROPE_* */
+  int32_t original_len;  /* YARN, LLAMA3: the trained length */
+  double theta;          /* base, > 1 */
+  double factor;         /* > 0 */
+  double beta_fast, beta_slow;
+  double low_freq, high_freq;
+  double attention_factor;
+  const double* factors; /* HOST [rotary_dim/2], FACTORS only */
+} dflash_rope_config;
+
+#define DFLASH_ROPE_MAX_PAIRS 128
+/* Filled by dflash_rope_init, read only by the calls it is passed to (their
+ * kernels receive it by value). */
+typedef struct dflash_rope_plan {
+  int32_t rotary_dim, interleaved;
+  float amplitude;                      /* of cos and sin */
+  int32_t reserved;
+  uint64_t turn[DFLASH_ROPE_MAX_PAIRS]; /* turns per position, modulo 1, in units of 2^-64 */
+} dflash_rope_plan;
+
+/* Host only.  DFLASH_ERR_INVALID_ARG for a null, non-finite or out-of-range
+ * parameter; *plan is then untouched. */
+DFLASH_API int dflash_rope_init(const dflash_rope_config* cfg, dflash_rope_plan* plan);
+
+/* Rotate the heads of q and (data non-null) k at positions[t] (DEVICE int32
+ * [rows]): the first rotary_dim dims of a head by the plan, the others copied.
+ * Any alignment and strides; an output may be its own input (same pointer and
+ * strides) and must not overlap it otherwise.  backward = 1 applies the
+ * transposed map: the gradient of the inputs from the gradient of the outputs. */
+typedef struct dflash_rope_args {
+  dflash_rows q, k, q_out, k_out;
+  const int32_t* positions;
+  int32_t rows, q_heads, k_heads, head_dim; /* head_dim even, rotary_dim..256 */
+  int32_t dtype, backward, device;
+} dflash_rope_args;
+DFLASH_API int dflash_rope(const dflash_rope_plan* plan, const dflash_rope_args* args, void* stream);
+
+/* A paged cache: pools of n_pages pages of page_size positions for every KV
+ * head, in any order of those three dimensions (strides in elements), and a
+ * page table; entry [b][p / page_size] is the page of position p. */
+typedef struct dflash_paged_cache {
+  void* k;
+  void* v;
+  int64_t k_page_stride, k_pos_stride, k_head_stride;
+  int64_t v_page_stride, v_pos_stride, v_head_stride;
+  const int32_t* page_table; /* DEVICE [batch][table_stride] */
+  int64_t table_stride;
+  uint32_t* status;          /* DEVICE word that device-side checks or bits into (DFLASH_DEV_*) */
+  int32_t max_pages;         /* entries of a table row */
+  int32_t n_pages;
+  int32_t page_size;         /* 16, 32, 64, 128 or 256 */
+  int32_t kv_heads, head_dim;
+  int32_t dtype, device;
+} dflash_paged_cache;
+
+/* Append k and v of every row at its position: k rotated by the plan (null:
+ * copied).  q (data non-null) is rotated alike into q_out, under dflash_rope's
+ * rules.  A row whose position is negative or has no page (beyond the table,
+ * or an entry outside the pool) is not written and sets DFLASH_DEV_PAGE; its
+ * q is still rotated.  head_dim even, up to 256.  Rows of one call must have
+ * different places. */
+typedef struct dflash_append_args {
+  dflash_rows k, v, q, q_out;
+  const int32_t* cu_rows;
+  const int32_t* ctx_len; /* DEVICE [batch] */
+  int32_t rows, batch, q_heads;
+  int32_t reserved;
+} dflash_append_args;
+DFLASH_API int dflash_paged_append(const dflash_paged_cache* cache, const dflash_rope_plan* plan,
+                                   const dflash_append_args* args, void* stream);
+
+/* out_t = sum_j softmax_j(scale q_t . k_j) v_j over the cached positions j that
+ * row t sees: 0 <= j < kv_len[b] (null: ctx_len[b] + the sequence's rows), with
+ * causal also j <= position, with window w > 0 also j > position - w.  Query
+ * head h reads KV head h / (q_heads / kv_heads).  A row that sees no position
+ * gets out 0 and lse -inf.  lse (optional, float32 [rows][q_heads], strides of
+ * its own): the natural logarithm of the row's sum of exponentials.  Only
+ * pages that hold a seen position are read, and of the last of them nothing
+ * behind kv_len reaches the result; a non-finite value within kv_len reaches
+ * rows that mask it only through v.
+ * Supported: head_dim 64 or 128, q_heads a multiple of kv_heads, at most 32
+ * times; q, out and the pools 16-byte aligned with strides that are multiples
+ * of 8 elements.  A page that is not in the pool reads as zeros and sets
+ * DFLASH_DEV_PAGE; a position beyond the table is not seen and sets it too.
+ * workspace: DEVICE, 256-byte aligned, dflash_paged_attention_workspace
+ * bytes, for this call alone until it is done. */
+typedef struct dflash_attention_args {
+  dflash_rows q, out;
+  float* lse;
+  int64_t lse_row_stride, lse_head_stride;
+  const int32_t* cu_rows;
+  const int32_t* ctx_len;
+  const int32_t* kv_len;
+  void* workspace;
+  int64_t workspace_bytes;
+  int32_t rows, batch, q_heads;
+  int32_t causal, window;
+  float scale;
+} dflash_attention_args;
+DFLASH_API size_t dflash_paged_attention_workspace(const dflash_paged_cache* cache, int32_t rows, int32_t batch,
+                                                   int32_t q_heads);
+DFLASH_API int dflash_paged_attention(const dflash_paged_cache* cache, const dflash_attention_args* args, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,276 @@
+"""The caller-target operators on the CPU: the rotation plans against the
+scalings' formulas, the packed argument structs against the C ones, and the
+refusals -- a wrong tensor never reaches the library."""
+import ctypes
+import math
+import os
+
+import pytest
+import torch
+
+from block_diffusion_speculative_hiddens_gb300 import _build, binding, ops
+from tests import ops_ref
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(_build.LIB):
+        _build.build()
+    return binding.load()
+
+
+SCALINGS = [None, {"kind": "linear", "factor": 4.0}, {"kind": "ntk", "factor": 8.0},
+            {"kind": "yarn", "factor": 4.0, "original_len": 32768},
+            {"kind": "yarn", "factor": 16.0, "original_len": 4096, "beta_fast": 24.0, "beta_slow": 2.0,
+             "attention_factor": 1.25},
+            {"kind": "llama3", "factor": 8.0, "original_len": 8192, "low_freq_factor": 1.0, "high_freq_factor": 4.0},
+            "factors"]
+
+
+@pytest.mark.parametrize("rd,theta", [(128, 1e6), (64, 5e5), (32, 1e4), (6, 1e4)])
+@pytest.mark.parametrize("scaling", SCALINGS, ids=lambda s: str(s and s["kind"] if isinstance(s, dict) else s))
+def test_plan_holds_the_scaled_frequencies(lib, rd, theta, scaling):
+    if scaling == "factors":
+        scaling = {"kind": "factors", "factors": [1 + 0.5 * i for i in range(rd // 2)], "attention_factor": 1.1}
+    p = ops.RopePlan(rd, theta, interleaved=True, scaling=scaling)
+    freq, amp = ops_ref.frequencies(rd, theta, scaling)
+    assert p.amplitude == pytest.approx(amp, rel=2 ** -24)
+    for i, w in enumerate(freq):
+        turn = w / (2 * math.pi) % 1.0  # a handful of double roundings, and the last place of 2^-64
+        assert abs(p._c.turn[i] / 2.0 ** 64 - turn) <= 16 * 2.0 ** -53 * turn + 2.0 ** -63
+    assert all(p._c.turn[i] == 0 for i in range(rd // 2, ops.MAX_PAIRS))
+
+
+@pytest.mark.parametrize("kw", [
+    dict(rotary_dim=3), dict(rotary_dim=0), dict(rotary_dim=258), dict(rotary_dim=64, theta=1.0),
+    dict(rotary_dim=64, theta=math.inf), dict(rotary_dim=64, theta=math.nan),
+    dict(rotary_dim=2, scaling={"kind": "ntk", "factor": 2.0}),
+    dict(rotary_dim=64, scaling={"kind": "linear", "factor": 0.0}),
+    dict(rotary_dim=64, scaling={"kind": "linear", "factor": math.nan}),
+    dict(rotary_dim=64, scaling={"kind": "yarn", "factor": 2.0, "original_len": 0}),
+    dict(rotary_dim=64, scaling={"kind": "yarn", "factor": 2.0, "original_len": 9, "beta_fast": 1.0, "beta_slow": 2.0}),
+    dict(rotary_dim=64, scaling={"kind": "llama3", "factor": 2.0, "original_len": 9, "low_freq_factor": 4.0}),
+    dict(rotary_dim=4, scaling={"kind": "factors", "factors": [1.0, -1.0]}),
+])
+def test_plan_refuses_what_has_no_rotation(lib, kw):
+    kw = dict(theta=1e4) | kw
+    with pytest.raises(binding.DflashError) as e:
+        ops.RopePlan(kw.pop("rotary_dim"), kw.pop("theta"), **kw)
+    assert e.value.code == 1
+
+
+@pytest.mark.parametrize("scaling", [{"kind": "dynamic", "factor": 2.0}, {"factor": 2.0}, {"kind": "linear"},
+                                     {"kind": "linear", "factor": 2.0, "original_len": 5},
+                                     {"kind": "factors", "factors": [1.0] * 3}])
+def test_plan_refuses_scalings_it_does_not_know(lib, scaling):
+    with pytest.raises(ValueError):
+        ops.RopePlan(64, 1e4, scaling=scaling)
+
+
+def test_c_entries_refuse_before_any_cuda_call(lib):
+    plan = ops.RopePlan(128, 1e4)
+    one = ops._ROWS
+    rows = (16, 128, 128)
+
+    def rope(rows_n=1, hq=1, hk=1, dim=128, dtype=1, pos=16, plan_=plan, q=rows, out=rows):
+        a = ops._ROPE.pack(*q, *rows, *out, *rows, pos, rows_n, hq, hk, dim, dtype, 0, 0)
+        return lib.dflash_rope(None if plan_ is None else plan_._ref, a, None)
+    assert one == "Pqq"
+    assert rope(plan_=None) == 1 and rope(rows_n=-1) == 1 and rope(hq=-1) == 1 and rope(dtype=2) == 1
+    assert rope(pos=0) == 1 and rope(out=(0, 0, 0)) == 1
+    assert rope(dim=64) == 2 and rope(dim=129) == 2 and rope(dim=258) == 2
+    assert rope(rows_n=0) == 0 and rope(hq=0, hk=0) == 0
+
+    def cache(k=256, table=256, status=256, max_pages=4, stride=4, pages=8, page=64, heads=2, dim=128, dtype=1,
+              ks=(16384, 256, 128)):
+        return ops._CACHE.pack(k, 256, *ks, 16384, 256, 128, table, stride, status, max_pages, pages, page, heads, dim,
+                               dtype, 0)
+
+    def append(c=None, rows_n=1, batch=1, k=rows, cu=16, ctx=16, q=(0, 0, 0), hq=0, plan_=plan):
+        a = ops._APPEND.pack(*k, *rows, *q, 0, 0, 0, cu, ctx, rows_n, batch, hq, 0)
+        return lib.dflash_paged_append(cache() if c is None else c, None if plan_ is None else plan_._ref, a, None)
+    assert append(rows_n=-1) == 1 and append(batch=-1) == 1 and append(k=(0, 0, 0)) == 1 and append(cu=0) == 1
+    assert append(ctx=0) == 1 and append(q=rows, hq=2) == 1  # q without a place to go
+    assert append(rows_n=0) == 0 and append(batch=0) == 0
+    assert lib.dflash_paged_append(None, None, None, None) == 1
+
+    def attention(c=None, rows_n=1, batch=1, hq=4, q=rows, out=rows, cu=16, ctx=16, ws=256, wsb=1 << 40, window=0,
+                  scale=1.0):
+        a = ops._ATTENTION.pack(*q, *out, 0, 0, 0, cu, ctx, 0, ws, wsb, rows_n, batch, hq, 1, window, scale)
+        return lib.dflash_paged_attention(cache() if c is None else c, a, None)
+    assert attention(rows_n=-1) == 1 and attention(window=-1) == 1 and attention(scale=math.nan) == 1
+    assert attention(q=(0, 0, 0)) == 1 and attention(out=(0, 0, 0)) == 1 and attention(cu=0) == 1
+    assert attention(ctx=0) == 1
+    assert attention(hq=3) == 2 and attention(hq=0) == 2 and attention(hq=66) == 2
+    assert attention(q=(24, 128, 128)) == 1 and attention(q=(16, 100, 128)) == 1 and attention(out=(16, 128, 4)) == 1
+    assert attention(c=cache(ks=(16384, 260, 128))) == 1 and attention(c=cache(ks=(16380, 256, 128))) == 1
+    assert attention(ws=0) == 6 and attention(ws=128) == 6 and attention(wsb=0) == 6 and attention(wsb=-1) == 6
+    assert attention(rows_n=0) == 0 and attention(batch=0) == 0
+    for bad, code in ((dict(k=0), 1), (dict(table=0), 1), (dict(status=0), 1), (dict(max_pages=0), 1),
+                      (dict(stride=3), 1), (dict(pages=0), 1), (dict(heads=0), 1), (dict(dtype=5), 1),
+                      (dict(page=8), 2), (dict(page=48), 2), (dict(page=512), 2)):
+        assert append(c=cache(**bad)) == code, bad
+        assert attention(c=cache(**bad)) == code, bad
+    assert attention(c=cache(dim=96)) == 2
+    assert lib.dflash_paged_attention(None, None, None) == 1
+    assert lib.dflash_paged_attention_workspace(None, 1, 1, 1) == 0
+
+
+class FakeT:
+    """A tensor that says it is on a CUDA device."""
+
+    def __init__(self, shape, dtype=torch.bfloat16, device="cuda:0", stride=None, ptr=0x100000):
+        self.shape, self.dtype, self.device, self.ptr = tuple(shape), dtype, torch.device(device), ptr
+        self._s = tuple(stride) if stride else tuple(math.prod(self.shape[i + 1:]) for i in range(len(self.shape)))
+
+    def stride(self, i=None):
+        return self._s if i is None else self._s[i]
+
+    def get_device(self):
+        return -1 if self.device.type == "cpu" else self.device.index
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return math.prod(self.shape)
+
+    def is_contiguous(self):
+        return self._s == FakeT(self.shape)._s
+
+    def data_ptr(self):
+        return self.ptr
+
+
+class Stream:
+    cuda_stream = 0
+    device = torch.device("cuda:0")
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    got = []
+
+    class Lib:
+        def __getattr__(self, name):
+            def fn(*a):
+                got.append(name)
+                return 0
+            return fn
+    monkeypatch.setattr(ops, "load", lambda: Lib())
+    return got
+
+
+def _cache():
+    c = ops.PagedCache.__new__(ops.PagedCache)
+    c.device, c.dtype, c.head_dim, c.kv_heads, c.batch, c._c = 0, torch.bfloat16, 128, 2, 3, b""
+    return c
+
+
+I32 = torch.int32
+
+
+def _attention(**kw):
+    a = dict(q=FakeT([7, 4, 128]), cu=FakeT([4], I32), ctx=FakeT([3], I32), out=FakeT([7, 4, 128], ptr=1 << 30),
+             workspace=FakeT([256], torch.uint8), stream=Stream(), lse=None, kv_len=None)
+    a.update(kw)
+    return ops.attention(_cache(), a.pop("q"), a.pop("cu"), a.pop("ctx"), **a)
+
+
+def _append(**kw):
+    a = dict(k=FakeT([7, 2, 128]), v=FakeT([7, 2, 128]), cu=FakeT([4], I32), ctx=FakeT([3], I32),
+             q=FakeT([7, 4, 128]), q_out=FakeT([7, 4, 128], ptr=1 << 30), stream=Stream())
+    a.update(kw)
+    return ops.append(_cache(), a.pop("k"), a.pop("v"), a.pop("cu"), a.pop("ctx"), **a)
+
+
+def _rope(**kw):
+    class P:
+        _ref = None
+    a = dict(q=FakeT([7, 4, 128]), k=FakeT([7, 2, 128]), positions=FakeT([7], I32),
+             q_out=FakeT([7, 4, 128], ptr=1 << 30), k_out=FakeT([7, 2, 128], ptr=1 << 31), stream=Stream())
+    a.update(kw)
+    return ops.rope(P(), a.pop("q"), a.pop("k"), a.pop("positions"), **a)
+
+
+def test_well_formed_calls_reach_the_library(calls):
+    _rope()
+    _rope(k=None, k_out=None)
+    _rope(q_out=FakeT([7, 4, 128]))  # in place
+    _append()
+    _append(q=None, q_out=None)
+    _attention()
+    _attention(lse=FakeT([7, 4], torch.float32), kv_len=FakeT([3], I32))
+    assert [c for c in calls if "workspace" not in c] == ["dflash_rope"] * 3 + ["dflash_paged_append"] * 2 + [
+        "dflash_paged_attention"] * 2
+
+
+def test_q_and_k_views_of_one_projection_rotate_in_place_and_apart(calls):
+    qkv = dict(stride=(8 * 128, 128, 1))
+    q, k = FakeT([7, 4, 128], **qkv), FakeT([7, 2, 128], ptr=0x100000 + 4 * 256, **qkv)
+    _rope(q=q, k=k, q_out=q, k_out=k)
+    _rope(q=q, k=k, q_out=FakeT([7, 4, 128], ptr=0x100000 + 4 * 256, **qkv), k_out=k)  # other heads of the same rows
+    with pytest.raises(ValueError, match="overlaps"):
+        _rope(q=q, k=k, q_out=FakeT([7, 4, 128], ptr=0x100000 + 2 * 256, **qkv), k_out=k)
+
+
+BAD = [FakeT([7, 4, 128], torch.float16), FakeT([7, 4, 128], device="cuda:1"), FakeT([7, 4, 128], device="cpu"),
+       FakeT([7, 128]), FakeT([7, 4, 64]), FakeT([7, 4, 128], stride=(1024, 256, 2))]
+
+
+@pytest.mark.parametrize("bad", BAD, ids=range(len(BAD)))
+def test_wrong_row_tensors_are_refused(calls, bad):
+    for call in (lambda: _attention(q=bad), lambda: _attention(out=bad), lambda: _append(q=bad), lambda: _append(q_out=bad),
+                 lambda: _append(k=bad), lambda: _append(v=bad), lambda: _rope(q_out=bad), lambda: _rope(k=bad)):
+        with pytest.raises(ValueError):
+            call()
+    assert [c for c in calls if "workspace" not in c] == []
+
+
+@pytest.mark.parametrize("kw", [
+    dict(cu=FakeT([3], I32)), dict(cu=FakeT([4], torch.int64)), dict(ctx=FakeT([4], I32), cu=FakeT([5], I32)),
+    dict(ctx=FakeT([3], I32, device="cuda:1")), dict(cu=FakeT([4], I32, stride=(2,)))])
+def test_wrong_batches_are_refused(calls, kw):
+    for call in (_attention, _append):
+        with pytest.raises(ValueError):
+            call(**kw)
+    assert [c for c in calls if "workspace" not in c] == []
+
+
+def test_other_refusals(calls):
+    for kw in (dict(lse=FakeT([7, 4], torch.float16)), dict(lse=FakeT([4, 7], torch.float32)),
+               dict(kv_len=FakeT([2], I32)), dict(workspace=FakeT([256], torch.float32)),
+               dict(workspace=FakeT([256], torch.uint8, device="cuda:1")), dict(out=FakeT([6, 4, 128]))):
+        with pytest.raises(ValueError):
+            _attention(**kw)
+    for kw in (dict(positions=FakeT([6], I32)), dict(positions=FakeT([7], torch.int64)), dict(q_out=FakeT([7, 5, 128])),
+               dict(q_out=FakeT([7, 4, 128], ptr=0x100000 + 256)), dict(k=FakeT([6, 2, 128]))):
+        with pytest.raises(ValueError):
+            _rope(**kw)
+    other = Stream()
+    other.device = torch.device("cuda:1")
+    for call in (_rope, _append, _attention):
+        with pytest.raises(ValueError, match="stream"):
+            call(stream=other)
+    assert [c for c in calls if "workspace" not in c] == []
+    cpu = torch.zeros(4, 64, 2, 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        ops.PagedCache(cpu, cpu, torch.zeros(1, 4, dtype=torch.int32))
+
+
+def test_packed_structs_match_the_header(tmp_path):
+    """The sizes a C compiler gives the header's structs."""
+    import shutil
+    import subprocess
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        pytest.skip("no C compiler")
+    names = ["dflash_rope_args", "dflash_paged_cache", "dflash_append_args", "dflash_attention_args",
+             "dflash_rope_config", "dflash_rope_plan"]
+    src = tmp_path / "s.c"
+    src.write_text('#include "%s"\n#include <stdio.h>\nint main(void) { printf("%s", %s); return 0; }\n' % (
+        binding.HEADER, " ".join(["%zu"] * 6), ", ".join("sizeof(%s)" % n for n in names)))
+    subprocess.run([cc, str(src), "-o", str(tmp_path / "s")], check=True)
+    got = [int(x) for x in subprocess.run([str(tmp_path / "s")], capture_output=True, text=True, check=True).stdout.split()]
+    assert got == [ops._ROPE.size, ops._CACHE.size, ops._APPEND.size, ops._ATTENTION.size,
+                   ctypes.sizeof(ops.RopeConfig), ctypes.sizeof(ops._Plan)]
