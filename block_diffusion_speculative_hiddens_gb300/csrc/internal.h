@@ -251,3 +251,9 @@ inline int paged_cache_check(const dflash_paged_cache* c) {
   if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1))) return DFLASH_ERR_SHAPE;
   return DFLASH_OK;
 }
+
+// A tiled TMA map over 16-bit values, 128-byte swizzle: `rank` sizes and boxes
+// (innermost first, box[0] = 64), rank - 1 strides in bytes.  False: the
+// driver refuses it.
+bool tmap_tiled(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                const uint32_t* box, bool is_bf16);
