@@ -28,9 +28,20 @@
 #include "common.cuh"
 #include "internal.h"
 
+#ifndef DFL_SETUP2
+#define DFL_SETUP2 2
+#endif
+#ifndef DFL_SETUP1
+#define DFL_SETUP1 1
+#endif
+
 namespace {
 
 constexpr int KT = 128;  // keys of a tile
+// What an item costs beside its tiles, in tiles: the load of Q, the first and
+// last tile that overlap nothing, the output.
+template <int NM>
+constexpr int SETUP = NM == 2 ? DFL_SETUP2 : DFL_SETUP1;
 
 struct PagedParams {
   uint16_t* out;
@@ -54,28 +65,29 @@ struct PagedParams {
 
 // Workspace: a header, one record a CTA, two partial slots a CTA.
 struct WsHead {
-  long long units;
-  int ctas;
+  long long cost;  // of all items
+  int ctas;        // that share it
 };
 struct WsCta {
-  int off, units;  // of the item its run begins in: tiles before it, tiles of the item
+  int at, cost;  // of the item its run begins in: cost before it, cost of the item
   int b, mt, kvh, pad[3];
 };
 constexpr size_t ws_records(int grid) { return 256 + ((size_t)grid * sizeof(WsCta) + 255) / 256 * 256; }
 // One slot: O [D/4][rows] float4, running maxima [rows], sums [rows].
-constexpr size_t ws_slot_floats(int rows, int D) { return (size_t)rows * (D + 2); }
+constexpr size_t ws_slot_floats(int rows, int D) { return (size_t)rows * (D + 2); }  // a multiple of 4
 
 template <int D, int NM>
 struct PCfg {
   static constexpr int ROWS = 128 * NM;
   static constexpr int PANEL = 128 * 128;            // 128 rows x 64 dims
   static constexpr int TILE = (D / 64) * PANEL;      // Q of an M tile, K or V of a key tile
-  static constexpr int SLOTS = (D == 128 ? 7 : 12) - NM;
-  static constexpr int OFF_RING = NM * TILE;
+  // Q of the next item lands beside this one's where there is room for both
+  static constexpr int QBUFS = D == 128 && NM == 2 ? 1 : 2;
+  static constexpr int SLOTS = D == 128 ? 5 : 10;
+  static constexpr int OFF_RING = QBUFS * NM * TILE;
   static constexpr int OFF_BAR = OFF_RING + SLOTS * TILE;
   static constexpr int SMEM = 1024 + OFF_BAR + 512;  // + 1024 for aligning the base
-  // NM = 2: a third warpgroup issues and loads, and hands registers to the softmax ones
-  static constexpr int THREADS = NM == 2 ? 384 : 192;
+  static constexpr int THREADS = 128 * NM + 64;
   static constexpr int S_COL = 0;                    // two S buffers of 128 columns
   static constexpr int O_COL = 256;
   static constexpr uint32_t TMEM_COLS = 512;
@@ -96,6 +108,32 @@ DFL_DEV float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+
+DFL_DEV float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+// Two float32 in one register pair.
+DFL_DEV uint64_t pack_u32x2(uint32_t lo, uint32_t hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
+  return v;
+}
+DFL_DEV uint64_t pack_f32x2(float lo, float hi) { return pack_u32x2(__float_as_uint(lo), __float_as_uint(hi)); }
+DFL_DEV void unpack_f32x2(uint64_t v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+DFL_DEV uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+DFL_DEV uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// The n lowest bits (n outside 0..32: none, all).
+DFL_DEV uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
 
 DFL_DEV void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
   asm volatile(
@@ -125,15 +163,11 @@ DFL_DEV void tmem_ld32_nowait(uint32_t taddr, uint32_t* r) {
       : "r"(taddr)
       : "memory");
 }
-DFL_DEV void tmem_st32_nowait(uint32_t taddr, const uint32_t* r) {
+DFL_DEV void tmem_st16_nowait(uint32_t taddr, const uint32_t* r) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,"
-      "%31,%32};" ::"r"(taddr),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 DFL_DEV void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -176,29 +210,31 @@ DFL_DEV Span load_span(const PagedParams& p, const Seq& s, int t0, int t1) {
   return r;
 }
 
-// A CTA's run through the items.
+// A CTA's run through the items.  An item's cost is SETUP, then one a tile.
 struct Walk {
-  int b, mt, kvh, off;  // the item and the first of its tiles that is this CTA's
-  long long left;       // units still to do
+  int b, mt, kvh, at;  // the item and the part of its cost that lies before this CTA's run
+  long long left;      // cost still to come
   Seq s;
   Span span;
-  int t0, t1;           // the item's tokens
-  int n;                // units of this segment
-  int units;            // units of the item (1 if it has no tile: its rows get zeros)
+  int t0, t1;          // the item's tokens
+  int off, n;          // this CTA's tiles of the item
+  bool out;            // it has something to write: tiles, or the zeros of an item without any
 };
 template <int NM>
 DFL_DEV void walk_item(const PagedParams& p, Walk& w) {
   w.t0 = w.mt * p.tok * NM;
   w.t1 = min(w.t0 + p.tok * NM, w.s.n);
   w.span = load_span(p, w.s, w.t0, w.t1);
-  w.units = max(w.span.tiles, 1);
-  w.n = (int)min((long long)(w.units - w.off), w.left);
+  const int end = (int)min((long long)(SETUP<NM> + w.span.tiles), w.at + w.left);
+  w.off = max(w.at - SETUP<NM>, 0);
+  w.n = max(end - SETUP<NM>, 0) - w.off;
+  w.out = w.n > 0 || (w.span.tiles == 0 && w.at == 0);
 }
 template <int NM>
 DFL_DEV bool walk_next(const PagedParams& p, Walk& w) {
-  w.left -= w.n;
+  w.left -= SETUP<NM> + w.span.tiles - w.at;
   if (w.left <= 0) return false;
-  w.off = 0;
+  w.at = 0;
   if (++w.kvh == p.hkv) {
     w.kvh = 0;
     ++w.mt;
@@ -237,27 +273,33 @@ DFL_DEV long long cta_scan(long long v, long long* part, long long* total) {
 
 struct Sched {
   long long part[16];
-  int b, mt, units, pairs;
-  long long before;  // units before the pair (b, mt)
+  int b, mt, cost;
+  long long before;  // cost before the pair (b, mt)
 };
 
 // Where this CTA's run begins.  Pairs (sequence, token tile) are counted and
-// weighed by the whole CTA, blockDim.x at a time; `first` [batch + 1] receives
-// the sequences' first pairs.  False: no work at all, or none for this CTA.
+// weighed by the whole CTA, blockDim.x at a time; the tile area, free until
+// the loads begin, holds the sequences (`seqs`, as long as each thread has one
+// at most) and their first pairs (`first` [batch + 1]).  False: no work at
+// all, or none for this CTA.
 template <int NM>
-DFL_DEV bool locate(const PagedParams& p, Sched* sc, int* first, Walk& w, long long* units_out, int* ctas_out) {
+DFL_DEV bool locate(const PagedParams& p, Sched* sc, Seq* seqs, int* first, Walk& w, long long* cost_out, int* ctas_out) {
   const int per = p.tok * NM;
+  const bool kept = p.batch <= (int)blockDim.x;
   long long pairs = 0;
   for (int b0 = 0; b0 < p.batch; b0 += blockDim.x) {
     const int b = b0 + threadIdx.x;
     int m = 0;
-    if (b < p.batch) m = (load_seq(p, b).n + per - 1) / per;
+    if (b < p.batch) {
+      const Seq s = load_seq(p, b);
+      if (kept) seqs[b] = s;
+      m = (s.n + per - 1) / per;
+    }
     long long all;
     const long long at = cta_scan(m, sc->part, &all);
     if (b < p.batch) first[b] = (int)(pairs + at - m);
     pairs += all;
   }
-  if (threadIdx.x == 0) first[p.batch] = (int)pairs;
   __syncthreads();
   auto weigh = [&](int pair, int* b_out, int* mt_out) {
     int lo = 0, hi = p.batch - 1;  // the last sequence whose first pair is not behind
@@ -266,11 +308,11 @@ DFL_DEV bool locate(const PagedParams& p, Sched* sc, int* first, Walk& w, long l
       if (first[mid] <= pair) lo = mid;
       else hi = mid - 1;
     }
-    const Seq s = load_seq(p, lo);
+    const Seq s = kept ? seqs[lo] : load_seq(p, lo);
     const int mt = pair - first[lo], t0 = mt * per;
     *b_out = lo;
     *mt_out = mt;
-    return max(load_span(p, s, t0, min(t0 + per, s.n)).tiles, 1);
+    return SETUP<NM> + load_span(p, s, t0, min(t0 + per, s.n)).tiles;
   };
   long long total = 0, all;
   int b = 0, mt = 0, u = 0;
@@ -284,7 +326,7 @@ DFL_DEV bool locate(const PagedParams& p, Sched* sc, int* first, Walk& w, long l
   }
   if (total == 0) return false;
   const int ctas = (int)min((long long)gridDim.x, total);
-  *units_out = total;
+  *cost_out = total;
   *ctas_out = ctas;
   if ((int)blockIdx.x >= ctas) return false;
   const long long u0 = total * blockIdx.x / ctas, u1 = total * (blockIdx.x + 1) / ctas;
@@ -299,7 +341,7 @@ DFL_DEV bool locate(const PagedParams& p, Sched* sc, int* first, Walk& w, long l
     if (u > 0 && incl > u0 && incl - (long long)u * p.hkv <= u0) {
       sc->b = b;
       sc->mt = mt;
-      sc->units = u;
+      sc->cost = u;
       sc->before = incl - (long long)u * p.hkv;
     }
     if (!once && base > u0) break;  // uniform: base is the CTA's
@@ -308,10 +350,10 @@ DFL_DEV bool locate(const PagedParams& p, Sched* sc, int* first, Walk& w, long l
   const long long in = u0 - sc->before;
   w.b = sc->b;
   w.mt = sc->mt;
-  w.kvh = (int)(in / sc->units);
-  w.off = (int)(in % sc->units);
+  w.kvh = (int)(in / sc->cost);
+  w.at = (int)(in % sc->cost);
   w.left = u1 - u0;
-  w.s = load_seq(p, w.b);
+  w.s = kept ? seqs[w.b] : load_seq(p, w.b);
   walk_item<NM>(p, w);
   return true;
 }
@@ -328,14 +370,15 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
   uint64_t* empty = full + C::SLOTS;    // [SLOTS] tile's MMAs done
   uint64_t* s_full = empty + C::SLOTS;  // [2] S (and every MMA before it) done
   uint64_t* p_full = s_full + 2;        // [2] P written
-  uint64_t* o_done = p_full + 2;        // [2] an O MMA done
+  uint64_t* p_half = p_full + 2;        // [2] the first 64 keys of P written
+  uint64_t* o_done = p_half + 2;        // [2] an O MMA done
   uint64_t* o_empty = o_done + 2;       // [2] O read out
-  uint64_t* q_full = o_empty + 2;
-  uint64_t* q_empty = q_full + 1;
-  uint64_t* mdone = q_empty + 1;
+  uint64_t* q_full = o_empty + 2;       // [QBUFS]
+  uint64_t* q_empty = q_full + 2;
+  uint64_t* mdone = q_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mdone + 1);
   Sched* sched = reinterpret_cast<Sched*>(sm + C::OFF_BAR + 320);
-  static_assert((2 * C::SLOTS + 11) * 8 + 8 <= 320 && sizeof(Sched) <= 192, "barrier area");
+  static_assert((2 * C::SLOTS + 15) * 8 + 8 <= 320 && sizeof(Sched) <= 192, "barrier area");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int MMA_WARP = 4 * NM, LOAD_WARP = 4 * NM + 1;
@@ -347,11 +390,14 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full + i, 1);
       mbar_init(p_full + i, 4);
+      mbar_init(p_half + i, 4);
       mbar_init(o_done + i, 1);
       mbar_init(o_empty + i, 4);
     }
-    mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
+    for (int i = 0; i < C::QBUFS; ++i) {
+      mbar_init(q_full + i, 1);
+      mbar_init(q_empty + i, 1);
+    }
     mbar_init(mdone, 1);
     fence_mbar_init();
   }
@@ -372,22 +418,22 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
   pdl_wait();
 
   Walk w;
-  long long units = 0;
+  long long cost = 0;
   int ctas = 0;
-  // the tile area is free until the loads begin: it holds the sequences' first pairs
-  const bool work = locate<NM>(p, sched, reinterpret_cast<int*>(sm), w, &units, &ctas);
+  Seq* seqs = reinterpret_cast<Seq*>(sm);
+  const bool work = locate<NM>(p, sched, seqs, reinterpret_cast<int*>(seqs + C::THREADS), w, &cost, &ctas);
   if (threadIdx.x == 0) {
-    if (blockIdx.x == 0) *reinterpret_cast<WsHead*>(p.ws) = WsHead{units, ctas};
+    if (blockIdx.x == 0) *reinterpret_cast<WsHead*>(p.ws) = WsHead{cost, ctas};
     if (work) {
       WsCta* rec = reinterpret_cast<WsCta*>(p.ws + 256) + blockIdx.x;
-      rec->off = w.off;
-      rec->units = w.units;
+      rec->at = w.at;
+      rec->cost = SETUP<NM> + w.span.tiles;
       rec->b = w.b;
       rec->mt = w.mt;
       rec->kvh = w.kvh;
     }
   }
-  fence_proxy_async_smem();  // the first pairs were written and read before the loads land over them
+  fence_proxy_async_smem();  // the sequences were written and read before the loads land over them
   __syncthreads();
   bool aborted = false;
   auto wait_all = [&](uint64_t* bar, uint32_t par) {  // warp-uniform
@@ -396,30 +442,27 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
     return ok;
   };
 
-  // registers of the NM = 2 roles: 168 a thread at launch, 384 threads; 2 x 200 + 104 is as much
   if (!work) {
     // nothing for this CTA
-  } else if (warp > LOAD_WARP) {
-    if (NM == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
   } else if (warp == LOAD_WARP) {
-    if (NM == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     // ------------------------------------------------ loads
     const int page = 1 << p.shift, box = min(page, KT), boxes = KT / box;
     int seg = 0;
     long long nt = 0;  // ring slots filled
     bool ok = true;
     do {
-      const int tiles = w.span.tiles ? w.n : 0;
+      const int tiles = w.n;
       if (tiles == 0) continue;
       if (lane == 0 && (p.kv_len ? (long long)p.kv_len[w.b] : w.s.ctx + w.s.n) > p.cap)
         dev_error(p.status, DFLASH_DEV_PAGE);
-      if (seg > 0 && !wait_all(q_empty, (uint32_t)((seg - 1) & 1))) break;
+      const int qb = seg % C::QBUFS;
+      if (seg >= C::QBUFS && !wait_all(q_empty + qb, (uint32_t)((seg / C::QBUFS - 1) & 1))) break;
       const int nm = NM == 2 && w.t0 + p.tok < w.t1 ? 2 : 1;
       if (lane == 0) {
-        mbar_arrive_expect_tx(q_full, (uint32_t)(nm * (D / 64) * p.tok * p.group * 128));
+        mbar_arrive_expect_tx(q_full + qb, (uint32_t)(nm * (D / 64) * p.tok * p.group * 128));
         for (int m = 0; m < nm; ++m)
           for (int h = 0; h < D / 64; ++h)
-            tma_load_3d(sm + m * C::TILE + h * C::PANEL, &qmap, q_full, 64 * h, w.kvh * p.group,
+            tma_load_3d(sm + (qb * NM + m) * C::TILE + h * C::PANEL, &qmap, q_full + qb, 64 * h, w.kvh * p.group,
                         w.s.row0 + w.t0 + m * p.tok);
       }
       ++seg;
@@ -462,21 +505,21 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
       bool drain = false;
       mbar_wait(full + i % C::SLOTS, (uint32_t)((i / C::SLOTS) & 1), p.status, &drain);
     }
-    if (seg > 0) {
+    for (int i = seg > C::QBUFS ? seg - C::QBUFS : 0; i < seg; ++i) {
       bool drain = false;
-      mbar_wait(q_full, (uint32_t)((seg - 1) & 1), p.status, &drain);
+      mbar_wait(q_full + i % C::QBUFS, (uint32_t)((i / C::QBUFS) & 1), p.status, &drain);
     }
   } else if (warp == MMA_WARP) {
     // ------------------------------------------------ MMA issue (converged warp, one elected lane)
-    if (NM == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     const uint32_t idesc_s = idesc_f16_f32(128, KT, BF16 ? 1 : 0);
     const uint32_t idesc_o = idesc_f16_f32(128, D, BF16 ? 1 : 0) | (1u << 16);  // V is N-major
     int seg = 0;
     long long nt = 0;          // ring slots used
     int it[2] = {0, 0};        // S tiles issued for each M tile
     int sg[2] = {0, 0};        // segments of each M tile
+    int qb = 0;
     auto issue_s = [&](int m, long long slot) {
-      const uint32_t qa = smem_u32(sm + m * C::TILE), ka = smem_u32(sm + C::OFF_RING + (int)(slot % C::SLOTS) * C::TILE);
+      const uint32_t qa = smem_u32(sm + (qb * NM + m) * C::TILE), ka = smem_u32(sm + C::OFF_RING + (int)(slot % C::SLOTS) * C::TILE);
       const int buf = NM == 2 ? m : it[0] & 1;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
@@ -489,17 +532,18 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
     };
     bool ok = true;
     do {
-      const int tiles = w.span.tiles ? w.n : 0;
+      const int tiles = w.n;
       if (tiles == 0) continue;
       const int nm = NM == 2 && w.t0 + p.tok < w.t1 ? 2 : 1;
       auto wait_full = [&](long long slot) { return wait_all(full + slot % C::SLOTS, (uint32_t)((slot / C::SLOTS) & 1)); };
       // S of tile j for every M tile (NM = 2: after its O MMA of tile j - 1)
-      if (!wait_all(q_full, (uint32_t)(seg & 1)) || !wait_full(nt)) break;
+      qb = seg % C::QBUFS;
+      if (!wait_all(q_full + qb, (uint32_t)((seg / C::QBUFS) & 1)) || !wait_full(nt)) break;
       ++seg;
       tc_fence_after();
       for (int m = 0; m < nm; ++m) issue_s(m, nt);
       tc_commit_elect(empty + nt % C::SLOTS);
-      if (tiles == 1) tc_commit_elect(q_empty);
+      if (tiles == 1) tc_commit_elect(q_empty + qb);
       for (int j = 0; j < tiles && ok; ++j, nt += 2) {
         const long long vs = nt + 1, ks = nt + 2;
         if (NM == 1 && j + 1 < tiles) {  // two S buffers: the next S runs beside this tile's softmax
@@ -507,7 +551,7 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
           tc_fence_after();
           issue_s(0, ks);
           tc_commit_elect(empty + ks % C::SLOTS);
-          if (j + 2 == tiles) tc_commit_elect(q_empty);
+          if (j + 2 == tiles) tc_commit_elect(q_empty + qb);
         }
         for (int m = 0; m < nm; ++m) {
           const int done = NM == 2 ? it[m] - 1 : it[0] - 1 - (j + 1 < tiles);  // the S tile whose P is next
@@ -530,13 +574,18 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
             tc_fence_after();
           }
           if (j == 0 && sg[m]++ > 0 && !(ok = wait_all(o_empty + m, (uint32_t)((sg[m] - 2) & 1)))) break;
-          if (!(ok = wait_all(p_full + buf, (uint32_t)((NM == 2 ? done : done >> 1) & 1)))) break;
-          tc_fence_after();
+          const uint32_t par = (uint32_t)((NM == 2 ? done : done >> 1) & 1);
           const uint32_t va = smem_u32(sm + C::OFF_RING + (int)(vs % C::SLOTS) * C::TILE);
 #pragma unroll
-          for (int kk = 0; kk < KT / 16; ++kk)
-            tc_mma_f16_ts_elect(tmem + (uint32_t)(C::O_COL + D * m), tmem + (uint32_t)(C::S_COL + 128 * buf + 8 * kk),
-                                sdesc_sw128_mn(va + 2048u * kk, C::PANEL), idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
+          for (int half = 0; half < 2; ++half) {
+            if (!(ok = wait_all((half ? p_full : p_half) + buf, par))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+              tc_mma_f16_ts_elect(tmem + (uint32_t)(C::O_COL + D * m), tmem + (uint32_t)(C::S_COL + 128 * buf + 8 * kk),
+                                  sdesc_sw128_mn(va + 2048u * kk, C::PANEL), idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
+          }
+          if (!ok) break;
           tc_commit_elect(o_done + m);
           if (m == nm - 1) tc_commit_elect(empty + vs % C::SLOTS);
           if (NM == 2 && j + 1 < tiles) {
@@ -547,7 +596,7 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
             issue_s(m, ks);
             if (m == nm - 1) {
               tc_commit_elect(empty + ks % C::SLOTS);
-              if (j + 2 == tiles) tc_commit_elect(q_empty);
+              if (j + 2 == tiles) tc_commit_elect(q_empty + qb);
             }
           }
         }
@@ -559,7 +608,6 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
     mbar_wait(mdone, 0, p.status, &drain);
   } else {
     // ------------------------------------------------ softmax: one row a thread
-    if (NM == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     const int m = warp >> 2;
     const int r = threadIdx.x & 127;
     const int rt = r / p.group, rh = r - rt * p.group;  // the row's token in the M tile and head in the group
@@ -568,7 +616,8 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
     int it = 0;  // S tiles of this M tile
     bool ok = true;
     do {
-      const int tiles = w.span.tiles ? w.n : 0;
+      const int tiles = w.n;
+      if (!w.out) continue;
       const int t = w.t0 + m * p.tok + rt;
       const bool valid = rt < p.tok && t < w.t1;
       if (NM == 2 && m == 1 && w.t0 + p.tok >= w.t1) continue;  // no row in this M tile
@@ -587,31 +636,52 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
         tc_fence_after();
         const uint32_t s_base = lane_base + (uint32_t)(C::S_COL + 128 * buf);
         if (warp_valid) {
-          uint32_t u[128];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32_nowait(s_base + 32 * c, u + 32 * c);
-          tmem_wait_ld();
-          float* s = reinterpret_cast<float*>(u);
           const int key0 = (w.span.tile0 + w.off + j) * KT;
-          if (p.negate) {
-#pragma unroll
-            for (int k = 0; k < 128; ++k) s[k] = -s[k];
-          }
           const int h = hi - key0, l = lo - key0;
-          if (__any_sync(0xffffffffu, h < KT || l > 0)) {
+          if (p.negate || __any_sync(0xffffffffu, h < KT || l > 0)) {
+            // S as the two passes below want it: its sign turned, -inf where the row does not see
+#pragma unroll 1
+            for (int c = 0; c < KT / 16; ++c) {
+              uint32_t x[16];
+              tmem_ld16_nowait(s_base + 16 * c, x);
+              tmem_wait_ld();
+              const uint32_t seen = low_bits(h - 16 * c) & ~low_bits(l - 16 * c);
 #pragma unroll
-            for (int k = 0; k < 128; ++k)
-              if (k >= h || k < l) s[k] = -INFINITY;
+              for (int k = 0; k < 16; ++k) {
+                if (p.negate) x[k] ^= 0x80000000u;
+                if (!(seen & (1u << k))) x[k] = 0xff800000u;
+              }
+              tmem_st16_nowait(s_base + 16 * c, x);
+            }
+            tmem_wait_st();
           }
-          float mx0 = s[0], mx1 = s[1], mx2 = s[2], mx3 = s[3];
+          // Both passes read S from TMEM, 32 columns ahead of the arithmetic;
+          // short loops, since the whole row unrolled waits on instruction fetch.
+          uint32_t x[32], y[32];
+          float mx = -INFINITY;
+          {
+            float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+            auto take = [&](const uint32_t* v) {
 #pragma unroll
-          for (int k = 4; k < 128; k += 4) {
-            mx0 = fmaxf(mx0, s[k]);
-            mx1 = fmaxf(mx1, s[k + 1]);
-            mx2 = fmaxf(mx2, s[k + 2]);
-            mx3 = fmaxf(mx3, s[k + 3]);
+              for (int k = 0; k < 32; k += 8) {
+                m0 = max3(m0, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+                m1 = max3(m1, __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
+                m2 = max3(m2, __uint_as_float(v[k + 4]), __uint_as_float(v[k + 5]));
+                m3 = max3(m3, __uint_as_float(v[k + 6]), __uint_as_float(v[k + 7]));
+              }
+            };
+            tmem_ld32_nowait(s_base, x);
+#pragma unroll 1
+            for (int c = 0; c < KT; c += 64) {
+              tmem_wait_ld();
+              tmem_ld32_nowait(s_base + c + 32, y);
+              take(x);
+              tmem_wait_ld();
+              tmem_ld32_nowait(s_base + (c + 64) % KT, x);  // at the end: the next pass's first
+              take(y);
+            }
+            mx = max3(fmaxf(m0, m1), m2, m3) * p.scale_log2;
           }
-          const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * p.scale_log2;
           const bool move = mx > m_run + 8.f;
           if (__any_sync(0xffffffffu, move)) {
             const float m_new = move ? mx : m_run;
@@ -619,42 +689,63 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
               if (NM == 1 && !(ok = wait_all(o_done + m, (uint32_t)((it - 1) & 1)))) break;
               tc_fence_after();
               const float alpha = move ? ex2(m_run - m_new) : 1.f;
+              tmem_wait_ld();
+#pragma unroll 1
+              for (int c = 0; c < D; c += 16) {
+                float o[16];
+                tmem_ld16(o_base + c, o);
 #pragma unroll
-              for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
-                tmem_ld32_nowait(o_base + 32 * c, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                tmem_st32_nowait(o_base + 32 * c, o);
+                for (int e = 0; e < 16; ++e) o[e] *= alpha;
+                tmem_st16(o_base + c, o);
               }
-              tmem_wait_st();
               l_run *= alpha;
             }
             m_run = m_new;
           }
-          const float ref = m_run == -INFINITY ? 0.f : m_run;  // a row that has seen no key yet adds 0
-          float sum0 = 0.f, sum1 = 0.f, sum2 = 0.f, sum3 = 0.f;
+          const float ref = m_run == -INFINITY ? 0.f : -m_run;  // a row that has seen no key yet adds 0
+          const uint64_t scale2 = pack_f32x2(p.scale_log2, p.scale_log2), ref2 = pack_f32x2(ref, ref);
+          uint64_t sum0 = 0, sum1 = 0;  // pairs of partial sums
+          auto weigh = [&](const uint32_t* v, int c) {  // 32 columns of S into 16 of P
+            uint32_t pk[16];
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t pk[32];
-#pragma unroll
-            for (int k = 0; k < 32; k += 2) {
-              const float a = ex2(fmaf(s[64 * c + 2 * k], p.scale_log2, -ref));
-              const float b = ex2(fmaf(s[64 * c + 2 * k + 1], p.scale_log2, -ref));
-              const float d = ex2(fmaf(s[64 * c + 2 * k + 2], p.scale_log2, -ref));
-              const float e = ex2(fmaf(s[64 * c + 2 * k + 3], p.scale_log2, -ref));
-              sum0 += a;
-              sum1 += b;
-              sum2 += d;
-              sum3 += e;
-              pk[k] = pack16<BF16>(a, b);
-              pk[k + 1] = pack16<BF16>(d, e);
+            for (int k = 0; k < 32; k += 4) {
+              const uint64_t f = fma_f32x2(pack_u32x2(v[k], v[k + 1]), scale2, ref2);
+              const uint64_t g = fma_f32x2(pack_u32x2(v[k + 2], v[k + 3]), scale2, ref2);
+              float a, b, d, e;
+              unpack_f32x2(f, a, b);
+              unpack_f32x2(g, d, e);
+              a = ex2(a);
+              b = ex2(b);
+              d = ex2(d);
+              e = ex2(e);
+              sum0 = add_f32x2(sum0, pack_f32x2(a, b));
+              sum1 = add_f32x2(sum1, pack_f32x2(d, e));
+              pk[k / 2] = pack16<BF16>(a, b);
+              pk[k / 2 + 1] = pack16<BF16>(d, e);
             }
-            tmem_st32_nowait(s_base + 32 * c, pk);
+            tmem_st16_nowait(s_base + c / 2, pk);
+          };
+#pragma unroll 1
+          for (int c = 0; c < KT; c += 64) {
+            tmem_wait_ld();
+            tmem_ld32_nowait(s_base + c + 32, y);
+            weigh(x, c);
+            tmem_wait_ld();
+            if (c + 64 < KT) tmem_ld32_nowait(s_base + c + 64, x);
+            weigh(y, c + 32);
+            if (c == 0) {  // the first half of P: its O MMAs may begin
+              tmem_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(p_half + buf);
+            }
           }
-          l_run += (sum0 + sum1) + (sum2 + sum3);
+          float a, b;
+          unpack_f32x2(add_f32x2(sum0, sum1), a, b);
+          l_run += a + b;
           tmem_wait_st();
+        } else if (lane == 0) {
+          mbar_arrive(p_half + buf);
         }
         tc_fence_before();
         __syncwarp();
@@ -667,7 +758,7 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
         if (!(ok = wait_all(o_done + m, (uint32_t)((it - 1) & 1)))) break;
         tc_fence_after();
       }
-      const bool whole = w.n == w.units;
+      const bool whole = tiles == w.span.tiles;
       if (warp_valid) {
         if (whole) {
           const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
@@ -737,56 +828,89 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
 // Joins the shares of the items that more than one CTA worked on.  CTA x is
 // the boundary between runs x and x + 1; the first boundary inside an item
 // joins it, in the order of the runs.  One thread takes 4 columns of a row.
+constexpr int MERGE_ROWS = 8, MERGE_AHEAD = 8;
+
 template <bool BF16, int D, int NM>
-__global__ void __launch_bounds__(256) k_paged_merge(const PagedParams p, int grid) {
+__global__ void __launch_bounds__(MERGE_ROWS * D / 4) k_paged_merge(const PagedParams p, int grid) {
   constexpr int ROWS = 128 * NM;
+  extern __shared__ float merge_sm[];
+  float(*wm)[MERGE_ROWS] = reinterpret_cast<float(*)[MERGE_ROWS]>(merge_sm);  // [grid]
+  float(*wl)[MERGE_ROWS] = wm + grid;
+  __shared__ float inv[MERGE_ROWS];
   pdl_launch_dependents();
   pdl_wait();
   const WsHead head = *reinterpret_cast<const WsHead*>(p.ws);
   const int c = blockIdx.x + 1;
   if (c >= head.ctas) return;
   const WsCta rec = reinterpret_cast<const WsCta*>(p.ws + 256)[c];
-  if (rec.off == 0) return;  // the run begins with its item
-  auto start = [&](int x) { return head.units * x / head.ctas; };
-  const long long item0 = start(c) - rec.off, item1 = item0 + rec.units;
-  if (start(c - 1) > item0) return;  // an earlier boundary joins this item
+  if (rec.at <= SETUP<NM>) return;  // the run begins with the item's first tile
+  auto start = [&](int x) { return head.cost * x / head.ctas; };
+  const long long item0 = start(c) - rec.at, item1 = item0 + rec.cost;
+  if (start(c - 1) > item0 + SETUP<NM>) return;  // an earlier boundary joins this item
   int end = c + 1;                   // runs c - 1 .. end - 1 hold a share
   while (end < head.ctas && start(end) < item1) ++end;
   const Seq s = load_seq(p, rec.b);
   const int t0 = rec.mt * p.tok * NM, tokens = min(p.tok * NM, s.n - t0);
   const int per = p.tok * p.group;  // rows of an M tile
   const int rows = tokens * p.group;
-  const float* parts = reinterpret_cast<const float*>(p.ws + ws_records(grid));
+  const int n = end - (c - 1);      // shares
   constexpr size_t SF = ws_slot_floats(ROWS, D);
-  auto share = [&](int x) { return parts + (2 * (size_t)x + (x == c - 1 ? 1 : 0)) * SF; };
-  for (int e = blockIdx.y * blockDim.x + threadIdx.x; e < rows * (D / 4); e += gridDim.y * blockDim.x) {
-    const int d4 = e / rows, i = e - d4 * rows;         // i: token-major row of the item
-    const int mi = i / per, row = mi * 128 + (i - mi * per);
-    float M = -INFINITY;
-    for (int x = c - 1; x < end; ++x) {
-      const float* q = share(x);
-      if (q[(size_t)ROWS * (D + 1) + row] != 0.f) M = fmaxf(M, q[(size_t)ROWS * D + row]);
+  const float* parts = reinterpret_cast<const float*>(p.ws + ws_records(grid)) + 2 * (size_t)(c - 1) * SF;
+  auto share = [&](int x) { return parts + (2 * (size_t)x + (x == 0 ? 1 : 0)) * SF; };
+  // this CTA's rows, MERGE_ROWS at a time
+  for (int r0 = blockIdx.y * MERGE_ROWS; r0 < rows; r0 += gridDim.y * MERGE_ROWS) {
+    const int nr = min(MERGE_ROWS, rows - r0);
+    __syncthreads();  // the last pass has read its weights
+    // the shares' maxima and sums; then, a row a thread, their weights
+    for (int e = threadIdx.x; e < n * MERGE_ROWS; e += blockDim.x) {
+      const int x = e / MERGE_ROWS, i = e % MERGE_ROWS;
+      if (i >= nr) continue;
+      const int mi = (r0 + i) / per, row = mi * 128 + (r0 + i - mi * per);
+      const float* q = share(x) + (size_t)ROWS * D + row;
+      wm[x][i] = q[0];
+      wl[x][i] = q[ROWS];
     }
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float L = 0.f;
-    for (int x = c - 1; x < end; ++x) {
-      const float* q = share(x);
-      const float l = q[(size_t)ROWS * (D + 1) + row];
-      if (l == 0.f) continue;  // this share saw no key of the row
-      const float wgt = exp2f(q[(size_t)ROWS * D + row] - M);
-      const float4 o = *reinterpret_cast<const float4*>(q + ((size_t)d4 * ROWS + row) * 4);
-      acc.x += wgt * o.x;
-      acc.y += wgt * o.y;
-      acc.z += wgt * o.z;
-      acc.w += wgt * o.w;
-      L += wgt * l;
+    __syncthreads();
+    if ((int)threadIdx.x < nr) {
+      const int i = threadIdx.x;
+      float M = -INFINITY, L = 0.f;
+      for (int x = 0; x < n; ++x)
+        if (wl[x][i] != 0.f) M = fmaxf(M, wm[x][i]);
+      for (int x = 0; x < n; ++x) {
+        const float wgt = wl[x][i] != 0.f ? ex2(wm[x][i] - M) : 0.f;  // 0: this share saw no key of the row
+        L += wgt * wl[x][i];
+        wm[x][i] = wgt;
+      }
+      inv[i] = L == 0.f ? 0.f : 1.f / L;
+      const int t = s.row0 + t0 + (r0 + i) / p.group, h = rec.kvh * p.group + (r0 + i) % p.group;
+      if (p.lse)
+        p.lse[t * p.lse_row + h * p.lse_head] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
     }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    const long long t = s.row0 + t0 + i / p.group, h = rec.kvh * p.group + i % p.group;
-    *reinterpret_cast<uint2*>(p.out + t * p.o_row + h * p.o_head + 4 * d4) =
-        make_uint2(pack16<BF16>(acc.x * inv, acc.y * inv), pack16<BF16>(acc.z * inv, acc.w * inv));
-    if (p.lse && d4 == 0)
-      p.lse[t * p.lse_row + h * p.lse_head] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+    __syncthreads();
+    const int i = threadIdx.x % MERGE_ROWS, d4 = threadIdx.x / MERGE_ROWS;
+    if (i < nr) {
+      const int mi = (r0 + i) / per, row = mi * 128 + (r0 + i - mi * per);
+      const float4* q = reinterpret_cast<const float4*>(parts) + (size_t)d4 * ROWS + row;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int x0 = 0; x0 < n; x0 += MERGE_AHEAD) {  // MERGE_AHEAD loads in flight
+        float4 o[MERGE_AHEAD];
+#pragma unroll
+        for (int k = 0; k < MERGE_AHEAD; ++k)
+          if (x0 + k < n) o[k] = q[(2 * (size_t)(x0 + k) + (x0 + k == 0 ? 1 : 0)) * (SF / 4)];
+#pragma unroll
+        for (int k = 0; k < MERGE_AHEAD; ++k) {
+          const float wgt = x0 + k < n ? wm[x0 + k][i] : 0.f;
+          if (wgt == 0.f) continue;
+          acc.x += wgt * o[k].x;
+          acc.y += wgt * o[k].y;
+          acc.z += wgt * o[k].z;
+          acc.w += wgt * o[k].w;
+        }
+      }
+      const long long t = s.row0 + t0 + (r0 + i) / p.group, h = rec.kvh * p.group + (r0 + i) % p.group;
+      *reinterpret_cast<uint2*>(p.out + t * p.o_row + h * p.o_head + 4 * d4) =
+          make_uint2(pack16<BF16>(acc.x * inv[i], acc.y * inv[i]), pack16<BF16>(acc.z * inv[i], acc.w * inv[i]));
+    }
   }
 }
 
@@ -848,9 +972,9 @@ int launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, con
   if (cudaLaunchKernelEx(&cfg, kern, q, k, v, p) != cudaSuccess) return DFLASH_ERR_CUDA;
   if (grid == 1) return DFLASH_OK;
   cudaLaunchConfig_t mc = cfg;
-  mc.gridDim = dim3((unsigned)(grid - 1), 4);
-  mc.blockDim = dim3(256);
-  mc.dynamicSmemBytes = 0;
+  mc.gridDim = dim3((unsigned)(grid - 1), 8);
+  mc.blockDim = dim3(MERGE_ROWS * D / 4);
+  mc.dynamicSmemBytes = (size_t)grid * 2 * MERGE_ROWS * sizeof(float);
   return cudaLaunchKernelEx(&mc, k_paged_merge<BF16, D, NM>, p, grid) == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
 }
 
