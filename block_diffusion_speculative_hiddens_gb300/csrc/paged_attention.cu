@@ -64,13 +64,16 @@ struct PagedParams {
 };
 
 // Workspace: a header, one record a CTA, two partial slots a CTA.
-struct WsHead {
-  long long cost;  // of all items
-  int ctas;        // that share it
+// The cost of all items in runs of `each`, the first `more` of them one longer.
+struct Runs {
+  long long each;
+  int more, ctas;
 };
+DFL_DEV long long run_start(const Runs& r, int c) { return r.each * c + min(c, r.more); }
 struct WsCta {
-  int at, cost;  // of the item its run begins in: cost before it, cost of the item
-  int b, mt, kvh, pad[3];
+  int at, cost;        // of the item its run begins in: cost before the run, cost of the item
+  int row0, rows, head;  // the item's first row of q, its rows x heads, its first head
+  int pad[3];
 };
 constexpr size_t ws_records(int grid) { return 256 + ((size_t)grid * sizeof(WsCta) + 255) / 256 * 256; }
 // One slot: O [D/4][rows] float4, running maxima [rows], sums [rows].
@@ -283,7 +286,7 @@ struct Sched {
 // at most) and their first pairs (`first` [batch + 1]).  False: no work at
 // all, or none for this CTA.
 template <int NM>
-DFL_DEV bool locate(const PagedParams& p, Sched* sc, Seq* seqs, int* first, Walk& w, long long* cost_out, int* ctas_out) {
+DFL_DEV bool locate(const PagedParams& p, Sched* sc, Seq* seqs, int* first, Walk& w, Runs* runs) {
   const int per = p.tok * NM;
   const bool kept = p.batch <= (int)blockDim.x;
   long long pairs = 0;
@@ -325,11 +328,16 @@ DFL_DEV bool locate(const PagedParams& p, Sched* sc, Seq* seqs, int* first, Walk
     total += all;
   }
   if (total == 0) return false;
-  const int ctas = (int)min((long long)gridDim.x, total);
-  *cost_out = total;
-  *ctas_out = ctas;
-  if ((int)blockIdx.x >= ctas) return false;
-  const long long u0 = total * blockIdx.x / ctas, u1 = total * (blockIdx.x + 1) / ctas;
+  runs->ctas = (int)min((long long)gridDim.x, total);
+  if (total < (1ll << 31)) {  // a 64-bit division takes a hundred cycles more
+    runs->each = (uint32_t)total / (uint32_t)runs->ctas;
+    runs->more = (int)((uint32_t)total % (uint32_t)runs->ctas);
+  } else {
+    runs->each = total / runs->ctas;
+    runs->more = (int)(total % runs->ctas);
+  }
+  if ((int)blockIdx.x >= runs->ctas) return false;
+  const long long u0 = run_start(*runs, blockIdx.x), u1 = run_start(*runs, blockIdx.x + 1);
   long long base = 0;
   for (long long p0 = 0; p0 < pairs; p0 += blockDim.x) {
     if (!once) {
@@ -350,8 +358,8 @@ DFL_DEV bool locate(const PagedParams& p, Sched* sc, Seq* seqs, int* first, Walk
   const long long in = u0 - sc->before;
   w.b = sc->b;
   w.mt = sc->mt;
-  w.kvh = (int)(in / sc->cost);
-  w.at = (int)(in % sc->cost);
+  w.kvh = in < (1ll << 31) ? (int)((uint32_t)in / (uint32_t)sc->cost) : (int)(in / sc->cost);
+  w.at = (int)(in - (long long)w.kvh * sc->cost);
   w.left = u1 - u0;
   w.s = kept ? seqs[w.b] : load_seq(p, w.b);
   walk_item<NM>(p, w);
@@ -418,19 +426,18 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
   pdl_wait();
 
   Walk w;
-  long long cost = 0;
-  int ctas = 0;
+  Runs runs = {0, 0, 0};
   Seq* seqs = reinterpret_cast<Seq*>(sm);
-  const bool work = locate<NM>(p, sched, seqs, reinterpret_cast<int*>(seqs + C::THREADS), w, &cost, &ctas);
+  const bool work = locate<NM>(p, sched, seqs, reinterpret_cast<int*>(seqs + C::THREADS), w, &runs);
   if (threadIdx.x == 0) {
-    if (blockIdx.x == 0) *reinterpret_cast<WsHead*>(p.ws) = WsHead{cost, ctas};
+    if (blockIdx.x == 0) *reinterpret_cast<Runs*>(p.ws) = runs;
     if (work) {
       WsCta* rec = reinterpret_cast<WsCta*>(p.ws + 256) + blockIdx.x;
       rec->at = w.at;
       rec->cost = SETUP<NM> + w.span.tiles;
-      rec->b = w.b;
-      rec->mt = w.mt;
-      rec->kvh = w.kvh;
+      rec->row0 = w.s.row0 + w.t0;
+      rec->rows = (w.t1 - w.t0) * p.group;
+      rec->head = w.kvh * p.group;
     }
   }
   fence_proxy_async_smem();  // the sequences were written and read before the loads land over them
@@ -828,7 +835,7 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
 // Joins the shares of the items that more than one CTA worked on.  CTA x is
 // the boundary between runs x and x + 1; the first boundary inside an item
 // joins it, in the order of the runs.  One thread takes 4 columns of a row.
-constexpr int MERGE_ROWS = 8, MERGE_AHEAD = 8;
+constexpr int MERGE_ROWS = 8, MERGE_AHEAD = 16;
 
 template <bool BF16, int D, int NM>
 __global__ void __launch_bounds__(MERGE_ROWS * D / 4) k_paged_merge(const PagedParams p, int grid) {
@@ -836,81 +843,74 @@ __global__ void __launch_bounds__(MERGE_ROWS * D / 4) k_paged_merge(const PagedP
   extern __shared__ float merge_sm[];
   float(*wm)[MERGE_ROWS] = reinterpret_cast<float(*)[MERGE_ROWS]>(merge_sm);  // [grid]
   float(*wl)[MERGE_ROWS] = wm + grid;
-  __shared__ float inv[MERGE_ROWS];
+  __shared__ float red[D / 4][MERGE_ROWS];
   pdl_launch_dependents();
   pdl_wait();
-  const WsHead head = *reinterpret_cast<const WsHead*>(p.ws);
   const int c = blockIdx.x + 1;
-  if (c >= head.ctas) return;
-  const WsCta rec = reinterpret_cast<const WsCta*>(p.ws + 256)[c];
-  if (rec.at <= SETUP<NM>) return;  // the run begins with the item's first tile
-  auto start = [&](int x) { return head.cost * x / head.ctas; };
-  const long long item0 = start(c) - rec.at, item1 = item0 + rec.cost;
-  if (start(c - 1) > item0 + SETUP<NM>) return;  // an earlier boundary joins this item
-  int end = c + 1;                   // runs c - 1 .. end - 1 hold a share
-  while (end < head.ctas && start(end) < item1) ++end;
-  const Seq s = load_seq(p, rec.b);
-  const int t0 = rec.mt * p.tok * NM, tokens = min(p.tok * NM, s.n - t0);
+  const Runs runs = *reinterpret_cast<const Runs*>(p.ws);
+  const WsCta rec = reinterpret_cast<const WsCta*>(p.ws + 256)[c];  // its bytes exist for every c < grid
+  if (c >= runs.ctas || rec.at <= SETUP<NM>) return;                // the run begins with the item's first tile
+  const long long item0 = run_start(runs, c) - rec.at, item1 = item0 + rec.cost;
+  if (run_start(runs, c - 1) > item0 + SETUP<NM>) return;  // an earlier boundary joins this item
+  int n = 2;                                               // runs c - 1 .. c - 2 + n hold a share
+  while (c - 1 + n < runs.ctas && run_start(runs, c - 1 + n) < item1) ++n;
   const int per = p.tok * p.group;  // rows of an M tile
-  const int rows = tokens * p.group;
-  const int n = end - (c - 1);      // shares
   constexpr size_t SF = ws_slot_floats(ROWS, D);
   const float* parts = reinterpret_cast<const float*>(p.ws + ws_records(grid)) + 2 * (size_t)(c - 1) * SF;
-  auto share = [&](int x) { return parts + (2 * (size_t)x + (x == 0 ? 1 : 0)) * SF; };
+  auto share = [&](int x) { return (2 * (size_t)x + (x == 0 ? 1 : 0)) * SF; };
+  const int i = threadIdx.x % MERGE_ROWS, d4 = threadIdx.x / MERGE_ROWS;
   // this CTA's rows, MERGE_ROWS at a time
-  for (int r0 = blockIdx.y * MERGE_ROWS; r0 < rows; r0 += gridDim.y * MERGE_ROWS) {
-    const int nr = min(MERGE_ROWS, rows - r0);
-    __syncthreads();  // the last pass has read its weights
-    // the shares' maxima and sums; then, a row a thread, their weights
-    for (int e = threadIdx.x; e < n * MERGE_ROWS; e += blockDim.x) {
-      const int x = e / MERGE_ROWS, i = e % MERGE_ROWS;
-      if (i >= nr) continue;
-      const int mi = (r0 + i) / per, row = mi * 128 + (r0 + i - mi * per);
-      const float* q = share(x) + (size_t)ROWS * D + row;
-      wm[x][i] = q[0];
-      wl[x][i] = q[ROWS];
+  for (int r0 = blockIdx.y * MERGE_ROWS; r0 < rec.rows; r0 += gridDim.y * MERGE_ROWS) {
+    const int ri = min(r0 + i, rec.rows - 1), mi = ri / per, row = mi * 128 + (ri - mi * per);
+    // the first shares' outputs are on their way while the weights are made
+    const float* q = parts + ((size_t)d4 * ROWS + row) * 4;
+    float4 o[MERGE_AHEAD];
+#pragma unroll
+    for (int k = 0; k < MERGE_AHEAD; ++k)
+      if (k < n) o[k] = *reinterpret_cast<const float4*>(q + share(k));
+    // the shares' maxima and sums, and with them their weights: thread (i, d4) takes shares d4, d4 + D / 4, ...
+    float M = -INFINITY;
+    for (int x = d4; x < n; x += D / 4) {
+      const float* ml = parts + share(x) + (size_t)ROWS * D + row;
+      const float m = ml[0], l = ml[ROWS];
+      wm[x][i] = m;
+      wl[x][i] = l;
+      if (l != 0.f) M = fmaxf(M, m);
     }
+    red[d4][i] = M;
     __syncthreads();
-    if ((int)threadIdx.x < nr) {
-      const int i = threadIdx.x;
-      float M = -INFINITY, L = 0.f;
-      for (int x = 0; x < n; ++x)
-        if (wl[x][i] != 0.f) M = fmaxf(M, wm[x][i]);
-      for (int x = 0; x < n; ++x) {
-        const float wgt = wl[x][i] != 0.f ? ex2(wm[x][i] - M) : 0.f;  // 0: this share saw no key of the row
-        L += wgt * wl[x][i];
-        wm[x][i] = wgt;
-      }
-      inv[i] = L == 0.f ? 0.f : 1.f / L;
-      const int t = s.row0 + t0 + (r0 + i) / p.group, h = rec.kvh * p.group + (r0 + i) % p.group;
-      if (p.lse)
-        p.lse[t * p.lse_row + h * p.lse_head] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
-    }
-    __syncthreads();
-    const int i = threadIdx.x % MERGE_ROWS, d4 = threadIdx.x / MERGE_ROWS;
-    if (i < nr) {
-      const int mi = (r0 + i) / per, row = mi * 128 + (r0 + i - mi * per);
-      const float4* q = reinterpret_cast<const float4*>(parts) + (size_t)d4 * ROWS + row;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int x0 = 0; x0 < n; x0 += MERGE_AHEAD) {  // MERGE_AHEAD loads in flight
-        float4 o[MERGE_AHEAD];
+#pragma unroll 8
+    for (int x = 0; x < min(n, D / 4); ++x) M = fmaxf(M, red[x][i]);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float L = 0.f;
+    for (int x0 = 0; x0 < n; x0 += MERGE_AHEAD) {
+      if (x0 > 0) {
 #pragma unroll
         for (int k = 0; k < MERGE_AHEAD; ++k)
-          if (x0 + k < n) o[k] = q[(2 * (size_t)(x0 + k) + (x0 + k == 0 ? 1 : 0)) * (SF / 4)];
-#pragma unroll
-        for (int k = 0; k < MERGE_AHEAD; ++k) {
-          const float wgt = x0 + k < n ? wm[x0 + k][i] : 0.f;
-          if (wgt == 0.f) continue;
-          acc.x += wgt * o[k].x;
-          acc.y += wgt * o[k].y;
-          acc.z += wgt * o[k].z;
-          acc.w += wgt * o[k].w;
-        }
+          if (x0 + k < n) o[k] = *reinterpret_cast<const float4*>(q + share(x0 + k));
       }
-      const long long t = s.row0 + t0 + (r0 + i) / p.group, h = rec.kvh * p.group + (r0 + i) % p.group;
-      *reinterpret_cast<uint2*>(p.out + t * p.o_row + h * p.o_head + 4 * d4) =
-          make_uint2(pack16<BF16>(acc.x * inv[i], acc.y * inv[i]), pack16<BF16>(acc.z * inv[i], acc.w * inv[i]));
+#pragma unroll
+      for (int k = 0; k < MERGE_AHEAD; ++k) {
+        if (x0 + k >= n) break;
+        const float l = wl[x0 + k][i];
+        if (l == 0.f) continue;  // this share saw no key of the row
+        const float wgt = ex2(wm[x0 + k][i] - M);
+        L += wgt * l;
+        acc.x += wgt * o[k].x;
+        acc.y += wgt * o[k].y;
+        acc.z += wgt * o[k].z;
+        acc.w += wgt * o[k].w;
+      }
     }
+    if (r0 + i < rec.rows) {
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+      const long long t = rec.row0 + ri / p.group, h = rec.head + ri % p.group;
+      *reinterpret_cast<uint2*>(p.out + t * p.o_row + h * p.o_head + 4 * d4) =
+          make_uint2(pack16<BF16>(acc.x * inv, acc.y * inv), pack16<BF16>(acc.z * inv, acc.w * inv));
+      if (p.lse && d4 == 0)
+        p.lse[t * p.lse_row + h * p.lse_head] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+    }
+    __syncthreads();  // the weights are read
   }
 }
 
