@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
   uint64_t* s_full = empty + C::SLOTS;  // [2] S (and every MMA before it) done
   uint64_t* p_full = s_full + 2;        // [2] P written
   uint64_t* p_half = p_full + 2;        // [2] the first 64 keys of P written
-  uint64_t* o_done = p_half + 2;        // [2] an O MMA done
+  uint64_t* o_done = p_half + 2;        // [2] an O MMA done: of M tile m, or (NM = 1) of tiles of one parity
   uint64_t* o_empty = o_done + 2;       // [2] O read out
   uint64_t* q_full = o_empty + 2;       // [QBUFS]
   uint64_t* q_empty = q_full + 2;
@@ -453,7 +453,11 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
     // nothing for this CTA
   } else if (warp == LOAD_WARP) {
     // ------------------------------------------------ loads
+    // A thread has only a few copies in flight at a time, so every box of a
+    // tile has a lane of its own: `boxes` pages (or one part of a page) of
+    // each 64-dim panel.
     const int page = 1 << p.shift, box = min(page, KT), boxes = KT / box;
+    const int bi = lane % boxes, bh = lane / boxes;  // this lane's box, if bh is a panel
     int seg = 0;
     long long nt = 0;  // ring slots filled
     bool ok = true;
@@ -462,17 +466,20 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
       if (tiles == 0) continue;
       if (lane == 0 && (p.kv_len ? (long long)p.kv_len[w.b] : w.s.ctx + w.s.n) > p.cap)
         dev_error(p.status, DFLASH_DEV_PAGE);
-      const int qb = seg % C::QBUFS;
-      if (seg >= C::QBUFS && !wait_all(q_empty + qb, (uint32_t)((seg / C::QBUFS - 1) & 1))) break;
-      const int nm = NM == 2 && w.t0 + p.tok < w.t1 ? 2 : 1;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(q_full + qb, (uint32_t)(nm * (D / 64) * p.tok * p.group * 128));
-        for (int m = 0; m < nm; ++m)
-          for (int h = 0; h < D / 64; ++h)
-            tma_load_3d(sm + (qb * NM + m) * C::TILE + h * C::PANEL, &qmap, q_full + qb, 64 * h, w.kvh * p.group,
-                        w.s.row0 + w.t0 + m * p.tok);
-      }
-      ++seg;
+      auto load_q = [&] {
+        const int qb = seg % C::QBUFS;
+        if (seg >= C::QBUFS && !wait_all(q_empty + qb, (uint32_t)((seg / C::QBUFS - 1) & 1))) return false;
+        const int nm = NM == 2 && w.t0 + p.tok < w.t1 ? 2 : 1;
+        if (lane == 0) mbar_arrive_expect_tx(q_full + qb, (uint32_t)(nm * (D / 64) * p.tok * p.group * 128));
+        __syncwarp();
+        const int m = lane / (D / 64), h = lane % (D / 64);
+        if (m < nm)
+          tma_load_3d(sm + (qb * NM + m) * C::TILE + h * C::PANEL, &qmap, q_full + qb, 64 * h, w.kvh * p.group,
+                      w.s.row0 + w.t0 + m * p.tok);
+        ++seg;
+        return true;
+      };
+      if (C::QBUFS == 2 && !load_q()) break;
       const int* row = p.table + w.b * p.table_stride;
       const int first_page = w.span.lo >> p.shift, end_page = (w.span.hi + page - 1) >> p.shift;
       int base = -64, ids = 0;  // lanes hold 32 entries of the table row from `base` on
@@ -489,6 +496,7 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
             else dev_error(p.status, DFLASH_DEV_PAGE);
           }
         }
+        const int id = __shfl_sync(0xffffffffu, ids, e0 + bi - base);
         for (int kv = 0; kv < 2; ++kv, ++nt) {  // K, then V
           const int s = (int)(nt % C::SLOTS);
           if (nt >= C::SLOTS && !wait_all(empty + s, (uint32_t)((nt / C::SLOTS - 1) & 1))) {
@@ -496,15 +504,13 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
             break;
           }
           if (lane == 0) mbar_arrive_expect_tx(full + s, C::TILE);
-          uint8_t* dst = sm + C::OFF_RING + s * C::TILE;
-          for (int i = 0; i < boxes; ++i) {
-            const int id = __shfl_sync(0xffffffffu, ids, e0 + i - base);
-            if (lane == 0)
-              for (int h = 0; h < D / 64; ++h)
-                tma_load_4d(dst + h * C::PANEL + i * box * 128, kv ? &vmap : &kmap, full + s, 64 * h,
-                            page > KT ? key0 & (page - 1) : 0, w.kvh, id);
-          }
+          __syncwarp();
+          if (bh < D / 64)
+            tma_load_4d(sm + C::OFF_RING + s * C::TILE + bh * C::PANEL + bi * box * 128, kv ? &vmap : &kmap, full + s,
+                        64 * bh, page > KT ? key0 & (page - 1) : 0, w.kvh, id);
         }
+        // one Q buffer: its load waits for the last item's S, the first tiles do not
+        if (C::QBUFS == 1 && j == 0 && ok) ok = load_q();
       }
     } while (ok && walk_next<NM>(p, w));
     // every copy lands before the CTA may exit
@@ -593,7 +599,7 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
                                   sdesc_sw128_mn(va + 2048u * kk, C::PANEL), idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
           }
           if (!ok) break;
-          tc_commit_elect(o_done + m);
+          tc_commit_elect(o_done + buf);
           if (m == nm - 1) tc_commit_elect(empty + vs % C::SLOTS);
           if (NM == 2 && j + 1 < tiles) {
             if (m == 0) {
@@ -622,6 +628,14 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
     const uint32_t o_base = lane_base + (uint32_t)(C::O_COL + D * m);
     int it = 0;  // S tiles of this M tile
     bool ok = true;
+    // The O MMA of S tile i, and with it every one before.  A barrier tells
+    // only whether one phase is over, so it must never be two ahead of a
+    // waiting warp: NM = 2 waits after S i, which follows the O MMA of i - 1 on
+    // the tensor core; NM = 1, whose S runs a tile ahead, has a barrier for
+    // each parity.  The next O MMA on either needs this warp's P.
+    auto wait_o = [&](int i) {
+      return NM == 2 ? wait_all(o_done + m, (uint32_t)(i & 1)) : wait_all(o_done + (i & 1), (uint32_t)((i >> 1) & 1));
+    };
     do {
       const int tiles = w.n;
       if (!w.out) continue;
@@ -693,7 +707,7 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
           if (__any_sync(0xffffffffu, move)) {
             const float m_new = move ? mx : m_run;
             if (j > 0) {  // O of the tiles before is against m_run
-              if (NM == 1 && !(ok = wait_all(o_done + m, (uint32_t)((it - 1) & 1)))) break;
+              if (NM == 1 && !(ok = wait_o(it - 1))) break;
               tc_fence_after();
               const float alpha = move ? ex2(m_run - m_new) : 1.f;
               tmem_wait_ld();
@@ -761,8 +775,7 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
       if (!ok) break;
       // the segment's O
       if (tiles > 0) {
-        if (NM == 1 && tiles > 1 && !(ok = wait_all(o_done + m, (uint32_t)((it - 2) & 1)))) break;
-        if (!(ok = wait_all(o_done + m, (uint32_t)((it - 1) & 1)))) break;
+        if (!(ok = wait_o(it - 1))) break;
         tc_fence_after();
       }
       const bool whole = tiles == w.span.tiles;

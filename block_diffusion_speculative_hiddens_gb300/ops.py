@@ -102,20 +102,21 @@ class RopePlan:
 
 def _rows(t, what, dtype, device, rows=None, heads=None, dim=None):
     """A [rows, heads, head_dim] tensor's (pointer, row stride, head stride)."""
+    shape, stride = t.shape, t.stride()
+    if t.dtype is dtype and t.get_device() == device and len(shape) == 3 and stride[2] == 1 and \
+            (rows is None or shape[0] == rows) and (heads is None or shape[1] == heads) and \
+            (dim is None or shape[2] == dim):
+        return t.data_ptr(), stride[0], stride[1]
     if t.dtype is not dtype or t.get_device() != device:
         raise ValueError(f"{what}: expected {dtype} on cuda:{device}, got {t.dtype} on {t.device}")
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 3 or (rows is not None and shape[0] != rows) or (heads is not None and shape[1] != heads) \
-            or (dim is not None and shape[2] != dim):
-        raise ValueError(f"{what}: expected [{rows or 'rows'}, {heads or 'heads'}, {dim or 'head_dim'}], got {list(shape)}")
-    if stride[2] != 1:
+    if len(shape) == 3 and stride[2] != 1:
         raise ValueError(f"{what}: the head dimension has stride {stride[2]}, expected 1")
-    return t.data_ptr(), stride[0], stride[1]
+    raise ValueError(f"{what}: expected [{'rows' if rows is None else rows}, {'heads' if heads is None else heads}, "
+                     f"{'head_dim' if dim is None else dim}], got {list(shape)}")
 
 
 def _i32(t, what, n, device):
-    if t.dtype is not torch.int32 or t.get_device() != device or t.dim() != 1 or t.shape[0] != n or \
-            not t.is_contiguous():
+    if t.dtype is not torch.int32 or t.get_device() != device or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{what}: expected {n} contiguous int32 values on cuda:{device}, got {list(t.shape)} "
                          f"{t.dtype} on {t.device}")
     return t.data_ptr()
@@ -142,26 +143,44 @@ def _disjoint_heads(x, y):
     return wx <= gap and gap + wy <= row
 
 
+# The current stream's handle; torch.cuda.current_stream builds an object for
+# it, a microsecond of a call that takes ten.
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _raw_stream(stream, device):
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        return _current_stream(device)
     if stream.device.index != device:
         raise ValueError(f"stream: on {stream.device}, the tensors are on cuda:{device}")
     return stream.cuda_stream
 
 
-def _empty(shape, like, stream):
-    """An output on the call's stream: the allocator hands its memory out again in that stream's order."""
+def _empty(shape, dtype, like, stream):
+    """Memory on the call's stream: the allocator hands it out again in that stream's order."""
     if stream is None:
-        return torch.empty(shape, dtype=like.dtype, device=like.device)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=like.dtype, device=like.device)
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _out(out, src, rows, heads, dim, what, dtype, device, stream):
+    """A call's output beside its input `src` -- the caller's, checked, or a new one -- and its pointer and strides."""
+    if out is None:
+        out = _empty((rows, heads, dim), dtype, src, stream)
+        return out, (out.data_ptr(), heads * dim, dim)
+    at = _rows(out, what, dtype, device, rows, heads, dim)
+    if out is not src:
+        _no_overlap(out, src, what)
+    return out, at
 
 
 def _cuda_half(t, what):
-    if t.dtype not in _DTYPES or t.device.type != "cuda":
+    device = t.get_device()
+    if t.dtype not in _DTYPES or device < 0:
         raise ValueError(f"{what}: expected a float16 or bfloat16 CUDA tensor, got {t.dtype} on {t.device}")
-    return t.get_device()
+    return device
 
 
 def rope(plan: RopePlan, q, k, positions, *, backward: bool = False, q_out=None, k_out=None, stream=None):
@@ -170,26 +189,19 @@ def rope(plan: RopePlan, q, k, positions, *, backward: bool = False, q_out=None,
     unless given (an input itself: in place).  Any strides of rows and heads.
     backward=True applies the transposed rotation: the inputs' gradient from
     the outputs'."""
-    device = _cuda_half(q, "q")
-    rows, hq, dim = q.shape if q.dim() == 3 else (None, None, None)
-    qs = _rows(q, "q", q.dtype, device)
-    if q_out is None:
-        q_out = _empty((rows, hq, dim), q, stream)
-    else:
-        _no_overlap(q_out, q, "q_out")
-    qo = _rows(q_out, "q_out", q.dtype, device, rows, hq, dim)
+    device, dtype = _cuda_half(q, "q"), q.dtype
+    raw = _raw_stream(stream, device)
+    qs = _rows(q, "q", dtype, device)
+    rows, hq, dim = q.shape
+    q_out, qo = _out(q_out, q, rows, hq, dim, "q_out", dtype, device, stream)
     ks, ko, hk = _NONE, _NONE, 0
     if k is not None:
-        ks = _rows(k, "k", q.dtype, device, rows, None, dim)
+        ks = _rows(k, "k", dtype, device, rows, None, dim)
         hk = k.shape[1]
-        if k_out is None:
-            k_out = _empty((rows, hk, dim), k, stream)
-        else:
-            _no_overlap(k_out, k, "k_out")
-        ko = _rows(k_out, "k_out", q.dtype, device, rows, hk, dim)
-    pos = _i32(positions, "positions", rows, device)
-    args = _ROPE.pack(*qs, *ks, *qo, *ko, pos, rows, hq, hk, dim, _DTYPES[q.dtype], int(backward), device)
-    code = load().dflash_rope(plan._ref, args, _raw_stream(stream, device))
+        k_out, ko = _out(k_out, k, rows, hk, dim, "k_out", dtype, device, stream)
+    args = _ROPE.pack(*qs, *ks, *qo, *ko, _i32(positions, "positions", rows, device), rows, hq, hk, dim, _DTYPES[dtype],
+                      bool(backward), device)
+    code = load().dflash_rope(plan._ref, args, raw)
     if code:
         raise DflashError("dflash_rope", code)
     return q_out, k_out
@@ -244,6 +256,7 @@ def append(cache: PagedCache, k, v, cu_rows, ctx_len, *, plan: RopePlan = None, 
     [rows, q_heads, head_dim], if given, is rotated alike; returns q_out (None
     without q)."""
     device, dtype, dim = cache.device, cache.dtype, cache.head_dim
+    raw = _raw_stream(stream, device)
     ks = _rows(k, "k", dtype, device, None, cache.kv_heads, dim)
     rows = k.shape[0]
     vs = _rows(v, "v", dtype, device, rows, cache.kv_heads, dim)
@@ -252,13 +265,9 @@ def append(cache: PagedCache, k, v, cu_rows, ctx_len, *, plan: RopePlan = None, 
     if q is not None:
         qs = _rows(q, "q", dtype, device, rows, None, dim)
         hq = q.shape[1]
-        if q_out is None:
-            q_out = _empty((rows, hq, dim), q, stream)
-        else:
-            _no_overlap(q_out, q, "q_out")
-        qo = _rows(q_out, "q_out", dtype, device, rows, hq, dim)
+        q_out, qo = _out(q_out, q, rows, hq, dim, "q_out", dtype, device, stream)
     args = _APPEND.pack(*ks, *vs, *qs, *qo, cu, ctx, rows, b, hq, 0)
-    code = load().dflash_paged_append(cache._c, None if plan is None else plan._ref, args, _raw_stream(stream, device))
+    code = load().dflash_paged_append(cache._c, None if plan is None else plan._ref, args, raw)
     if code:
         raise DflashError("dflash_paged_append", code)
     return q_out
@@ -273,13 +282,16 @@ def attention(cache: PagedCache, q, cu_rows, ctx_len, *, kv_len=None, causal: bo
     lse: float32 [rows, q_heads] output for the rows' log-sum-exp.  workspace:
     uint8, attention_workspace() bytes; by default allocated for the call."""
     device, dtype, dim = cache.device, cache.dtype, cache.head_dim
+    raw = _raw_stream(stream, device)
     qs = _rows(q, "q", dtype, device, None, None, dim)
     rows, hq, _ = q.shape
     b, cu, ctx = _batch(cache, cu_rows, ctx_len)
     kv = 0 if kv_len is None else _i32(kv_len, "kv_len", b, device)
     if out is None:
-        out = _empty((rows, hq, dim), q, stream)
-    os_ = _rows(out, "out", dtype, device, rows, hq, dim)
+        out = _empty((rows, hq, dim), dtype, q, stream)
+        os_ = out.data_ptr(), hq * dim, dim
+    else:
+        os_ = _rows(out, "out", dtype, device, rows, hq, dim)
     ls = _NONE
     if lse is not None:
         if lse.dtype is not torch.float32 or lse.get_device() != device or tuple(lse.shape) != (rows, hq):
@@ -287,19 +299,17 @@ def attention(cache: PagedCache, q, cu_rows, ctx_len, *, kv_len=None, causal: bo
                              f"on {lse.device}")
         ls = (lse.data_ptr(), lse.stride(0), lse.stride(1))
     lib = load()
-    need = lib.dflash_paged_attention_workspace(cache._c, rows, b, hq)
     if workspace is None:
-        if stream is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        else:
-            with torch.cuda.stream(stream):
-                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        nbytes = lib.dflash_paged_attention_workspace(cache._c, rows, b, hq)
+        workspace = _empty(nbytes, torch.uint8, q, stream)
     elif workspace.dtype is not torch.uint8 or workspace.get_device() != device or not workspace.is_contiguous():
         raise ValueError(f"workspace: expected contiguous uint8 on cuda:{device}, got {workspace.dtype} on "
                          f"{workspace.device}")
-    args = _ATTENTION.pack(*qs, *os_, *ls, cu, ctx, kv, workspace.data_ptr(), workspace.numel(), rows, b, hq,
-                           int(causal), window, dim ** -0.5 if scale is None else scale)
-    code = lib.dflash_paged_attention(cache._c, args, _raw_stream(stream, device))
+    else:
+        nbytes = workspace.numel()
+    args = _ATTENTION.pack(*qs, *os_, *ls, cu, ctx, kv, workspace.data_ptr(), nbytes, rows, b, hq, bool(causal), window,
+                           dim ** -0.5 if scale is None else scale)
+    code = lib.dflash_paged_attention(cache._c, args, raw)
     if code:
         raise DflashError("dflash_paged_attention", code)
     return out

@@ -246,6 +246,22 @@ def test_attention_of_many_sequences(ops):
     check_attention(ops, (4, 2, 64), rows, ctx, BF16, page=16)
 
 
+def test_attention_runs_of_many_small_items_end_alike(ops):
+    """Several short items a CTA, most of an M tile's warps without a row: 300
+    calls back to back give the first one's output and no wait runs out."""
+    rows, ctx = [(i * 7) % 5 for i in range(300)], [(i * 37) % 400 for i in range(300)]
+    pg, q, out = check_attention(ops, (4, 2, 64), rows, ctx, BF16, page=16)
+    cu = i32([sum(rows[:i]) for i in range(301)])
+    for _ in range(300):
+        got = ops.attention(pg.cache, q, cu, i32(ctx))
+    assert torch.equal(got, out) and pg.cache.read_status() == 0
+    pg, q, out = check_attention(ops, (8, 2, 128), [40] * 60, [300] * 60, F16)  # two M tiles an item
+    cu = i32([40 * i for i in range(61)])
+    for _ in range(100):
+        got = ops.attention(pg.cache, q, cu, i32([300] * 60))
+    assert torch.equal(got, out) and pg.cache.read_status() == 0
+
+
 def test_attention_of_nothing(ops):
     pg = Paged(ops, [5], 2, 64, 64, BF16)
     out = ops.attention(pg.cache, torch.zeros(0, 4, 64, dtype=BF16, device="cuda"), i32([0, 0]), i32([5]))
