@@ -79,6 +79,71 @@ constexpr size_t ws_records(int grid) { return 256 + ((size_t)grid * sizeof(WsCt
 // One slot: O [D/4][rows] float4, running maxima [rows], sums [rows].
 constexpr size_t ws_slot_floats(int rows, int D) { return (size_t)rows * (D + 2); }  // a multiple of 4
 
+
+// The MMAs of a whole tile under one elect.sync: with one for each MMA the
+// issuing warp is what the tensor core waits for.
+// S = Q K^T, K = D: both operands in 64-dim panels 16 KB apart, 16 dims = 32 bytes a step.
+template <int D>
+DFL_DEV void tc_mma_s(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc) {
+  if constexpr (D == 128)
+    asm volatile(
+          "{\n\t.reg .pred e, p, t;\n\t.reg .b64 a, b;\n\t.reg .b32 c;\n\t"
+          "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+          "add.s64 a, %1, 0;\n\tadd.s64 b, %2, 0;\n\t"
+          "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t"
+          "add.s64 a, %1, 2;\n\tadd.s64 b, %2, 2;\n\t"
+          "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+          "add.s64 a, %1, 4;\n\tadd.s64 b, %2, 4;\n\t"
+          "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+          "add.s64 a, %1, 6;\n\tadd.s64 b, %2, 6;\n\t"
+          "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+          "add.s64 a, %1, 1024;\n\tadd.s64 b, %2, 1024;\n\t"
+          "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+          "add.s64 a, %1, 1026;\n\tadd.s64 b, %2, 1026;\n\t"
+          "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+          "add.s64 a, %1, 1028;\n\tadd.s64 b, %2, 1028;\n\t"
+          "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+          "add.s64 a, %1, 1030;\n\tadd.s64 b, %2, 1030;\n\t"
+          "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t}" ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(0u)
+        : "memory");
+  else
+    asm volatile(
+          "{\n\t.reg .pred e, p, t;\n\t.reg .b64 a, b;\n\t.reg .b32 c;\n\t"
+          "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+          "add.s64 a, %1, 0;\n\tadd.s64 b, %2, 0;\n\t"
+          "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t"
+          "add.s64 a, %1, 2;\n\tadd.s64 b, %2, 2;\n\t"
+          "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+          "add.s64 a, %1, 4;\n\tadd.s64 b, %2, 4;\n\t"
+          "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+          "add.s64 a, %1, 6;\n\tadd.s64 b, %2, 6;\n\t"
+          "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t}" ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(0u)
+        : "memory");
+}
+// O (+)= P V, K = 128 keys: P in TMEM, 8 columns a step, V 16 keys = 2 KB a step.
+DFL_DEV void tc_mma_o(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accum) {
+  asm volatile(
+          "{\n\t.reg .pred e, p, t;\n\t.reg .b64 a, b;\n\t.reg .b32 c;\n\t"
+          "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+          "add.u32 c, %1, 0;\n\tadd.s64 b, %2, 0;\n\t"
+          "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [c], b, %3, p;\n\t"
+          "add.u32 c, %1, 8;\n\tadd.s64 b, %2, 128;\n\t"
+          "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [c], b, %3, t;\n\t"
+          "add.u32 c, %1, 16;\n\tadd.s64 b, %2, 256;\n\t"
+          "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [c], b, %3, t;\n\t"
+          "add.u32 c, %1, 24;\n\tadd.s64 b, %2, 384;\n\t"
+          "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [c], b, %3, t;\n\t"
+          "add.u32 c, %1, 32;\n\tadd.s64 b, %2, 512;\n\t"
+          "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [c], b, %3, t;\n\t"
+          "add.u32 c, %1, 40;\n\tadd.s64 b, %2, 640;\n\t"
+          "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [c], b, %3, t;\n\t"
+          "add.u32 c, %1, 48;\n\tadd.s64 b, %2, 768;\n\t"
+          "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [c], b, %3, t;\n\t"
+          "add.u32 c, %1, 56;\n\tadd.s64 b, %2, 896;\n\t"
+          "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [c], b, %3, t;\n\t}" ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accum)
+      : "memory");
+}
+
 template <int D, int NM>
 struct PCfg {
   static constexpr int ROWS = 128 * NM;
@@ -182,6 +247,16 @@ DFL_DEV uint64_t sdesc_sw128_mn(uint32_t saddr, uint32_t panel) {
   return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(panel >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
          ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
+
+// A place in the ring of tiles: slot and phase.
+template <int SLOTS>
+struct Ring {
+  int s = 0;
+  uint32_t phase = 0;
+  DFL_DEV void next() {
+    if (++s == SLOTS) s = 0, phase ^= 1u;
+  }
+};
 
 // A sequence as the kernel sees it; lengths outside the batch's rows or the
 // table are cut to them.
@@ -378,15 +453,14 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
   uint64_t* empty = full + C::SLOTS;    // [SLOTS] tile's MMAs done
   uint64_t* s_full = empty + C::SLOTS;  // [2] S (and every MMA before it) done
   uint64_t* p_full = s_full + 2;        // [2] P written
-  uint64_t* p_half = p_full + 2;        // [2] the first 64 keys of P written
-  uint64_t* o_done = p_half + 2;        // [2] an O MMA done: of M tile m, or (NM = 1) of tiles of one parity
+  uint64_t* o_done = p_full + 2;        // [2] an O MMA done: of M tile m, or (NM = 1) of tiles of one parity
   uint64_t* o_empty = o_done + 2;       // [2] O read out
   uint64_t* q_full = o_empty + 2;       // [QBUFS]
   uint64_t* q_empty = q_full + 2;
   uint64_t* mdone = q_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mdone + 1);
   Sched* sched = reinterpret_cast<Sched*>(sm + C::OFF_BAR + 320);
-  static_assert((2 * C::SLOTS + 15) * 8 + 8 <= 320 && sizeof(Sched) <= 192, "barrier area");
+  static_assert((2 * C::SLOTS + 13) * 8 + 8 <= 320 && sizeof(Sched) <= 192, "barrier area");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int MMA_WARP = 4 * NM, LOAD_WARP = 4 * NM + 1;
@@ -398,7 +472,6 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full + i, 1);
       mbar_init(p_full + i, 4);
-      mbar_init(p_half + i, 4);
       mbar_init(o_done + i, 1);
       mbar_init(o_empty + i, 4);
     }
@@ -459,7 +532,8 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
     const int page = 1 << p.shift, box = min(page, KT), boxes = KT / box;
     const int bi = lane % boxes, bh = lane / boxes;  // this lane's box, if bh is a panel
     int seg = 0;
-    long long nt = 0;  // ring slots filled
+    Ring<C::SLOTS> at;
+    bool lap = false;  // the ring has been filled once
     bool ok = true;
     do {
       const int tiles = w.n;
@@ -497,9 +571,9 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
           }
         }
         const int id = __shfl_sync(0xffffffffu, ids, e0 + bi - base);
-        for (int kv = 0; kv < 2; ++kv, ++nt) {  // K, then V
-          const int s = (int)(nt % C::SLOTS);
-          if (nt >= C::SLOTS && !wait_all(empty + s, (uint32_t)((nt / C::SLOTS - 1) & 1))) {
+        for (int kv = 0; kv < 2; ++kv) {  // K, then V
+          const int s = at.s;
+          if (lap && !wait_all(empty + s, at.phase ^ 1u)) {
             ok = false;
             break;
           }
@@ -508,15 +582,18 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
           if (bh < D / 64)
             tma_load_4d(sm + C::OFF_RING + s * C::TILE + bh * C::PANEL + bi * box * 128, kv ? &vmap : &kmap, full + s,
                         64 * bh, page > KT ? key0 & (page - 1) : 0, w.kvh, id);
+          at.next();
+          lap = lap || at.s == 0;
         }
         // one Q buffer: its load waits for the last item's S, the first tiles do not
         if (C::QBUFS == 1 && j == 0 && ok) ok = load_q();
       }
     } while (ok && walk_next<NM>(p, w));
     // every copy lands before the CTA may exit
-    for (long long i = nt > C::SLOTS ? nt - C::SLOTS : 0; i < nt; ++i) {
+    for (int i = lap ? 0 : C::SLOTS - at.s; i < C::SLOTS; ++i) {  // from the oldest slot on
+      const int s = lap ? (at.s + i) % C::SLOTS : i - (C::SLOTS - at.s);
       bool drain = false;
-      mbar_wait(full + i % C::SLOTS, (uint32_t)((i / C::SLOTS) & 1), p.status, &drain);
+      mbar_wait(full + s, s < at.s ? at.phase : at.phase ^ 1u, p.status, &drain);
     }
     for (int i = seg > C::QBUFS ? seg - C::QBUFS : 0; i < seg; ++i) {
       bool drain = false;
@@ -524,95 +601,95 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
     }
   } else if (warp == MMA_WARP) {
     // ------------------------------------------------ MMA issue (converged warp, one elected lane)
+    // This warp's scalar work between two MMAs is what the tensor core waits
+    // for: slots and phases are counted, not divided out, and descriptors added up.
     const uint32_t idesc_s = idesc_f16_f32(128, KT, BF16 ? 1 : 0);
     const uint32_t idesc_o = idesc_f16_f32(128, D, BF16 ? 1 : 0) | (1u << 16);  // V is N-major
+    const uint64_t q_desc = sdesc_sw128(smem_u32(sm)), k_desc = sdesc_sw128(smem_u32(sm + C::OFF_RING));
+    const uint64_t v_desc = sdesc_sw128_mn(smem_u32(sm + C::OFF_RING), C::PANEL);
     int seg = 0;
-    long long nt = 0;          // ring slots used
-    int it[2] = {0, 0};        // S tiles issued for each M tile
-    int sg[2] = {0, 0};        // segments of each M tile
-    int qb = 0;
-    auto issue_s = [&](int m, long long slot) {
-      const uint32_t qa = smem_u32(sm + (qb * NM + m) * C::TILE), ka = smem_u32(sm + C::OFF_RING + (int)(slot % C::SLOTS) * C::TILE);
-      const int buf = NM == 2 ? m : it[0] & 1;
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t o = (uint32_t)((kk >> 2) * C::PANEL);
-        tc_mma_f16_elect(tmem + (uint32_t)(C::S_COL + 128 * buf), sdesc_sw128(qa + o) + (uint64_t)(2 * (kk & 3)),
-                         sdesc_sw128(ka + o) + (uint64_t)(2 * (kk & 3)), idesc_s, kk > 0 ? 1u : 0u);
-      }
+    Ring<C::SLOTS> kr, vr;  // the next tile of K and of V
+    vr.next();
+    uint32_t p_phase = 0;        // bit b: phase of the next P of S buffer b
+    int it = 0;                  // NM = 1: S tiles issued
+    int sg[2] = {0, 0};          // segments of each M tile
+    auto issue_s = [&](int m, int buf, int qb, int slot) {
+      const uint64_t qd = q_desc + (uint64_t)((qb * NM + m) * (C::TILE >> 4)), kd = k_desc + (uint64_t)(slot * (C::TILE >> 4));
+      tc_mma_s<D>(tmem + (uint32_t)(C::S_COL + 128 * buf), qd, kd, idesc_s);
       tc_commit_elect(s_full + buf);
-      ++it[m];
     };
     bool ok = true;
     do {
       const int tiles = w.n;
       if (tiles == 0) continue;
       const int nm = NM == 2 && w.t0 + p.tok < w.t1 ? 2 : 1;
-      auto wait_full = [&](long long slot) { return wait_all(full + slot % C::SLOTS, (uint32_t)((slot / C::SLOTS) & 1)); };
-      // S of tile j for every M tile (NM = 2: after its O MMA of tile j - 1)
-      qb = seg % C::QBUFS;
-      if (!wait_all(q_full + qb, (uint32_t)((seg / C::QBUFS) & 1)) || !wait_full(nt)) break;
+      const int qb = seg % C::QBUFS;
+      if (!wait_all(q_full + qb, (uint32_t)((seg / C::QBUFS) & 1)) || !wait_all(full + kr.s, kr.phase)) break;
       ++seg;
       tc_fence_after();
-      for (int m = 0; m < nm; ++m) issue_s(m, nt);
-      tc_commit_elect(empty + nt % C::SLOTS);
+      // S of the first tile.  NM = 2: S of a tile follows the O MMA of the one
+      // before, whose P it overwrites; NM = 1: it runs ahead of it, into the other buffer.
+      for (int m = 0; m < nm; ++m) issue_s(m, NM == 2 ? m : it & 1, qb, kr.s);
+      ++it;
+      tc_commit_elect(empty + kr.s);
+      kr.next();
+      kr.next();
       if (tiles == 1) tc_commit_elect(q_empty + qb);
-      for (int j = 0; j < tiles && ok; ++j, nt += 2) {
-        const long long vs = nt + 1, ks = nt + 2;
-        if (NM == 1 && j + 1 < tiles) {  // two S buffers: the next S runs beside this tile's softmax
-          if (!(ok = wait_full(ks))) break;
+      // keys of the sequence behind the start of its last tile, if that tile ends inside a page
+      const int last_v = w.s.kv - (w.span.tile0 + w.off + tiles - 1) * KT;
+      for (int j = 0; j < tiles && ok; ++j) {
+        const bool more = j + 1 < tiles;
+        const int buf1 = NM == 1 ? it - 1 & 1 : 0;
+        if (NM == 1 && more) {
+          if (!(ok = wait_all(full + kr.s, kr.phase))) break;
           tc_fence_after();
-          issue_s(0, ks);
-          tc_commit_elect(empty + ks % C::SLOTS);
+          issue_s(0, it & 1, qb, kr.s);
+          ++it;
+          tc_commit_elect(empty + kr.s);
+          kr.next();
+          kr.next();
           if (j + 2 == tiles) tc_commit_elect(q_empty + qb);
         }
+        if (!(ok = wait_all(full + vr.s, vr.phase))) break;
+        if (!more && last_v < KT && (last_v & ((1 << p.shift) - 1))) {
+          // the sequence ends inside a page: what lies behind it (stale,
+          // perhaps not finite) must not meet P's zeros in the MMA
+          const int v1 = min(KT, ((last_v >> p.shift) + 1) << p.shift);
+          uint8_t* vt = sm + C::OFF_RING + vr.s * C::TILE;
+          for (int i = lane; i < (v1 - last_v) * 8; i += 32)
+            for (int h = 0; h < D / 64; ++h)
+              *reinterpret_cast<uint4*>(vt + h * C::PANEL + (last_v + (i >> 3)) * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        // the next tile's K is looked for while P is awaited
+        const bool k_here = NM == 2 && more && __all_sync(0xffffffffu, mbar_try_wait(full + kr.s, kr.phase));
+        const uint64_t vd = v_desc + (uint64_t)(vr.s * (C::TILE >> 4));
         for (int m = 0; m < nm; ++m) {
-          const int done = NM == 2 ? it[m] - 1 : it[0] - 1 - (j + 1 < tiles);  // the S tile whose P is next
-          const int buf = NM == 2 ? m : done & 1;
-          if (m == 0) {
-            if (!(ok = wait_full(vs))) break;
-            const int key0 = (w.span.tile0 + w.off + j) * KT;
-            const int v0 = w.s.kv - key0;
-            if (v0 < KT && (v0 & ((1 << p.shift) - 1))) {
-              // the sequence ends inside a page: what lies behind it (stale,
-              // perhaps not finite) must not meet P's zeros in the MMA
-              const int v1 = min(KT, ((v0 >> p.shift) + 1) << p.shift);
-              uint8_t* vt = sm + C::OFF_RING + (int)(vs % C::SLOTS) * C::TILE;
-              for (int i = lane; i < (v1 - v0) * 8; i += 32)
-                for (int h = 0; h < D / 64; ++h)
-                  *reinterpret_cast<uint4*>(vt + h * C::PANEL + (v0 + (i >> 3)) * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
-              fence_proxy_async_smem();
-              __syncwarp();
-            }
-            tc_fence_after();
-          }
+          const int buf = NM == 2 ? m : buf1;
           if (j == 0 && sg[m]++ > 0 && !(ok = wait_all(o_empty + m, (uint32_t)((sg[m] - 2) & 1)))) break;
-          const uint32_t par = (uint32_t)((NM == 2 ? done : done >> 1) & 1);
-          const uint32_t va = smem_u32(sm + C::OFF_RING + (int)(vs % C::SLOTS) * C::TILE);
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            if (!(ok = wait_all((half ? p_full : p_half) + buf, par))) break;
-            tc_fence_after();
-#pragma unroll
-            for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-              tc_mma_f16_ts_elect(tmem + (uint32_t)(C::O_COL + D * m), tmem + (uint32_t)(C::S_COL + 128 * buf + 8 * kk),
-                                  sdesc_sw128_mn(va + 2048u * kk, C::PANEL), idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
-          }
-          if (!ok) break;
+          if (!(ok = wait_all(p_full + buf, p_phase >> buf & 1u))) break;
+          tc_fence_after();
+          tc_mma_o(tmem + (uint32_t)(C::O_COL + D * m), tmem + (uint32_t)(C::S_COL + 128 * buf), vd, idesc_o, j > 0 ? 1u : 0u);
+          p_phase ^= 1u << buf;
           tc_commit_elect(o_done + buf);
-          if (m == nm - 1) tc_commit_elect(empty + vs % C::SLOTS);
-          if (NM == 2 && j + 1 < tiles) {
+          if (m == nm - 1) tc_commit_elect(empty + vr.s);
+          if (NM == 2 && more) {
             if (m == 0) {
-              if (!(ok = wait_full(ks))) break;
+              if (!k_here && !(ok = wait_all(full + kr.s, kr.phase))) break;
               tc_fence_after();
             }
-            issue_s(m, ks);
+            issue_s(m, m, qb, kr.s);
             if (m == nm - 1) {
-              tc_commit_elect(empty + ks % C::SLOTS);
+              tc_commit_elect(empty + kr.s);
+              kr.next();
+              kr.next();
               if (j + 2 == tiles) tc_commit_elect(q_empty + qb);
             }
           }
         }
+        vr.next();
+        vr.next();
       }
     } while (ok && walk_next<NM>(p, w));
     // every issued MMA completes before the columns are freed
@@ -754,19 +831,11 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
             tmem_wait_ld();
             if (c + 64 < KT) tmem_ld32_nowait(s_base + c + 64, x);
             weigh(y, c + 32);
-            if (c == 0) {  // the first half of P: its O MMAs may begin
-              tmem_wait_st();
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(p_half + buf);
-            }
           }
           float a, b;
           unpack_f32x2(add_f32x2(sum0, sum1), a, b);
           l_run += a + b;
           tmem_wait_st();
-        } else if (lane == 0) {
-          mbar_arrive(p_half + buf);
         }
         tc_fence_before();
         __syncwarp();
