@@ -12,7 +12,9 @@
 // serve all of its heads.  A thread moves two 16-byte vectors of one head at a
 // time: the two halves of 8 pairs, or 16 adjacent dims, so a pair never
 // crosses threads and an output may be its own input.
+#include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -80,12 +82,14 @@ DFL_DEV uint16_t pack1(float a) {
   }
 }
 
-constexpr int ROPE_MAX_ROWS = 4;  // rows of a CTA
-constexpr int ROPE_THREADS = 256;
+constexpr int ROPE_MAX_ROWS = 8;   // rows of a CTA
+constexpr int ROPE_THREADS = 256;  // at most
+constexpr int ROPE_AHEAD = 2;      // units of a thread whose loads are in flight at once
 
 struct RowPlace {
   int valid;            // 0: padding row
   int write;            // its page exists
+  int seq;
   long long pos;
   long long off[2];     // element offset of its place in the k and v pools
 };
@@ -97,49 +101,13 @@ __global__ void __launch_bounds__(ROPE_THREADS) k_rope(const __grid_constant__ R
   __shared__ __align__(16) float2 cs[ROPE_MAX_ROWS][DFLASH_ROPE_MAX_PAIRS];
   const int row0 = blockIdx.x * p.rows_per_cta;
   const int nr = min(p.rows_per_cta, p.rows - row0);
-  pdl_launch_dependents();
-  pdl_wait();
-  if (APPEND) {
-    if (threadIdx.x < nr) place[threadIdx.x].valid = 0;
-    __syncthreads();
-    // the row's sequence: the thread whose sequence holds it writes its place
-    for (int b = threadIdx.x; b < p.batch; b += blockDim.x) {
-      const int lo = p.cu[b], hi = p.cu[b + 1];
-      for (int r = 0; r < nr; ++r) {
-        const int t = row0 + r;
-        if (t < lo || t >= hi) continue;
-        RowPlace& w = place[r];
-        w.valid = 1;
-        w.pos = (long long)p.ctx[b] + (t - lo);
-        const long long pi = w.pos >> p.page_shift;
-        const int pg = w.pos >= 0 && pi < p.max_pages ? p.table[b * p.table_stride + pi] : -1;
-        w.write = pg >= 0 && pg < p.n_pages;
-        if (!w.write) dev_error(p.status, DFLASH_DEV_PAGE);
-        const long long in_page = w.pos & ((1 << p.page_shift) - 1);
-        w.off[0] = w.write ? pg * p.page_stride[0] + in_page * p.pool[0].row : 0;
-        w.off[1] = w.write ? pg * p.page_stride[1] + in_page * p.pool[1].row : 0;
-      }
-    }
-    __syncthreads();
-  }
-  const int pairs = p.rd >> 1;
-  for (int i = threadIdx.x; i < nr * pairs; i += blockDim.x) {
-    const int r = i / pairs, c = i - r * pairs;
-    const long long pos = APPEND ? (place[r].valid ? place[r].pos : 0) : (long long)p.positions[row0 + r];
-    const uint64_t turns = (uint64_t)pos * p.turn[c];
-    float s, co;
-    sincospif((float)(int32_t)(uint32_t)(turns >> 32) * 0x1p-31f, &s, &co);
-    cs[r][c] = make_float2(co * p.amplitude, (p.backward ? -s : s) * p.amplitude);
-  }
-  __syncthreads();
-
-  const int U = VEC ? p.D >> 4 : p.D >> 1;   // units of a head
-  const int c = threadIdx.x % U;             // blockDim is a multiple of U
+  const int U = VEC ? p.D >> 4 : p.D >> 1;      // units of a head
+  const int c = threadIdx.x % U;                // blockDim is a multiple of U
   const int H = p.heads[0] + p.heads[1] + (APPEND ? p.heads[2] : 0);
   const int step = blockDim.x / U;
   const int rot = VEC ? p.rd >> 4 : p.rd >> 1;  // rotated units of a head
   const bool turned = c < rot;
-  // first element of the unit's two parts, and its first pair
+  // first element of the unit's two parts
   int e0, e1;
   if (VEC) {
     if (p.interleaved) e0 = 16 * c, e1 = e0 + 8;
@@ -150,27 +118,95 @@ __global__ void __launch_bounds__(ROPE_THREADS) k_rope(const __grid_constant__ R
     else if (turned) e0 = c, e1 = e0 + (p.rd >> 1);
     else e0 = p.rd + 2 * (c - rot), e1 = e0 + 1;
   }
-  for (int it = threadIdx.x / U; it < nr * H; it += step) {
-    const int r = it / H;
-    int h = it - r * H;
-    if (APPEND && !place[r].valid) continue;
-    const int which = h < p.heads[0] ? 0 : h < p.heads[0] + p.heads[1] ? 1 : 2;
-    h -= which == 0 ? 0 : which == 1 ? p.heads[0] : p.heads[0] + p.heads[1];
-    const long long t = row0 + r;
-    const uint16_t* src = p.in[which].src + t * p.in[which].row + h * p.in[which].head;
-    uint16_t* dst;
-    if (APPEND && which > 0) {
-      if (!place[r].write) continue;
-      dst = p.pool[which - 1].dst + place[r].off[which - 1] + h * p.pool[which - 1].head;
-    } else {
-      dst = p.out[which].dst + t * p.out[which].row + h * p.out[which].head;
+  using Part = typename std::conditional<VEC, uint4, uint16_t>::type;
+  struct Unit {
+    Part a, b;
+    int r, which, h;  // row of the CTA (-1: none), tensor, head
+  };
+  auto load = [&](Unit& u, int it) {
+    u.r = it < nr * H ? it / H : -1;
+    if (u.r < 0) return;
+    u.h = it - u.r * H;
+    u.which = u.h < p.heads[0] ? 0 : u.h < p.heads[0] + p.heads[1] ? 1 : 2;
+    u.h -= u.which == 0 ? 0 : u.which == 1 ? p.heads[0] : p.heads[0] + p.heads[1];
+    const RowsIn& in = p.in[u.which];
+    const uint16_t* src = in.src + (long long)(row0 + u.r) * in.row + u.h * in.head;
+    u.a = *reinterpret_cast<const Part*>(src + e0);
+    u.b = *reinterpret_cast<const Part*>(src + e1);
+  };
+  pdl_launch_dependents();
+  pdl_wait();
+  // the first units' loads need no position: they are on their way while the
+  // row's place and angles are found
+  Unit unit[ROPE_AHEAD];
+  int it = threadIdx.x / U;
+#pragma unroll
+  for (int i = 0; i < ROPE_AHEAD; ++i) load(unit[i], it + i * step);
+  if (APPEND) {
+    // a warp finds a row's sequence and position; its page is looked up while
+    // the angles are computed
+    const int lane = threadIdx.x & 31, warps = (blockDim.x + 31) >> 5;
+    for (int r = threadIdx.x >> 5; r < nr; r += warps) {
+      const int t = row0 + r;
+      const uint32_t here = __activemask();  // the last warp may not be full
+      const int width = __popc(here);
+      RowPlace w = {};
+      for (int b0 = 0; b0 < p.batch; b0 += width) {
+        const int b = b0 + lane;
+        const bool in = b < p.batch;
+        const int lo = in ? p.cu[b] : 0, hi = in ? p.cu[b + 1] : 0, ctx = in ? p.ctx[b] : 0;
+        const uint32_t found = __ballot_sync(here, in && t >= lo && t < hi);
+        if (!found) continue;
+        if (lane == __ffs(found) - 1) {
+          w.valid = 1;
+          w.seq = b;
+          w.pos = (long long)ctx + (t - lo);
+          place[r] = w;
+        }
+        w.valid = 1;
+        break;
+      }
+      if (!w.valid && lane == 0) place[r] = w;
     }
-    const bool rotate = turned && which < 2;
-    if (VEC) {
-      uint4 a = *reinterpret_cast<const uint4*>(src + e0), b = *reinterpret_cast<const uint4*>(src + e1);
-      if (rotate) {
-        uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
-        const float4* w4 = reinterpret_cast<const float4*>(&cs[r][8 * c]);
+    __syncthreads();
+    if (threadIdx.x < nr && place[threadIdx.x].valid) {
+      RowPlace& w = place[threadIdx.x];
+      const long long pi = w.pos >> p.page_shift;
+      const int pg = w.pos >= 0 && pi < p.max_pages ? p.table[w.seq * p.table_stride + pi] : -1;
+      if (pg >= 0 && pg < p.n_pages) {
+        const long long in_page = w.pos & ((1 << p.page_shift) - 1);
+        w.write = 1;
+        w.off[0] = pg * p.page_stride[0] + in_page * p.pool[0].row;
+        w.off[1] = pg * p.page_stride[1] + in_page * p.pool[1].row;
+      } else {
+        dev_error(p.status, DFLASH_DEV_PAGE);
+      }
+    }
+  }
+  const int pairs = p.rd >> 1;
+  for (int i = threadIdx.x; i < nr * pairs; i += blockDim.x) {
+    const int r = i / pairs, j = i - r * pairs;
+    const long long pos = APPEND ? (place[r].valid ? place[r].pos : 0) : (long long)p.positions[row0 + r];
+    const uint64_t turns = (uint64_t)pos * p.turn[j];
+    float s, co;
+    sincospif((float)(int32_t)(uint32_t)(turns >> 32) * 0x1p-31f, &s, &co);
+    cs[r][j] = make_float2(co * p.amplitude, (p.backward ? -s : s) * p.amplitude);
+  }
+  __syncthreads();
+
+  auto finish = [&](Unit& u) {
+    if (u.r < 0 || (APPEND && !place[u.r].valid)) return;
+    uint16_t* dst;
+    if (APPEND && u.which > 0) {
+      if (!place[u.r].write) return;
+      dst = p.pool[u.which - 1].dst + place[u.r].off[u.which - 1] + u.h * p.pool[u.which - 1].head;
+    } else {
+      dst = p.out[u.which].dst + (long long)(row0 + u.r) * p.out[u.which].row + u.h * p.out[u.which].head;
+    }
+    if (turned && u.which < 2) {
+      if constexpr (VEC) {
+        uint32_t x[4] = {u.a.x, u.a.y, u.a.z, u.a.w}, y[4] = {u.b.x, u.b.y, u.b.z, u.b.w};
+        const float4* w4 = reinterpret_cast<const float4*>(&cs[u.r][8 * c]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float4 w = w4[i];  // two pairs' (cos, sin)
@@ -186,22 +222,25 @@ __global__ void __launch_bounds__(ROPE_THREADS) k_rope(const __grid_constant__ R
             y[i] = pack2<BF16>(fa.x * w.y + fb.x * w.x, fa.y * w.w + fb.y * w.z);
           }
         }
-        a = make_uint4(x[0], x[1], x[2], x[3]);
-        b = make_uint4(y[0], y[1], y[2], y[3]);
+        u.a = make_uint4(x[0], x[1], x[2], x[3]);
+        u.b = make_uint4(y[0], y[1], y[2], y[3]);
+      } else {
+        const float2 w = cs[u.r][c];
+        const float fa = unpack1<BF16>(u.a), fb = unpack1<BF16>(u.b);
+        u.a = pack1<BF16>(fa * w.x - fb * w.y);
+        u.b = pack1<BF16>(fa * w.y + fb * w.x);
       }
-      *reinterpret_cast<uint4*>(dst + e0) = a;
-      *reinterpret_cast<uint4*>(dst + e1) = b;
-    } else {
-      uint16_t a = src[e0], b = src[e1];
-      if (rotate) {
-        const float2 w = cs[r][c];
-        const float fa = unpack1<BF16>(a), fb = unpack1<BF16>(b);
-        a = pack1<BF16>(fa * w.x - fb * w.y);
-        b = pack1<BF16>(fa * w.y + fb * w.x);
-      }
-      dst[e0] = a;
-      dst[e1] = b;
     }
+    *reinterpret_cast<Part*>(dst + e0) = u.a;
+    *reinterpret_cast<Part*>(dst + e1) = u.b;
+  };
+  for (;;) {
+#pragma unroll
+    for (int i = 0; i < ROPE_AHEAD; ++i) finish(unit[i]);
+    it += ROPE_AHEAD * step;
+    if (it >= nr * H) break;
+#pragma unroll
+    for (int i = 0; i < ROPE_AHEAD; ++i) load(unit[i], it + i * step);
   }
 }
 
@@ -209,12 +248,16 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 
 template <bool APPEND>
 int launch_rope(RopeParams& p, bool bf16_, bool vec, cudaStream_t s) {
+  // One row a CTA, its heads ROPE_AHEAD units a thread if that fits; rows with
+  // few heads share a CTA.
   const int U = vec ? p.D / 16 : p.D / 2;
-  // a CTA of 4 rows once that still gives every SM eight CTAs, else one row
-  p.rows_per_cta = p.rows >= 8 * 152 * ROPE_MAX_ROWS ? ROPE_MAX_ROWS : 1;
+  const int H = p.heads[0] + p.heads[1] + p.heads[2], per = ROPE_THREADS / U;  // heads a pass, at most
+  p.rows_per_cta = std::max(1, std::min(ROPE_MAX_ROWS, ROPE_AHEAD * per / std::max(H, 1)));
+  const int items = p.rows_per_cta * H;
+  const int lanes = std::min(per, std::max((items + ROPE_AHEAD - 1) / ROPE_AHEAD, (64 + U - 1) / U));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((p.rows + p.rows_per_cta - 1) / p.rows_per_cta));
-  cfg.blockDim = dim3((unsigned)(U * (ROPE_THREADS / U)));
+  cfg.blockDim = dim3((unsigned)(U * lanes));
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -431,7 +431,7 @@ DFLASH_API int dflash_harness_verify(dflash_handle* h, const int32_t* slots, int
  * A batch is ragged: row t of q/k/v belongs to the sequence b with
  * cu_rows[b] <= t < cu_rows[b+1] (DEVICE int32 [batch+1], non-decreasing, from
  * 0); its position is ctx_len[b] + t - cu_rows[b].  Rows from cu_rows[batch]
- * on are padding: nothing is read or written for them.  Values are f16 or
+ * on are padding: what they hold does not matter and nothing is written for them.  Values are f16 or
  * bf16, one type for all tensors of a call.  A tensor of rows is given by its
  * pointer and the strides, in elements, of its rows and heads; the head
  * dimension is contiguous.  `device` is the ordinal that every pointer and
