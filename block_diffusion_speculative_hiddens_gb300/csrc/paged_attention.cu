@@ -23,7 +23,9 @@
 // The tensor core runs the MMAs in issue order, so S of the next tile may
 // overwrite the P that the O MMA before it read.
 // Warps: 4 NM softmax, one issuing MMAs, one loading.
+#include <algorithm>
 #include <atomic>
+#include <mutex>
 
 #include "common.cuh"
 #include "internal.h"
@@ -61,6 +63,7 @@ struct PagedParams {
   int negate;         // the caller's scale is negative
   uint32_t* status;
   char* ws;
+  int cs;             // > 0: an item a cluster of cs CTAs, its shares joined over distributed shared memory
 };
 
 // Workspace: a header, one record a CTA, two partial slots a CTA.
@@ -441,6 +444,96 @@ DFL_DEV bool locate(const PagedParams& p, Sched* sc, Seq* seqs, int* first, Walk
   return true;
 }
 
+// The item of this CTA's cluster and its share of the item's tiles.
+DFL_DEV bool locate_cluster(const PagedParams& p, Sched* sc, Walk& w) {
+  const int item = blockIdx.x / p.cs, rank = blockIdx.x - item * p.cs;
+  int pair = item / p.hkv;
+  w.kvh = item - pair * p.hkv;
+  w.b = 0;
+  if (p.batch > 1) {
+    int before = 0;
+    if (threadIdx.x == 0) sc->b = -1;
+    for (int b0 = 0; b0 < p.batch; b0 += blockDim.x) {
+      const int b = b0 + threadIdx.x;
+      const int m = b < p.batch ? (load_seq(p, b).n + p.tok - 1) / p.tok : 0;
+      long long all;
+      const int at = before + (int)cta_scan(m, sc->part, &all);  // its barriers order the write above
+      if (pair < at && pair >= at - m) {
+        sc->b = b;
+        sc->mt = pair - (at - m);
+      }
+      before += (int)all;
+    }
+    __syncthreads();
+    if (sc->b < 0) return false;
+    w.b = sc->b;
+    pair = sc->mt;
+  }
+  w.mt = pair;
+  w.s = load_seq(p, w.b);
+  w.t0 = w.mt * p.tok;
+  w.t1 = min(w.t0 + p.tok, w.s.n);
+  if (w.t0 >= w.t1) return false;
+  w.span = load_span(p, w.s, w.t0, w.t1);
+  w.off = (int)((long long)w.span.tiles * rank / p.cs);
+  w.n = (int)((long long)w.span.tiles * (rank + 1) / p.cs) - w.off;
+  w.out = w.n > 0;
+  w.at = 0;
+  w.left = 0;  // and nothing after it
+  return true;
+}
+
+// Joins the shares that the CTAs of a cluster left in their shared memory:
+// O [128][D + 4] unnormalised, maxima [128], sums [128].  Each takes every
+// cs-th row, with the loads of all shares in flight.
+constexpr int MAX_CLUSTER = 16;
+constexpr long long CLUSTER_TILES = 640;  // key tiles that a call's tables can hold
+template <bool BF16, int D>
+DFL_DEV void join_cluster(const PagedParams& p, const uint8_t* sm, const Walk& w) {
+  constexpr int PS = D + 4;
+  const uint32_t at = smem_u32(sm);
+  const int rank = (int)cluster_ctarank(), rows = (w.t1 - w.t0) * p.group;
+  const int mine = (rows - rank + p.cs - 1) / p.cs;
+  for (int e = threadIdx.x; e < mine * (D / 4); e += blockDim.x) {
+    const int r = rank + e / (D / 4) * p.cs, d = e % (D / 4) * 4;
+    float m[MAX_CLUSTER], l[MAX_CLUSTER];
+    float4 o[MAX_CLUSTER];
+#pragma unroll
+    for (int x = 0; x < MAX_CLUSTER; ++x) {
+      m[x] = -INFINITY;
+      l[x] = 0.f;
+      o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (x < p.cs) {
+        const uint32_t a = dsmem_addr(at, (uint32_t)x);
+        m[x] = ld_dsmem(a + 4u * (uint32_t)(128 * PS + r));
+        l[x] = ld_dsmem(a + 4u * (uint32_t)(128 * PS + 128 + r));
+        o[x] = ld_dsmem4(a + 4u * (uint32_t)(r * PS + d));
+      }
+    }
+    float M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int x = 0; x < MAX_CLUSTER; ++x)
+      if (l[x] != 0.f) M = fmaxf(M, m[x]);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int x = 0; x < MAX_CLUSTER; ++x) {
+      if (l[x] == 0.f) continue;  // a share without a key of the row, its O not written
+      const float wgt = ex2(m[x] - M);
+      L += wgt * l[x];
+      acc.x += wgt * o[x].x;
+      acc.y += wgt * o[x].y;
+      acc.z += wgt * o[x].z;
+      acc.w += wgt * o[x].w;
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const long long t = w.s.row0 + w.t0 + r / p.group, h = w.kvh * p.group + r % p.group;
+    *reinterpret_cast<uint2*>(p.out + t * p.o_row + h * p.o_head + d) =
+        make_uint2(pack16<BF16>(acc.x * inv, acc.y * inv), pack16<BF16>(acc.z * inv, acc.w * inv));
+    if (p.lse && d == 0)
+      p.lse[t * p.lse_row + h * p.lse_head] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+  }
+}
+
 template <bool BF16, int D, int NM>
 __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
     k_paged_attn(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
@@ -501,8 +594,10 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
   Walk w;
   Runs runs = {0, 0, 0};
   Seq* seqs = reinterpret_cast<Seq*>(sm);
-  const bool work = locate<NM>(p, sched, seqs, reinterpret_cast<int*>(seqs + C::THREADS), w, &runs);
-  if (threadIdx.x == 0) {
+  const bool in_cluster = NM == 1 && p.cs > 0;
+  const bool work = in_cluster ? locate_cluster(p, sched, w)
+                               : locate<NM>(p, sched, seqs, reinterpret_cast<int*>(seqs + C::THREADS), w, &runs);
+  if (threadIdx.x == 0 && !in_cluster) {
     if (blockIdx.x == 0) *reinterpret_cast<Runs*>(p.ws) = runs;
     if (work) {
       WsCta* rec = reinterpret_cast<WsCta*>(p.ws + 256) + blockIdx.x;
@@ -715,7 +810,14 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
     };
     do {
       const int tiles = w.n;
-      if (!w.out) continue;
+      if (!w.out) {
+        if (NM == 1 && in_cluster) {  // no tile of the item: a share without keys
+          float* part = reinterpret_cast<float*>(sm) + 128 * (D + 4);
+          part[r] = -INFINITY;
+          part[128 + r] = 0.f;
+        }
+        continue;
+      }
       const int t = w.t0 + m * p.tok + rt;
       const bool valid = rt < p.tok && t < w.t1;
       if (NM == 2 && m == 1 && w.t0 + p.tok >= w.t1) continue;  // no row in this M tile
@@ -847,8 +949,22 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
         if (!(ok = wait_o(it - 1))) break;
         tc_fence_after();
       }
-      const bool whole = tiles == w.span.tiles;
-      if (warp_valid) {
+      const bool whole = tiles == w.span.tiles && !in_cluster;
+      if (NM == 1 && in_cluster) {  // the tile area is free: every load has been used
+        float* part = reinterpret_cast<float*>(sm);
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32_nowait(o_base + 32 * c, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<uint4*>(part + r * (D + 4) + 32 * c + 4 * e) =
+                make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        }
+        part[128 * (D + 4) + r] = m_run;
+        part[128 * (D + 4) + 128 + r] = l_run;
+      } else if (warp_valid) {
         if (whole) {
           const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
           const long long head = w.kvh * p.group + rh, row = w.s.row0 + t;
@@ -911,6 +1027,11 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
   if (warp == MMA_WARP) {
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+  if (NM == 1 && in_cluster && work) {  // the whole cluster's answer
+    cluster_sync_all();
+    join_cluster<BF16, D>(p, sm, w);
+    cluster_sync_all();  // this CTA's share is there until every other has read it
   }
 }
 
@@ -996,6 +1117,11 @@ __global__ void __launch_bounds__(MERGE_ROWS * D / 4) k_paged_merge(const PagedP
   }
 }
 
+bool shape_ok(const dflash_paged_cache* c, int q_heads) {
+  return (c->head_dim == 64 || c->head_dim == 128) && q_heads >= 1 && q_heads % c->kv_heads == 0 &&
+         q_heads / c->kv_heads <= 32;
+}
+
 bool rows_ok(const dflash_rows& r) {
   return (reinterpret_cast<uintptr_t>(r.data) & 15) == 0 && r.row_stride % 8 == 0 && r.head_stride % 8 == 0;
 }
@@ -1008,56 +1134,114 @@ size_t workspace_bytes(int grid, int nm, int D) {
   return ws_records(grid) + 2 * (size_t)grid * ws_slot_floats(128 * nm, D) * sizeof(float);
 }
 
-// One CTA an SM: the SMs of a device, 0 if it has none to give.  The kernels'
-// shared-memory limits are set when a device is first asked for.
+// What a device offers, asked once; the kernels' launch limits are set then.
 constexpr int MAX_DEVICES = 64;
-std::atomic<int> g_sms[MAX_DEVICES];
+struct Device {
+  int sms = 0;                    // one CTA an SM
+  int clusters[2 * MAX_CLUSTER] = {};  // clusters of n CTAs it holds at once (n = 2, 4, 8, 16)
+};
+Device g_devices[MAX_DEVICES];
+std::atomic<bool> g_known[MAX_DEVICES];
+std::mutex g_devices_lock;
 
 template <bool BF16, int D, int NM>
-bool allow_smem() {
-  return cudaFuncSetAttribute(k_paged_attn<BF16, D, NM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              PCfg<D, NM>::SMEM) == cudaSuccess;
-}
-template <bool BF16>
-bool allow_all() {
-  return allow_smem<BF16, 64, 1>() && allow_smem<BF16, 64, 2>() && allow_smem<BF16, 128, 1>() && allow_smem<BF16, 128, 2>();
-}
-
-int device_grid(int device) {
-  if (device < 0 || device >= MAX_DEVICES) return 0;
-  int n = g_sms[device].load(std::memory_order_acquire);
-  if (n) return n;
-  DeviceGuard guard(device);
-  if (!guard.ok || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || n < 1 ||
-      !allow_all<true>() || !allow_all<false>()) {
-    cudaGetLastError();
-    return 0;
-  }
-  g_sms[device].store(n, std::memory_order_release);
-  return n;
-}
-
-template <bool BF16, int D, int NM>
-int launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const PagedParams& p, int grid,
-           cudaStream_t s) {
+cudaError_t allow() {
   auto kern = k_paged_attn<BF16, D, NM>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PCfg<D, NM>::SMEM);
+  if (!e && NM == 1) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  return e;
+}
+
+const Device* device_of(int device) {
+  if (device < 0 || device >= MAX_DEVICES) return nullptr;
+  Device& d = g_devices[device];
+  if (g_known[device].load(std::memory_order_acquire)) return &d;
+  std::lock_guard<std::mutex> lock(g_devices_lock);
+  if (g_known[device].load(std::memory_order_acquire)) return &d;
+  DeviceGuard guard(device);
+  if (!guard.ok || cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, device) || d.sms < 1 ||
+      allow<true, 64, 1>() || allow<true, 64, 2>() || allow<true, 128, 1>() || allow<true, 128, 2>() ||
+      allow<false, 64, 1>() || allow<false, 64, 2>() || allow<false, 128, 1>() || allow<false, 128, 2>()) {
+    cudaGetLastError();
+    return nullptr;
+  }
+  for (int n = 2; n <= MAX_CLUSTER; n *= 2) {  // the 128-wide kernel's shared memory is the larger one
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)n);
+    cfg.blockDim = dim3(PCfg<128, 1>::THREADS);
+    cfg.dynamicSmemBytes = PCfg<128, 1>::SMEM;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)n;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&d.clusters[n], k_paged_attn<true, 128, 1>, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      d.clusters[n] = 0;
+    }
+  }
+  g_known[device].store(true, std::memory_order_release);
+  return &d;
+}
+
+// How a call is launched.
+struct Plan {
+  int nm;       // M tiles an item
+  int cs;       // > 0: a cluster of cs CTAs an item
+  int grid;
+  size_t ws;
+};
+// Items to launch a cluster for, at most: a sequence of n rows has ceil(n / tok) token tiles.
+long long max_items(int rows, int batch, int tok, int hkv) {
+  return std::min<long long>(rows, ((long long)rows + (long long)batch * (tok - 1)) / tok) * hkv;
+}
+Plan plan_call(const Device& dev, const dflash_paged_cache* c, int rows, int batch, int q_heads) {
+  const int group = q_heads / c->kv_heads, D = c->head_dim;
+  Plan pl = {m_tiles(rows, batch, group), 0, dev.sms, 0};
+  const long long items = max_items(rows, batch, 128 / group, c->kv_heads);
+  const long long tiles = (((long long)c->max_pages << page_shift(c->page_size)) + KT - 1) / KT;  // of a sequence, at most
+  // Few items over little cache: a cluster each, the largest that lets all run
+  // at once.  That saves the merge's launch, but leaves SMs idle.  Clusters
+  // against runs of equal length (us): a token over 100 positions 8.0 / 10.5,
+  // 16 over 2,048 11.8 / 14.9, a token over 8,192 15.9 / 16.6 (32 and 8 heads
+  // of 128: 8, 136 and 520 tiles); two of 16,000 with 4 KV heads 22.8 / 19.5,
+  // 16 over 32,000 39.9 / 35.6 (1,000 and 2,000 tiles).
+  if (pl.nm == 1 && items * tiles <= CLUSTER_TILES) {
+    int cs = 1;
+    while (cs < MAX_CLUSTER && cs < tiles && items <= dev.clusters[2 * cs]) cs *= 2;
+    if (cs >= 4 || cs >= tiles) {
+      pl.cs = cs;
+      pl.grid = (int)items * cs;
+    }
+  }
+  if (!pl.cs) pl.ws = workspace_bytes(dev.sms, pl.nm, D);
+  return pl;
+}
+
+template <bool BF16, int D, int NM>
+int launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const PagedParams& p, const Plan& pl,
+           cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
+  cfg.gridDim = dim3((unsigned)pl.grid);
   cfg.blockDim = dim3(PCfg<D, NM>::THREADS);
   cfg.dynamicSmemBytes = PCfg<D, NM>::SMEM;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)std::max(pl.cs, 1);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kern, q, k, v, p) != cudaSuccess) return DFLASH_ERR_CUDA;
-  if (grid == 1) return DFLASH_OK;
+  cfg.numAttrs = pl.cs ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, k_paged_attn<BF16, D, NM>, q, k, v, p) != cudaSuccess) return DFLASH_ERR_CUDA;
+  if (pl.cs || pl.grid == 1) return DFLASH_OK;
   cudaLaunchConfig_t mc = cfg;
-  mc.gridDim = dim3((unsigned)(grid - 1), 8);
+  mc.gridDim = dim3((unsigned)(pl.grid - 1), 8);
   mc.blockDim = dim3(MERGE_ROWS * D / 4);
-  mc.dynamicSmemBytes = (size_t)grid * 2 * MERGE_ROWS * sizeof(float);
-  return cudaLaunchKernelEx(&mc, k_paged_merge<BF16, D, NM>, p, grid) == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
+  mc.dynamicSmemBytes = (size_t)pl.grid * 2 * MERGE_ROWS * sizeof(float);
+  return cudaLaunchKernelEx(&mc, k_paged_merge<BF16, D, NM>, p, pl.grid) == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
 }
 
 }  // namespace
@@ -1065,29 +1249,28 @@ int launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, con
 extern "C" {
 
 size_t dflash_paged_attention_workspace(const dflash_paged_cache* c, int32_t rows, int32_t batch, int32_t q_heads) {
-  if (paged_cache_check(c) || rows < 0 || batch < 0 || q_heads < 1 || q_heads % c->kv_heads) return 0;
-  const int grid = device_grid(c->device);
-  return grid ? workspace_bytes(grid, m_tiles(rows, batch, q_heads / c->kv_heads), c->head_dim) : 0;
+  if (paged_cache_check(c) || !shape_ok(c, q_heads) || rows < 1 || batch < 1) return 0;
+  const Device* dev = device_of(c->device);
+  return dev ? plan_call(*dev, c, rows, batch, q_heads).ws : 0;
 }
 
 int dflash_paged_attention(const dflash_paged_cache* c, const dflash_attention_args* a, void* stream) {
   if (!a || a->rows < 0 || a->batch < 0 || a->window < 0 || !(a->scale == a->scale)) return DFLASH_ERR_INVALID_ARG;
   if (int e = paged_cache_check(c)) return e;
   const int D = c->head_dim;
-  if ((D != 64 && D != 128) || a->q_heads < 1 || a->q_heads % c->kv_heads || a->q_heads / c->kv_heads > 32)
-    return DFLASH_ERR_SHAPE;
+  if (!shape_ok(c, a->q_heads)) return DFLASH_ERR_SHAPE;
   if (a->rows == 0 || a->batch == 0) return DFLASH_OK;
   if (!a->q.data || !a->out.data || !a->cu_rows || !a->ctx_len || !rows_ok(a->q) || !rows_ok(a->out) ||
       !rows_ok({c->k, c->k_pos_stride, c->k_head_stride}) || !rows_ok({c->v, c->v_pos_stride, c->v_head_stride}) ||
       c->k_page_stride % 8 || c->v_page_stride % 8)
     return DFLASH_ERR_INVALID_ARG;
   if (a->batch > 8192) return DFLASH_ERR_CAPACITY;  // the sequences' first pairs lie in one M tile's shared memory
-  if (!a->workspace || (reinterpret_cast<uintptr_t>(a->workspace) & 255)) return DFLASH_ERR_WORKSPACE;
-  const int group = a->q_heads / c->kv_heads, nm = m_tiles(a->rows, a->batch, group);
-  if (a->workspace_bytes <= 0) return DFLASH_ERR_WORKSPACE;
-  const int grid = device_grid(c->device);
-  if (!grid) return DFLASH_ERR_CUDA;
-  if ((size_t)a->workspace_bytes < workspace_bytes(grid, nm, D)) return DFLASH_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(a->workspace) & 255) || a->workspace_bytes < 0) return DFLASH_ERR_WORKSPACE;
+  const Device* dev = device_of(c->device);
+  if (!dev) return DFLASH_ERR_CUDA;
+  const int group = a->q_heads / c->kv_heads;
+  const Plan pl = plan_call(*dev, c, a->rows, a->batch, a->q_heads);
+  if (pl.ws && (!a->workspace || (size_t)a->workspace_bytes < pl.ws)) return DFLASH_ERR_WORKSPACE;
   PagedParams p = {};
   p.out = static_cast<uint16_t*>(a->out.data);
   p.o_row = a->out.row_stride;
@@ -1119,6 +1302,7 @@ int dflash_paged_attention(const dflash_paged_cache* c, const dflash_attention_a
   p.scale_log2 = scale == 0.f ? 1e-30f : p.negate ? -scale : scale;
   p.status = c->status;
   p.ws = static_cast<char*>(a->workspace);
+  p.cs = pl.cs;
   DeviceGuard guard(c->device);
   if (!guard.ok) return DFLASH_ERR_CUDA;
   const bool bf = c->dtype == DFLASH_BF16;
@@ -1135,11 +1319,11 @@ int dflash_paged_attention(const dflash_paged_cache* c, const dflash_attention_a
     return DFLASH_ERR_INVALID_ARG;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (D == 128) {
-    if (nm == 2) return bf ? launch<true, 128, 2>(qm, km, vm, p, grid, s) : launch<false, 128, 2>(qm, km, vm, p, grid, s);
-    return bf ? launch<true, 128, 1>(qm, km, vm, p, grid, s) : launch<false, 128, 1>(qm, km, vm, p, grid, s);
+    if (pl.nm == 2) return bf ? launch<true, 128, 2>(qm, km, vm, p, pl, s) : launch<false, 128, 2>(qm, km, vm, p, pl, s);
+    return bf ? launch<true, 128, 1>(qm, km, vm, p, pl, s) : launch<false, 128, 1>(qm, km, vm, p, pl, s);
   }
-  if (nm == 2) return bf ? launch<true, 64, 2>(qm, km, vm, p, grid, s) : launch<false, 64, 2>(qm, km, vm, p, grid, s);
-  return bf ? launch<true, 64, 1>(qm, km, vm, p, grid, s) : launch<false, 64, 1>(qm, km, vm, p, grid, s);
+  if (pl.nm == 2) return bf ? launch<true, 64, 2>(qm, km, vm, p, pl, s) : launch<false, 64, 2>(qm, km, vm, p, pl, s);
+  return bf ? launch<true, 64, 1>(qm, km, vm, p, pl, s) : launch<false, 64, 1>(qm, km, vm, p, pl, s);
 }
 
 }  // extern "C"

@@ -280,7 +280,8 @@ def attention(cache: PagedCache, q, cu_rows, ctx_len, *, kv_len=None, causal: bo
     (None: ctx_len[b] + its rows, appended before), those up to p if causal,
     those above p - window if window > 0.  scale: 1/sqrt(head_dim) by default.
     lse: float32 [rows, q_heads] output for the rows' log-sum-exp.  workspace:
-    uint8, attention_workspace() bytes; by default allocated for the call."""
+    uint8, attention_workspace() bytes (0 for small calls); by default allocated
+    for the call."""
     device, dtype, dim = cache.device, cache.dtype, cache.head_dim
     raw = _raw_stream(stream, device)
     qs = _rows(q, "q", dtype, device, None, None, dim)
@@ -301,13 +302,14 @@ def attention(cache: PagedCache, q, cu_rows, ctx_len, *, kv_len=None, causal: bo
     lib = load()
     if workspace is None:
         nbytes = lib.dflash_paged_attention_workspace(cache._c, rows, b, hq)
-        workspace = _empty(nbytes, torch.uint8, q, stream)
+        if nbytes:
+            workspace = _empty(nbytes, torch.uint8, q, stream)
     elif workspace.dtype is not torch.uint8 or workspace.get_device() != device or not workspace.is_contiguous():
         raise ValueError(f"workspace: expected contiguous uint8 on cuda:{device}, got {workspace.dtype} on "
                          f"{workspace.device}")
     else:
         nbytes = workspace.numel()
-    args = _ATTENTION.pack(*qs, *os_, *ls, cu, ctx, kv, workspace.data_ptr(), nbytes, rows, b, hq, bool(causal), window,
+    args = _ATTENTION.pack(*qs, *os_, *ls, cu, ctx, kv, 0 if workspace is None else workspace.data_ptr(), nbytes, rows, b, hq, bool(causal), window,
                            dim ** -0.5 if scale is None else scale)
     code = lib.dflash_paged_attention(cache._c, args, raw)
     if code:

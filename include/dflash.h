@@ -547,7 +547,8 @@ DFLASH_API int dflash_paged_append(const dflash_paged_cache* cache, const dflash
  * of 8 elements.  A page that is not in the pool reads as zeros and sets
  * DFLASH_DEV_PAGE; a position beyond the table is not seen and sets it too.
  * workspace: DEVICE, 256-byte aligned, dflash_paged_attention_workspace
- * bytes, for this call alone until it is done. */
+ * bytes (0 where the call needs none: it may be null), for this call alone
+ * until it is done.  At most 8192 sequences a call (DFLASH_ERR_CAPACITY). */
 typedef struct dflash_attention_args {
   dflash_rows q, out;
   float* lse;

@@ -104,7 +104,8 @@ def test_c_entries_refuse_before_any_cuda_call(lib):
     assert attention(hq=3) == 2 and attention(hq=0) == 2 and attention(hq=66) == 2
     assert attention(q=(24, 128, 128)) == 1 and attention(q=(16, 100, 128)) == 1 and attention(out=(16, 128, 4)) == 1
     assert attention(c=cache(ks=(16384, 260, 128))) == 1 and attention(c=cache(ks=(16380, 256, 128))) == 1
-    assert attention(ws=0) == 6 and attention(ws=128) == 6 and attention(wsb=0) == 6 and attention(wsb=-1) == 6
+    assert attention(ws=128) == 6 and attention(wsb=-1) == 6
+    assert attention(batch=8193) == 3
     assert attention(rows_n=0) == 0 and attention(batch=0) == 0
     for bad, code in ((dict(k=0), 1), (dict(table=0), 1), (dict(status=0), 1), (dict(max_pages=0), 1),
                       (dict(stride=3), 1), (dict(pages=0), 1), (dict(heads=0), 1), (dict(dtype=5), 1),
