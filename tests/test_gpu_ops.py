@@ -240,6 +240,24 @@ def test_attention_scales_and_sharp_rows(ops):
     check_attention(ops, (8, 2, 128), [17], [600], BF16, scale=0.0)
 
 
+def test_attention_into_strided_outputs(ops):
+    """Rows of out 32- and 16-byte aligned, heads apart, beside each other and before the rows."""
+    pg = Paged(ops, [300, 77], 2, 128, 64, BF16)
+    q = torch.randn(60, 6, 128, generator=gen(2), device="cuda").to(BF16)
+    cu, ctx = i32([0, 50, 60]), i32([250, 67])
+    want = ops.attention(pg.cache, q, cu, ctx)
+    for width, at in ((128, 0), (144, 16), (136, 8), (256, 128)):
+        buf = torch.full((60, 9, width), 3.0, dtype=BF16, device="cuda")
+        out = buf[:, 1:7, at:at + 128]
+        ops.attention(pg.cache, q, cu, ctx, out=out)
+        assert torch.equal(out, want)
+        out.fill_(3.0)
+        assert (buf == 3.0).all()
+    heads_first = torch.zeros(6, 60, 128, dtype=BF16, device="cuda")
+    ops.attention(pg.cache, q.transpose(0, 1).contiguous().transpose(0, 1), cu, ctx, out=heads_first.transpose(0, 1))
+    assert torch.equal(heads_first.transpose(0, 1), want)
+
+
 def test_attention_of_many_sequences(ops):
     rows = [(i * 7) % 5 for i in range(300)]
     ctx = [(i * 37) % 400 for i in range(300)]
