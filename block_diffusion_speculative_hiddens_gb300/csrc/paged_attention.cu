@@ -375,21 +375,10 @@ template <int NM>
 DFL_DEV bool locate(const PagedParams& p, Sched* sc, Seq* seqs, int* first, Walk& w, Runs* runs) {
   const int per = p.tok * NM;
   const bool kept = p.batch <= (int)blockDim.x;
-  long long pairs = 0;
-  for (int b0 = 0; b0 < p.batch; b0 += blockDim.x) {
-    const int b = b0 + threadIdx.x;
-    int m = 0;
-    if (b < p.batch) {
-      const Seq s = load_seq(p, b);
-      if (kept) seqs[b] = s;
-      m = (s.n + per - 1) / per;
-    }
-    long long all;
-    const long long at = cta_scan(m, sc->part, &all);
-    if (b < p.batch) first[b] = (int)(pairs + at - m);
-    pairs += all;
-  }
-  __syncthreads();
+  long long pairs = 0, total = 0, all;
+  int b = 0, mt = 0, u = 0;  // this thread's pair and its cost
+  long long incl = 0;
+  bool once = kept;  // one round over the pairs
   auto weigh = [&](int pair, int* b_out, int* mt_out) {
     int lo = 0, hi = p.batch - 1;  // the last sequence whose first pair is not behind
     while (lo < hi) {
@@ -403,15 +392,38 @@ DFL_DEV bool locate(const PagedParams& p, Sched* sc, Seq* seqs, int* first, Walk
     *mt_out = mt;
     return SETUP<NM> + load_span(p, s, t0, min(t0 + per, s.n)).tiles;
   };
-  long long total = 0, all;
-  int b = 0, mt = 0, u = 0;
-  long long incl = 0;
-  const bool once = pairs <= blockDim.x;
-  for (long long p0 = 0; p0 < pairs; p0 += blockDim.x) {
-    const long long pair = p0 + threadIdx.x;
-    u = pair < pairs ? weigh((int)pair, &b, &mt) : 0;
-    incl = cta_scan((long long)u * p.hkv, sc->part, &all);
-    total += all;
+  bool alone = false;  // each sequence has one pair at most, and a thread
+  if (kept) {
+    const bool in = (int)threadIdx.x < p.batch;
+    Seq s = {0, 0, 0, 0};
+    if (in) {
+      s = load_seq(p, threadIdx.x);
+      seqs[threadIdx.x] = s;
+    }
+    alone = !__syncthreads_or(s.n > per);
+    if (alone) {
+      b = threadIdx.x;
+      u = s.n > 0 ? SETUP<NM> + load_span(p, s, 0, s.n).tiles : 0;
+      pairs = p.batch;
+      incl = cta_scan((long long)u * p.hkv, sc->part, &total);
+    }
+  }
+  if (!alone) {
+    for (int b0 = 0; b0 < p.batch; b0 += blockDim.x) {
+      const int bb = b0 + threadIdx.x;
+      const int m = bb < p.batch ? ((kept ? seqs[bb].n : load_seq(p, bb).n) + per - 1) / per : 0;
+      const long long at = cta_scan(m, sc->part, &all);
+      if (bb < p.batch) first[bb] = (int)(pairs + at - m);
+      pairs += all;
+    }
+    __syncthreads();
+    once = pairs <= blockDim.x;
+    for (long long p0 = 0; p0 < pairs; p0 += blockDim.x) {
+      const long long pair = p0 + threadIdx.x;
+      u = pair < pairs ? weigh((int)pair, &b, &mt) : 0;
+      incl = cta_scan((long long)u * p.hkv, sc->part, &all);
+      total += all;
+    }
   }
   if (total == 0) return false;
   runs->ctas = (int)min((long long)gridDim.x, total);
