@@ -2,7 +2,7 @@
 // the 5th-generation tensor cores.
 //
 // The rows of one KV head -- its G query heads of consecutive tokens -- share
-// its keys, so they are packed into M tiles of 128 rows (TOK = 128 / G tokens
+// its keys, so they are packed into M tiles of 128 rows (tok = 128 / G tokens
 // each).  An item is one or two (NM) M tiles of one sequence and KV head; its
 // work is the 128-key tiles its rows see.  All items' tiles, in order
 // (sequence, token tile, KV head), are cut into equal runs, one for each CTA
@@ -10,19 +10,38 @@
 // a long context and a prompt all load the SMs evenly.  A run that covers
 // only part of an item leaves its share (O unnormalised, running maximum and
 // sum, float32) in the workspace, and k_paged_merge joins the shares in order.
+// Few items over little cache take a cluster of CTAs each instead, which join
+// their shares over distributed shared memory (see plan_call).
 //
 // Per key tile and M tile:
 //   S = Q K^T   tcgen05.mma M=128 x N=128 keys x K=D, operands in shared memory,
-//   softmax     one row a thread, S read from TMEM, one pass with a running
-//               maximum (log2 domain) that moves only when a tile's maximum
-//               exceeds it by more than 2^8 (then the row's O is rescaled in
-//               TMEM): P is the same softmax up to a power of two that the sum
-//               shares, and stays inside f16,
-//   O += P V    tcgen05.mma with P as the TMEM A operand (16 bits, over the S
-//               it came from) and V as it lies in the cache (N-major).
-// The tensor core runs the MMAs in issue order, so S of the next tile may
-// overwrite the P that the O MMA before it read.
+//   softmax     one row a thread, S read from TMEM twice (maximum, then
+//               weights; log2 domain) against a running reference that moves
+//               only when a tile's maximum exceeds it by more than 2^8 (then
+//               the row's O is rescaled in TMEM): P is the same softmax up to a
+//               power of two that the sum shares, and stays inside f16.  P is
+//               rounded to the operands' 16 bits, as the tensor core takes it;
+//               maxima, sums and O are float32.
+//   O += P V    tcgen05.mma with P as the TMEM A operand (over the S it came
+//               from) and V as it lies in the cache (N-major).
+// The tensor core runs one thread's MMAs in issue order, so S of the next tile
+// may overwrite the P that the O MMA before it read.
 // Warps: 4 NM softmax, one issuing MMAs, one loading.
+//
+// Bounds and measurements (GB300; 32 query and 8 KV heads of 128, bf16):
+// - One token each for 64 requests of 512 to 4,096 positions reads 605 MB in
+//   99.9 us (6.06 TB/s, 0.89 of the copy rate); the runs themselves keep 0.95,
+//   finding them, the first load and the merge take 9 us.
+// - A chunk of 2,048 over 30,001 positions is 1.04 PFLOP in 688 us (1.51
+//   PFLOP/s, 0.79 of the cuBLAS burst rate).  A tile's two S and O MMAs are
+//   2,048 cycles, and a tile takes 3,000: softmax (1,900 from S to P) and the
+//   hand-overs between it, the issuing warp and the tensor core leave it idle
+//   in between.  Without any exponential it takes 2,900, so no polynomial
+//   stands in for them.
+// - Measured and not kept: two threads a row (16 softmax warps, 96 registers:
+//   859 us), an issuing warp for each M tile (their MMAs interleave and both
+//   end late: 868 us), the row in registers over both passes (spills at every
+//   item's end: whole prompt 461 for 408 us), MMAs issued by one lane (793 us).
 #include <algorithm>
 #include <atomic>
 #include <mutex>
@@ -30,20 +49,16 @@
 #include "common.cuh"
 #include "internal.h"
 
-#ifndef DFL_SETUP2
-#define DFL_SETUP2 2
-#endif
-#ifndef DFL_SETUP1
-#define DFL_SETUP1 1
-#endif
-
 namespace {
 
 constexpr int KT = 128;  // keys of a tile
 // What an item costs beside its tiles, in tiles: the load of Q, the first and
-// last tile that overlap nothing, the output.
+// last tile that overlap nothing, the output.  Measured with 1, 2 and 3 (us):
+// a prompt of 8,192 430 / 393 / 396, a window of 1,024 155 / 153 / 153, ragged
+// prompts of 64-wide heads 62.6 / 60.0 / 62.2; NM = 1 with 0, 1 and 2: blocks
+// of 24 requests 16.9 / 15.4 / 15.3, a token each for 64 105.7 / 104.7 / 104.5.
 template <int NM>
-constexpr int SETUP = NM == 2 ? DFL_SETUP2 : DFL_SETUP1;
+constexpr int SETUP = NM == 2 ? 2 : 1;
 
 struct PagedParams {
   uint16_t* out;
