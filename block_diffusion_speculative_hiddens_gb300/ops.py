@@ -279,7 +279,7 @@ def attention(cache: PagedCache, q, cu_rows, ctx_len, *, kv_len=None, causal: bo
     b, at position p = ctx_len[b] + i, sees the cached positions below kv_len[b]
     (None: ctx_len[b] + its rows, appended before), those up to p if causal,
     those above p - window if window > 0.  scale: 1/sqrt(head_dim) by default.
-    lse: float32 [rows, q_heads] output for the rows' log-sum-exp.  workspace:
+    out: q itself, or apart from it.  lse: float32 [rows, q_heads] output for the rows' log-sum-exp.  workspace:
     uint8, attention_workspace() bytes (0 for small calls); by default allocated
     for the call."""
     device, dtype, dim = cache.device, cache.dtype, cache.head_dim
@@ -293,6 +293,8 @@ def attention(cache: PagedCache, q, cu_rows, ctx_len, *, kv_len=None, causal: bo
         os_ = out.data_ptr(), hq * dim, dim
     else:
         os_ = _rows(out, "out", dtype, device, rows, hq, dim)
+        if out is not q:
+            _no_overlap(out, q, "out")
     ls = _NONE
     if lse is not None:
         if lse.dtype is not torch.float32 or lse.get_device() != device or tuple(lse.shape) != (rows, hq):

@@ -537,7 +537,8 @@ DFLASH_API int dflash_paged_append(const dflash_paged_cache* cache, const dflash
  * row t sees: 0 <= j < kv_len[b] (null: ctx_len[b] + the sequence's rows), with
  * causal also j <= position, with window w > 0 also j > position - w.  Query
  * head h reads KV head h / (q_heads / kv_heads).  A row that sees no position
- * gets out 0 and lse -inf.  lse (optional, float32 [rows][q_heads], strides of
+ * gets out 0 and lse -inf.  out may be q (same pointer and strides) and must
+ * not overlap it otherwise.  lse (optional, float32 [rows][q_heads], strides of
  * its own): the natural logarithm of the row's sum of exponentials.  Only
  * pages that hold a seen position are read, and of the last of them nothing
  * behind kv_len reaches the result; a non-finite value within kv_len reaches

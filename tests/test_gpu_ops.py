@@ -258,6 +258,20 @@ def test_attention_into_strided_outputs(ops):
     assert torch.equal(heads_first.transpose(0, 1), want)
 
 
+def test_attention_in_place_of_its_queries(ops):
+    """out = q: in the middle of a sequence, with rows of the next one in the same tile, split and whole."""
+    for rows, ctx in (([16], [2000]), ([1, 1, 5], [5, 900, 70]), ([300, 7, 90], [40, 0, 3000]), ([1] * 70, [500] * 70)):
+        pg = Paged(ops, [a + b for a, b in zip(rows, ctx)], 2, 128, 64, BF16)
+        cu = i32([sum(rows[:i]) for i in range(len(rows) + 1)])
+        qkv = torch.randn(sum(rows), 10, 128, generator=gen(2), device="cuda").to(BF16)
+        rest = qkv[:, 6:].clone()
+        want = ops.attention(pg.cache, qkv[:, :6], cu, i32(ctx))
+        assert ops.attention(pg.cache, qkv[:, :6], cu, i32(ctx), out=qkv[:, :6]).data_ptr() == qkv.data_ptr()
+        assert torch.equal(qkv[:, :6], want) and torch.equal(qkv[:, 6:], rest)
+        with pytest.raises(ValueError, match="overlaps"):
+            ops.attention(pg.cache, qkv[:, :6], cu, i32(ctx), out=qkv[:, 1:7])
+
+
 def test_attention_of_many_sequences(ops):
     rows = [(i * 7) % 5 for i in range(300)]
     ctx = [(i * 37) % 400 for i in range(300)]
@@ -480,6 +494,63 @@ def test_captured_steps_replay_on_new_values(ops):
         assert torch.equal(got[:n], want[:n])
         assert n == 0 or want[:n].abs().max() > 0
     assert pg.cache.read_status() == 0
+
+
+FIRST_CALL = """
+import torch
+from block_diffusion_speculative_hiddens_gb300 import ops
+dev = dict(device="cuda")
+kp, vp = (torch.randn(8, 64, 2, 64, **dev).to(torch.bfloat16) for _ in range(2))
+rows = %d
+q = torch.randn(rows, 4, 64, **dev).to(torch.bfloat16)
+k = torch.randn(rows, 2, 64, **dev).to(torch.bfloat16)
+cu, ctx = (torch.tensor(x, dtype=torch.int32, **dev) for x in ([0, rows], [30]))
+cache = ops.PagedCache(kp, vp, torch.arange(8, dtype=torch.int32, **dev).view(1, 8))
+plan = ops.RopePlan(64, 1e4)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    out = ops.attention(cache, ops.append(cache, k, k, cu, ctx, plan=plan, q=q), cu, ctx)
+    r = ops.rope(plan, q, None, cu[1:].expand(rows).contiguous())[0]
+g.replay()
+torch.cuda.synchronize()
+want = ops.attention(cache, ops.append(cache, k, k, cu, ctx, plan=plan, q=q), cu, ctx)
+assert torch.equal(out, want) and torch.isfinite(r.float()).all() and cache.read_status() == 0
+"""
+
+
+@pytest.mark.parametrize("rows", [3, 200])
+def test_first_call_of_a_process_may_be_captured(ops, rows):
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL % rows], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_two_captured_graphs_run_at_once(ops):
+    """Each graph holds a workspace and outputs of its own."""
+    jobs = []
+    for seed, heads, rows, ctx in ((1, (8, 2, 128), [16] * 8, [3000] * 8), (2, (16, 2, 64), [300, 1], [0, 5000])):
+        pg = Paged(ops, [a + b for a, b in zip(rows, ctx)], heads[1], heads[2], 64, BF16, seed=seed)
+        q = torch.randn(sum(rows), heads[0], heads[2], generator=gen(seed), device="cuda").to(BF16)
+        args = (pg.cache, q, i32([sum(rows[:i]) for i in range(len(rows) + 1)]), i32(ctx))
+        want = ops.attention(*args)
+        torch.cuda.synchronize()
+        g, out = torch.cuda.CUDAGraph(), torch.zeros_like(q)
+        with torch.cuda.graph(g):
+            ops.attention(*args, out=out)
+        jobs.append((g, out, want, torch.cuda.Stream(), args))  # the inputs live as long as their graph
+    for _ in range(10):
+        for g, out, _, s, _ in jobs:
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for _, out, want, _, _ in jobs:
+            assert torch.equal(out, want)
+            out.zero_()
 
 
 def test_calls_on_two_streams_at_once(ops):
