@@ -173,7 +173,8 @@ struct PCfg {
   static constexpr int SLOTS = D == 128 ? 5 : 10;
   static constexpr int OFF_RING = QBUFS * NM * TILE;
   static constexpr int OFF_BAR = OFF_RING + SLOTS * TILE;
-  static constexpr int SMEM = 1024 + OFF_BAR + 512;  // + 1024 for aligning the base
+  static constexpr int OFF_ITEM = OFF_BAR + 576;     // the loading warp's notes of the next items
+  static constexpr int SMEM = 1024 + OFF_ITEM + 128;  // + 1024 for aligning the base
   static constexpr int THREADS = 128 * NM + 64;
   static constexpr int S_COL = 0;                    // two S buffers of 128 columns
   static constexpr int O_COL = 256;
@@ -189,6 +190,17 @@ DFL_DEV uint32_t pack16(float a, float b) {
     return pack_f16x2(a, b);
   }
 }
+
+// The rest of a bounded wait that has not succeeded at once; out of line, since
+// the kernel's code is fetched by warps in several places of it at once.
+static __device__ __noinline__ bool wait_rest(uint64_t* bar, uint32_t par, uint32_t* status) {
+  bool aborted = false;
+  return mbar_wait(bar, par, status, &aborted);
+}
+
+// A value that is the same in every lane, told to the compiler: addresses and
+// loop bounds made of it need no code for lanes that differ.
+DFL_DEV int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 DFL_DEV float ex2(float x) {
   float y;
@@ -375,6 +387,21 @@ DFL_DEV long long cta_scan(long long v, long long* part, long long* total) {
   return v + before;
 }
 
+// A segment as the issuing and the softmax warps need it: written by the
+// loading warp, which is ahead of them, since each working it out from its own
+// place in the run costs a microsecond between two items.
+struct Item {
+  int tiles;   // this CTA's key tiles (0: its rows get zeros; -1: no more items)
+  int key0;    // first key of the first of them
+  int row0;    // first row of q
+  int tokens;
+  int pos0;    // position of the first token
+  int kv;      // keys of the sequence
+  int kvh;
+  int share;   // 0: all of the item's tiles; 1: its first ones, 2: later ones
+};
+constexpr int ITEMS = 4;  // noted ahead, at most
+
 struct Sched {
   long long part[16];
   int b, mt, cost;
@@ -524,10 +551,10 @@ DFL_DEV bool locate_cluster(const PagedParams& p, Sched* sc, Walk& w) {
 constexpr int MAX_CLUSTER = 16;
 constexpr long long CLUSTER_TILES = 640;  // key tiles that a call's tables can hold
 template <bool BF16, int D>
-DFL_DEV void join_cluster(const PagedParams& p, const uint8_t* sm, const Walk& w) {
+DFL_DEV void join_cluster(const PagedParams& p, const uint8_t* sm, int row0, int rows, int head0) {
   constexpr int PS = D + 4;
   const uint32_t at = smem_u32(sm);
-  const int rank = (int)cluster_ctarank(), rows = (w.t1 - w.t0) * p.group;
+  const int rank = (int)cluster_ctarank();
   const int mine = (rows - rank + p.cs - 1) / p.cs;
   for (int e = threadIdx.x; e < mine * (D / 4); e += blockDim.x) {
     const int r = rank + e / (D / 4) * p.cs, d = e % (D / 4) * 4;
@@ -561,7 +588,7 @@ DFL_DEV void join_cluster(const PagedParams& p, const uint8_t* sm, const Walk& w
       acc.w += wgt * o[x].w;
     }
     const float inv = L == 0.f ? 0.f : 1.f / L;
-    const long long t = w.s.row0 + w.t0 + r / p.group, h = w.kvh * p.group + r % p.group;
+    const long long t = row0 + r / p.group, h = head0 + r % p.group;
     *reinterpret_cast<uint2*>(p.out + t * p.o_row + h * p.o_head + d) =
         make_uint2(pack16<BF16>(acc.x * inv, acc.y * inv), pack16<BF16>(acc.z * inv, acc.w * inv));
     if (p.lse && d == 0)
@@ -586,11 +613,15 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
   uint64_t* q_full = o_empty + 2;       // [QBUFS]
   uint64_t* q_empty = q_full + 2;
   uint64_t* mdone = q_empty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mdone + 1);
-  Sched* sched = reinterpret_cast<Sched*>(sm + C::OFF_BAR + 320);
-  static_assert((2 * C::SLOTS + 13) * 8 + 8 <= 320 && sizeof(Sched) <= 192, "barrier area");
+  uint64_t* item_full = mdone + 1;      // [ITEMS]
+  uint64_t* item_empty = item_full + ITEMS;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(item_empty + ITEMS);
+  Sched* sched = reinterpret_cast<Sched*>(sm + C::OFF_BAR + 384);
+  Item* items = reinterpret_cast<Item*>(sm + C::OFF_ITEM);
+  static_assert((2 * C::SLOTS + 13 + 2 * ITEMS) * 8 + 8 <= 384 && sizeof(Sched) <= 192 && sizeof(Item) * ITEMS == 128,
+                "barrier area");
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   constexpr int MMA_WARP = 4 * NM, LOAD_WARP = 4 * NM + 1;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::SLOTS; ++i) {
@@ -608,6 +639,10 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
       mbar_init(q_empty + i, 1);
     }
     mbar_init(mdone, 1);
+    for (int i = 0; i < ITEMS; ++i) {
+      mbar_init(item_full + i, 1);
+      mbar_init(item_empty + i, 4 * NM + 1);
+    }
     fence_mbar_init();
   }
   if (warp == MMA_WARP) {
@@ -622,7 +657,7 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
   pdl_launch_dependents();
   pdl_wait();
 
@@ -647,11 +682,23 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
   __syncthreads();
   bool aborted = false;
   auto wait_all = [&](uint64_t* bar, uint32_t par) {  // warp-uniform
-    const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, par, p.status, &aborted));
-    if (!ok) aborted = true;
-    return ok;
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, par))) return true;
+    if (aborted || !__all_sync(0xffffffffu, wait_rest(bar, par, p.status))) aborted = true;
+    return !aborted;
   };
-
+  // The next item, for a warp that takes them in turn; false after the last.
+  auto next_item = [&](int& taken, Item& x) {
+    const int i = taken % ITEMS;
+    if (!wait_all(item_full + i, (uint32_t)((taken / ITEMS) & 1))) return false;
+    ++taken;
+    x = items[i];
+    x.tiles = uniform(x.tiles);
+    x.key0 = uniform(x.key0);
+    x.tokens = uniform(x.tokens);
+    x.kv = uniform(x.kv);
+    if (lane == 0) mbar_arrive(item_empty + i);
+    return x.tiles >= 0;
+  };
   if (!work) {
     // nothing for this CTA
   } else if (warp == LOAD_WARP) {
@@ -662,11 +709,28 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
     const int page = 1 << p.shift, box = min(page, KT), boxes = KT / box;
     const int bi = lane % boxes, bh = lane / boxes;  // this lane's box, if bh is a panel
     int seg = 0;
+    int noted = 0;     // items
     Ring<C::SLOTS> at;
     bool lap = false;  // the ring has been filled once
     bool ok = true;
+    auto note = [&](const Item& x) {
+      const int i = noted % ITEMS;
+      if (noted >= ITEMS && !wait_all(item_empty + i, (uint32_t)((noted / ITEMS - 1) & 1))) return false;
+      if (lane == 0) {
+        items[i] = x;
+        mbar_arrive(item_full + i);
+      }
+      ++noted;
+      return true;
+    };
     do {
-      const int tiles = w.n;
+      const int tiles = uniform(w.n);
+      if (!w.out && !in_cluster) continue;
+      const int far = 0x7ff00000;  // farther than any key, and a tile's tokens more still fit
+      if (!(ok = note({tiles, (w.span.tile0 + w.off) * KT, w.s.row0 + w.t0, w.t1 - w.t0,
+                       (int)min(max(w.s.ctx + w.t0, -(long long)far), (long long)far), w.s.kv, w.kvh,
+                       tiles == w.span.tiles ? 0 : w.off == 0 ? 1 : 2})))
+        break;
       if (tiles == 0) continue;
       if (lane == 0 && (p.kv_len ? (long long)p.kv_len[w.b] : w.s.ctx + w.s.n) > p.cap)
         dev_error(p.status, DFLASH_DEV_PAGE);
@@ -719,15 +783,14 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
         if (C::QBUFS == 1 && j == 0 && ok) ok = load_q();
       }
     } while (ok && walk_next<NM>(p, w));
+    if (ok) note({-1, 0, 0, 0, 0, 0, 0, 0});
     // every copy lands before the CTA may exit
     for (int i = lap ? 0 : C::SLOTS - at.s; i < C::SLOTS; ++i) {  // from the oldest slot on
       const int s = lap ? (at.s + i) % C::SLOTS : i - (C::SLOTS - at.s);
-      bool drain = false;
-      mbar_wait(full + s, s < at.s ? at.phase : at.phase ^ 1u, p.status, &drain);
+      wait_rest(full + s, s < at.s ? at.phase : at.phase ^ 1u, p.status);
     }
     for (int i = seg > C::QBUFS ? seg - C::QBUFS : 0; i < seg; ++i) {
-      bool drain = false;
-      mbar_wait(q_full + i % C::QBUFS, (uint32_t)((i / C::QBUFS) & 1), p.status, &drain);
+      wait_rest(q_full + i % C::QBUFS, (uint32_t)((i / C::QBUFS) & 1), p.status);
     }
   } else if (warp == MMA_WARP) {
     // ------------------------------------------------ MMA issue (converged warp, one elected lane)
@@ -749,10 +812,12 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
       tc_commit_elect(s_full + buf);
     };
     bool ok = true;
-    do {
-      const int tiles = w.n;
+    int taken = 0;
+    Item x;
+    while (ok && next_item(taken, x)) {
+      const int tiles = x.tiles;
       if (tiles == 0) continue;
-      const int nm = NM == 2 && w.t0 + p.tok < w.t1 ? 2 : 1;
+      const int nm = NM == 2 && x.tokens > p.tok ? 2 : 1;
       const int qb = seg % C::QBUFS;
       if (!wait_all(q_full + qb, (uint32_t)((seg / C::QBUFS) & 1)) || !wait_all(full + kr.s, kr.phase)) break;
       ++seg;
@@ -766,7 +831,7 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
       kr.next();
       if (tiles == 1) tc_commit_elect(q_empty + qb);
       // keys of the sequence behind the start of its last tile, if that tile ends inside a page
-      const int last_v = w.s.kv - (w.span.tile0 + w.off + tiles - 1) * KT;
+      const int last_v = x.kv - x.key0 - (tiles - 1) * KT;
       for (int j = 0; j < tiles && ok; ++j) {
         const bool more = j + 1 < tiles;
         const int buf1 = NM == 1 ? it - 1 & 1 : 0;
@@ -821,11 +886,10 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
         vr.next();
         vr.next();
       }
-    } while (ok && walk_next<NM>(p, w));
+    }
     // every issued MMA completes before the columns are freed
     tc_commit_elect(mdone);
-    bool drain = false;
-    mbar_wait(mdone, 0, p.status, &drain);
+    wait_rest(mdone, 0, p.status);
   } else {
     // ------------------------------------------------ softmax: one row a thread
     const int m = warp >> 2;
@@ -843,25 +907,20 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
     auto wait_o = [&](int i) {
       return NM == 2 ? wait_all(o_done + m, (uint32_t)(i & 1)) : wait_all(o_done + (i & 1), (uint32_t)((i >> 1) & 1));
     };
-    do {
-      const int tiles = w.n;
-      if (!w.out) {
-        if (NM == 1 && in_cluster) {  // no tile of the item: a share without keys
-          float* part = reinterpret_cast<float*>(sm) + 128 * (D + 4);
-          part[r] = -INFINITY;
-          part[128 + r] = 0.f;
-        }
-        continue;
-      }
-      const int t = w.t0 + m * p.tok + rt;
-      const bool valid = rt < p.tok && t < w.t1;
-      if (NM == 2 && m == 1 && w.t0 + p.tok >= w.t1) continue;  // no row in this M tile
+    int taken = 0;
+    Item x;
+    while (next_item(taken, x)) {
+      const int tiles = x.tiles;
+      const int tm = m * p.tok + rt;  // the row's token in the item
+      if (NM == 2 && m == 1 && x.tokens <= p.tok) continue;  // no row in this M tile
+      const bool valid = rt < p.tok && tm < x.tokens;
       const bool warp_valid = __any_sync(0xffffffffu, valid);
       // the keys this row sees; rows that do not exist mask nothing (they are not written)
       int lo = 0, hi = 1 << 30;
       if (valid) {
-        hi = p.causal ? (int)min(max(w.s.ctx + t + 1, 0ll), (long long)w.s.kv) : w.s.kv;
-        lo = p.window > 0 ? (int)min(max(w.s.ctx + t - p.window + 1, 0ll), (long long)w.s.kv) : 0;
+        const int pos = x.pos0 + tm;
+        hi = p.causal ? min(max(pos + 1, 0), x.kv) : x.kv;
+        lo = p.window > 0 ? (int)min(max((long long)pos - p.window + 1, 0ll), (long long)x.kv) : 0;
       }
       float m_run = -INFINITY, l_run = 0.f;
       for (int j = 0; j < tiles; ++j, ++it) {
@@ -871,7 +930,7 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
         tc_fence_after();
         const uint32_t s_base = lane_base + (uint32_t)(C::S_COL + 128 * buf);
         if (warp_valid) {
-          const int key0 = (w.span.tile0 + w.off + j) * KT;
+          const int key0 = x.key0 + j * KT;
           const int h = hi - key0, l = lo - key0;
           if (p.negate || __any_sync(0xffffffffu, h < KT || l > 0)) {
             // S as the two passes below want it: its sign turned, -inf where the row does not see
@@ -893,7 +952,7 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
           // Both passes read S from TMEM, 64 columns at a time and ahead of the
           // arithmetic.  Held in registers over both (128 of them) a row takes
           // 0.2 us less, but what spills costs more at every item's end.
-          uint32_t x[32], y[32];
+          uint32_t sx[32], sy[32];
           float mx = -INFINITY;
           {
             float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
@@ -906,17 +965,17 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
                 m3 = max3(m3, __uint_as_float(v[k + 6]), __uint_as_float(v[k + 7]));
               }
             };
-            tmem_ld32_nowait(s_base, x);
-            tmem_ld32_nowait(s_base + 32, y);
+            tmem_ld32_nowait(s_base, sx);
+            tmem_ld32_nowait(s_base + 32, sy);
             tmem_wait_ld();
-            take(x);
-            tmem_ld32_nowait(s_base + 64, x);
-            take(y);
-            tmem_ld32_nowait(s_base + 96, y);
+            take(sx);
+            tmem_ld32_nowait(s_base + 64, sx);
+            take(sy);
+            tmem_ld32_nowait(s_base + 96, sy);
             tmem_wait_ld();
-            take(x);
-            tmem_ld32_nowait(s_base, x);
-            take(y);
+            take(sx);
+            tmem_ld32_nowait(s_base, sx);
+            take(sy);
             mx = max3(fmaxf(m0, m1), m2, m3) * p.scale_log2;
           }
           const bool move = mx > m_run + 8.f;
@@ -965,11 +1024,11 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
 #pragma unroll 1
           for (int c = 0; c < KT; c += 64) {
             tmem_wait_ld();
-            tmem_ld32_nowait(s_base + c + 32, y);
-            weigh(x, c);
+            tmem_ld32_nowait(s_base + c + 32, sy);
+            weigh(sx, c);
             tmem_wait_ld();
-            if (c + 64 < KT) tmem_ld32_nowait(s_base + c + 64, x);
-            weigh(y, c + 32);
+            if (c + 64 < KT) tmem_ld32_nowait(s_base + c + 64, sx);
+            weigh(sy, c + 32);
           }
           float a, b;
           unpack_f32x2(add_f32x2(sum0, sum1), a, b);
@@ -986,74 +1045,59 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
         if (!(ok = wait_o(it - 1))) break;
         tc_fence_after();
       }
-      const bool whole = tiles == w.span.tiles && !in_cluster;
-      if (NM == 1 && in_cluster) {  // the tile area is free: every load has been used
-        float* part = reinterpret_cast<float*>(sm);
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
+      const bool to_cluster = NM == 1 && in_cluster, whole = x.share == 0 && !to_cluster;
+      if (warp_valid || to_cluster) {
+        // where the row's O goes: out, this CTA's share in the workspace, or
+        // (the tile area being free: every load has been used) in shared memory
+        const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+        const int head = x.kvh * p.group + rh;
+        const long long qrow = x.row0 + tm;
+        uint16_t* dst = p.out + qrow * p.o_row + head * p.o_head;
+        const int row = m * 128 + r, stride = to_cluster ? 1 : C::ROWS;  // of the share's float4 columns
+        float* share = reinterpret_cast<float*>(p.ws + ws_records(gridDim.x)) +
+                       (2 * (size_t)blockIdx.x + (x.share == 1)) * ws_slot_floats(C::ROWS, D);
+        float4* part = reinterpret_cast<float4*>(to_cluster ? reinterpret_cast<float*>(sm) + r * (D + 4) : share + 4 * row);
+#pragma unroll 1  // once an item: a longer loop waits on instruction fetch
+        for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
-          tmem_ld32_nowait(o_base + 32 * c, o);
-          tmem_wait_ld();
+          if (tiles > 0) {
+            tmem_ld32_nowait(o_base + c, o);
+            tmem_wait_ld();
+          } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            *reinterpret_cast<uint4*>(part + r * (D + 4) + 32 * c + 4 * e) =
-                make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-        }
-        part[128 * (D + 4) + r] = m_run;
-        part[128 * (D + 4) + 128 + r] = l_run;
-      } else if (warp_valid) {
-        if (whole) {
-          const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
-          const long long head = w.kvh * p.group + rh, row = w.s.row0 + t;
-          uint16_t* dst = p.out + row * p.o_row + head * p.o_head;
+            for (int e = 0; e < 32; ++e) o[e] = 0u;
+          }
+          if (!whole && (valid || to_cluster)) {
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            if (tiles > 0) {
-              tmem_ld32_nowait(o_base + 32 * c, o);
-              tmem_wait_ld();
+            for (int e = 0; e < 8; ++e)
+              part[(c / 4 + e) * stride] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                                       __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+          }
+          if (whole && valid) {
+            uint32_t y[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              y[e] = pack16<BF16>(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+            if (p.wide_out) {  // a row a thread: whole 32-byte sectors, half the store instructions
+              st_global_32(dst + c, y);
+              st_global_32(dst + c + 16, y + 8);
             } else {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = 0u;
-            }
-            if (valid) {
-              uint32_t y[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e)
-                y[e] = pack16<BF16>(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-              if (p.wide_out) {  // a row a thread: whole 32-byte sectors, half the store instructions
-                st_global_32(dst + 32 * c, y);
-                st_global_32(dst + 32 * c + 16, y + 8);
-              } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  *reinterpret_cast<uint4*>(dst + 32 * c + 8 * e) = make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
-              }
+              for (int e = 0; e < 4; ++e)
+                *reinterpret_cast<uint4*>(dst + c + 8 * e) = make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
             }
           }
-          if (p.lse && valid)
-            p.lse[row * p.lse_row + head * p.lse_head] =
-                l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * 0.6931471805599453f;
-        } else {
-          const int slot = 2 * blockIdx.x + (w.off == 0 ? 1 : 0);
-          float* part = reinterpret_cast<float*>(p.ws + ws_records(gridDim.x)) + slot * ws_slot_floats(C::ROWS, D);
-          const int row = m * 128 + r;
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32_nowait(o_base + 32 * c, o);
-            tmem_wait_ld();
-            if (valid) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                *reinterpret_cast<uint4*>(part + ((size_t)(8 * c + e) * C::ROWS + row) * 4) =
-                    make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-            }
-          }
-          if (valid) {
-            part[(size_t)C::ROWS * D + row] = m_run;
-            part[(size_t)C::ROWS * (D + 1) + row] = l_run;
-          }
+        }
+        if (to_cluster) {  // without a tile: a share without keys
+          float* ml = reinterpret_cast<float*>(sm) + 128 * (D + 4);
+          ml[r] = m_run;
+          ml[128 + r] = l_run;
+        } else if (valid && !whole) {
+          share[(size_t)C::ROWS * D + row] = m_run;
+          share[(size_t)C::ROWS * (D + 1) + row] = l_run;
+        } else if (valid && p.lse) {
+          p.lse[qrow * p.lse_row + head * p.lse_head] =
+              l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * 0.6931471805599453f;
         }
       }
       if (tiles > 0) {
@@ -1061,7 +1105,7 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(o_empty + m);
       }
-    } while (walk_next<NM>(p, w));
+    }
   }
   tc_fence_before();
   __syncthreads();  // every MMA and TMEM read done, every tile landed
@@ -1071,7 +1115,7 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
   }
   if (NM == 1 && in_cluster && work) {  // the whole cluster's answer
     cluster_sync_all();
-    join_cluster<BF16, D>(p, sm, w);
+    join_cluster<BF16, D>(p, sm, w.s.row0 + w.t0, (w.t1 - w.t0) * p.group, w.kvh * p.group);
     cluster_sync_all();  // this CTA's share is there until every other has read it
   }
 }
