@@ -170,7 +170,7 @@ struct PCfg {
   static constexpr int TILE = (D / 64) * PANEL;      // Q of an M tile, K or V of a key tile
   // Q of the next item lands beside this one's where there is room for both
   static constexpr int QBUFS = D == 128 && NM == 2 ? 1 : 2;
-  static constexpr int SLOTS = D == 128 ? 5 : 10;
+  static constexpr int SLOTS = D == 64 ? 10 : NM == 2 ? 4 : 5;  // NM = 2: a fifth made nothing faster
   static constexpr int OFF_RING = QBUFS * NM * TILE;
   static constexpr int OFF_BAR = OFF_RING + SLOTS * TILE;
   static constexpr int OFF_ITEM = OFF_BAR + 576;     // the loading warp's notes of the next items
@@ -857,8 +857,6 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
           fence_proxy_async_smem();
           __syncwarp();
         }
-        // the next tile's K is looked for while P is awaited
-        const bool k_here = NM == 2 && more && __all_sync(0xffffffffu, mbar_try_wait(full + kr.s, kr.phase));
         const uint64_t vd = v_desc + (uint64_t)(vr.s * (C::TILE >> 4));
         for (int m = 0; m < nm; ++m) {
           const int buf = NM == 2 ? m : buf1;
@@ -871,7 +869,7 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
           if (m == nm - 1) tc_commit_elect(empty + vr.s);
           if (NM == 2 && more) {
             if (m == 0) {
-              if (!k_here && !(ok = wait_all(full + kr.s, kr.phase))) break;
+              if (!(ok = wait_all(full + kr.s, kr.phase))) break;
               tc_fence_after();
             }
             issue_s(m, m, qb, kr.s);
