@@ -930,27 +930,32 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
         if (warp_valid) {
           const int key0 = x.key0 + j * KT;
           const int h = hi - key0, l = lo - key0;
+          uint32_t sx[32], sy[32];
           if (p.negate || __any_sync(0xffffffffu, h < KT || l > 0)) {
             // S as the two passes below want it: its sign turned, -inf where the row does not see
-#pragma unroll 1
-            for (int c = 0; c < KT / 16; ++c) {
-              uint32_t x[16];
-              tmem_ld16_nowait(s_base + 16 * c, x);
-              tmem_wait_ld();
-              const uint32_t seen = low_bits(h - 16 * c) & ~low_bits(l - 16 * c);
+            auto edit = [&](uint32_t* v, int c) {
+              const uint32_t seen = low_bits(h - c) & ~low_bits(l - c);
 #pragma unroll
-              for (int k = 0; k < 16; ++k) {
-                if (p.negate) x[k] ^= 0x80000000u;
-                if (!(seen & (1u << k))) x[k] = 0xff800000u;
+              for (int k = 0; k < 32; ++k) {
+                if (p.negate) v[k] ^= 0x80000000u;
+                if (!(seen & (1u << k))) v[k] = 0xff800000u;
               }
-              tmem_st16_nowait(s_base + 16 * c, x);
+              tmem_st16_nowait(s_base + c, v);
+              tmem_st16_nowait(s_base + c + 16, v + 16);
+            };
+#pragma unroll 1
+            for (int c = 0; c < KT; c += 64) {
+              tmem_ld32_nowait(s_base + c, sx);
+              tmem_ld32_nowait(s_base + c + 32, sy);
+              tmem_wait_ld();
+              edit(sx, c);
+              edit(sy, c + 32);
             }
             tmem_wait_st();
           }
           // Both passes read S from TMEM, 64 columns at a time and ahead of the
           // arithmetic.  Held in registers over both (128 of them) a row takes
           // 0.2 us less, but what spills costs more at every item's end.
-          uint32_t sx[32], sy[32];
           float mx = -INFINITY;
           {
             float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
