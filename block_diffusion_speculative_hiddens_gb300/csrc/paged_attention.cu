@@ -1024,15 +1024,15 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
             }
             tmem_st16_nowait(s_base + c / 2, pk);
           };
-#pragma unroll 1
-          for (int c = 0; c < KT; c += 64) {
-            tmem_wait_ld();
-            tmem_ld32_nowait(s_base + c + 32, sy);
-            weigh(sx, c);
-            tmem_wait_ld();
-            if (c + 64 < KT) tmem_ld32_nowait(s_base + c + 64, sx);
-            weigh(sy, c + 32);
-          }
+          tmem_ld32_nowait(s_base + 32, sy);
+          tmem_wait_ld();
+          weigh(sx, 0);
+          tmem_ld32_nowait(s_base + 64, sx);
+          weigh(sy, 32);
+          tmem_ld32_nowait(s_base + 96, sy);
+          tmem_wait_ld();
+          weigh(sx, 64);
+          weigh(sy, 96);
           float a, b;
           unpack_f32x2(add_f32x2(sum0, sum1), a, b);
           l_run += a + b;
