@@ -30,18 +30,24 @@
 //
 // Bounds and measurements (GB300; 32 query and 8 KV heads of 128, bf16):
 // - One token each for 64 requests of 512 to 4,096 positions reads 605 MB in
-//   99.9 us (6.06 TB/s, 0.89 of the copy rate); the runs themselves keep 0.95,
+//   100 us (6.0 TB/s, 0.89 of the copy rate); the runs themselves keep 0.95,
 //   finding them, the first load and the merge take 9 us.
-// - A chunk of 2,048 over 30,001 positions is 1.04 PFLOP in 688 us (1.51
-//   PFLOP/s, 0.79 of the cuBLAS burst rate).  A tile's two S and O MMAs are
-//   2,048 cycles, and a tile takes 3,000: softmax (1,900 from S to P) and the
-//   hand-overs between it, the issuing warp and the tensor core leave it idle
-//   in between.  Without any exponential it takes 2,900, so no polynomial
-//   stands in for them.
+// - A chunk of 2,048 over 30,001 positions is 1.04 PFLOP in 641 us (1.62
+//   PFLOP/s, 0.84 of the cuBLAS burst rate); a whole prompt of 8,192 360 us.  A
+//   tile's two S and O MMAs are 2,048 cycles, and a tile takes 2,800: what a
+//   row's softmax takes from S to P, and the hand-overs between it, the
+//   issuing warp and the tensor core, which leave that idle in between.
+//   Without any exponential the chunk takes 624 us and 64-wide heads 12 % less.
+// - What moved it (chunk, us): softmax in short loops over TMEM 904 -> 733, one
+//   elect.sync a tile, counted ring places 730 -> 708, 64 columns of S in
+//   flight 708 -> 688 (first pass) and 666 -> 641 (second), warp-uniform values
+//   told to the compiler 689 -> 662.
 // - Measured and not kept: two threads a row (16 softmax warps, 96 registers:
-//   859 us), an issuing warp for each M tile (their MMAs interleave and both
-//   end late: 868 us), the row in registers over both passes (spills at every
-//   item's end: whole prompt 461 for 408 us), MMAs issued by one lane (793 us).
+//   859 for 729), an issuing warp for each M tile (their MMAs interleave and both
+//   end late: 868), the row in registers over both passes (645 for 641, but
+//   whole prompts 382 for 360: what spills costs at every item's end), MMAs
+//   issued by one lane (793 for 728), Q double-buffered with a ring of three
+//   tiles (826 for 716).
 #include <algorithm>
 #include <atomic>
 #include <mutex>
@@ -953,9 +959,7 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
             }
             tmem_wait_st();
           }
-          // Both passes read S from TMEM, 64 columns at a time and ahead of the
-          // arithmetic.  Held in registers over both (128 of them) a row takes
-          // 0.2 us less, but what spills costs more at every item's end.
+          // Both passes read S from TMEM, 64 columns at a time and ahead of the arithmetic.
           float mx = -INFINITY;
           {
             float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
