@@ -1284,27 +1284,31 @@ struct Plan {
   int grid;
   size_t ws;
 };
-// Items to launch a cluster for, at most: a sequence of n rows has ceil(n / tok) token tiles.
+// Items to launch a cluster for: a sequence of n rows has ceil(n / tok) token tiles; the most that any lengths make.
 long long max_items(int rows, int batch, int tok, int hkv) {
   return std::min<long long>(rows, ((long long)rows + (long long)batch * (tok - 1)) / tok) * hkv;
 }
 Plan plan_call(const Device& dev, const dflash_paged_cache* c, int rows, int batch, int q_heads) {
   const int group = q_heads / c->kv_heads, D = c->head_dim;
   Plan pl = {m_tiles(rows, batch, group), 0, dev.sms, 0};
-  const long long items = max_items(rows, batch, 128 / group, c->kv_heads);
+  const int tok = 128 / group, each = (rows + batch - 1) / batch;
+  const long long items = (long long)batch * ((each + tok - 1) / tok) * c->kv_heads;  // of sequences of equal length
   const long long tiles = (((long long)c->max_pages << page_shift(c->page_size)) + KT - 1) / KT;  // of a sequence, at most
   // Few items over little cache: a cluster each, the largest that lets all run
-  // at once.  That saves the merge's launch, but leaves SMs idle.  Clusters
-  // against runs of equal length (us): a token over 100 positions 8.0 / 10.5,
-  // 16 over 2,048 11.8 / 14.9, a token over 8,192 15.9 / 16.6 (32 and 8 heads
-  // of 128: 8, 136 and 520 tiles); two of 16,000 with 4 KV heads 22.8 / 19.5,
-  // 16 over 32,000 39.9 / 35.6 (1,000 and 2,000 tiles).
+  // at once (those of unequal sequences may take a second round).  That saves
+  // the merge's launch, but leaves SMs idle.  Clusters against runs of equal
+  // length (us): a token over 100 positions 8.0 / 10.5, 16 over 2,048 11.8 /
+  // 14.9, 16 blocks over 3,000 with one KV head 17.0 / 20.1, 8 over 1,000 with 4
+  // 12.5 / 14.7, a token over 8,192 15.9 / 16.6 (8 to 520 tiles); two of 16,000
+  // with 4 KV heads 22.8 / 19.5, 16 over 32,000 39.9 / 35.6 (1,000 and 2,000
+  // tiles).  Pairs only over short caches: 16 tokens over 500 with 4 KV heads
+  // 10.9 / 13.0, but 24 blocks over up to 2,000 with 2 17.4 / 15.0.
   if (pl.nm == 1 && items * tiles <= CLUSTER_TILES) {
     int cs = 1;
     while (cs < MAX_CLUSTER && cs < tiles && items <= dev.clusters[2 * cs]) cs *= 2;
-    if (cs >= 4 || cs >= tiles) {
+    if (cs >= 4 || tiles <= 2 * cs) {
       pl.cs = cs;
-      pl.grid = (int)items * cs;
+      pl.grid = (int)max_items(rows, batch, tok, c->kv_heads) * cs;
     }
   }
   if (!pl.cs) pl.ws = workspace_bytes(dev.sms, pl.nm, D);
