@@ -85,7 +85,7 @@ struct PagedParams {
   int negate;         // the caller's scale is negative
   uint32_t* status;
   char* ws;
-  int cs;             // > 0: an item a cluster of cs CTAs, its shares joined over distributed shared memory
+  int cs;             // > 0: a cluster of cs CTAs an item, its shares joined over distributed shared memory
 };
 
 // Workspace: a header, one record a CTA, two partial slots a CTA.
@@ -553,52 +553,62 @@ DFL_DEV bool locate_cluster(const PagedParams& p, Sched* sc, Walk& w) {
 
 // Joins the shares that the CTAs of a cluster left in their shared memory:
 // O [128][D + 4] unnormalised, maxima [128], sums [128].  Each takes every
-// cs-th row, with the loads of all shares in flight.
+// cs-th row; a thread has the loads of CS shares of PIECES of 4 columns in flight.
 constexpr int MAX_CLUSTER = 16;
 constexpr long long CLUSTER_TILES = 640;  // key tiles that a call's tables can hold
-template <bool BF16, int D>
+template <bool BF16, int D, int CS, int PIECES>
 DFL_DEV void join_cluster(const PagedParams& p, const uint8_t* sm, int row0, int rows, int head0) {
   constexpr int PS = D + 4;
   const uint32_t at = smem_u32(sm);
   const int rank = (int)cluster_ctarank();
-  const int mine = (rows - rank + p.cs - 1) / p.cs;
-  for (int e = threadIdx.x; e < mine * (D / 4); e += blockDim.x) {
-    const int r = rank + e / (D / 4) * p.cs, d = e % (D / 4) * 4;
-    float m[MAX_CLUSTER], l[MAX_CLUSTER];
-    float4 o[MAX_CLUSTER];
+  const int all = (rows - rank + p.cs - 1) / p.cs * (D / 4);
+  for (int e0 = threadIdx.x; e0 < all; e0 += PIECES * blockDim.x) {
+    float m[PIECES][CS], l[PIECES][CS];
+    float4 o[PIECES][CS];
 #pragma unroll
-    for (int x = 0; x < MAX_CLUSTER; ++x) {
-      m[x] = -INFINITY;
-      l[x] = 0.f;
-      o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (x < p.cs) {
-        const uint32_t a = dsmem_addr(at, (uint32_t)x);
-        m[x] = ld_dsmem(a + 4u * (uint32_t)(128 * PS + r));
-        l[x] = ld_dsmem(a + 4u * (uint32_t)(128 * PS + 128 + r));
-        o[x] = ld_dsmem4(a + 4u * (uint32_t)(r * PS + d));
+    for (int i = 0; i < PIECES; ++i) {
+      const int e = min(e0 + i * (int)blockDim.x, all - 1);
+      const int r = rank + e / (D / 4) * p.cs, d = e % (D / 4) * 4;
+#pragma unroll
+      for (int x = 0; x < CS; ++x) {
+        m[i][x] = -INFINITY;
+        l[i][x] = 0.f;
+        o[i][x] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (x < p.cs) {
+          const uint32_t a = dsmem_addr(at, (uint32_t)x);
+          m[i][x] = ld_dsmem(a + 4u * (uint32_t)(128 * PS + r));
+          l[i][x] = ld_dsmem(a + 4u * (uint32_t)(128 * PS + 128 + r));
+          o[i][x] = ld_dsmem4(a + 4u * (uint32_t)(r * PS + d));
+        }
       }
     }
-    float M = -INFINITY, L = 0.f;
 #pragma unroll
-    for (int x = 0; x < MAX_CLUSTER; ++x)
-      if (l[x] != 0.f) M = fmaxf(M, m[x]);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < PIECES; ++i) {
+      const int e = e0 + i * (int)blockDim.x;
+      if (e >= all) break;
+      const int r = rank + e / (D / 4) * p.cs, d = e % (D / 4) * 4;
+      float M = -INFINITY, L = 0.f;
 #pragma unroll
-    for (int x = 0; x < MAX_CLUSTER; ++x) {
-      if (l[x] == 0.f) continue;  // a share without a key of the row, its O not written
-      const float wgt = ex2(m[x] - M);
-      L += wgt * l[x];
-      acc.x += wgt * o[x].x;
-      acc.y += wgt * o[x].y;
-      acc.z += wgt * o[x].z;
-      acc.w += wgt * o[x].w;
+      for (int x = 0; x < CS; ++x)
+        if (l[i][x] != 0.f) M = fmaxf(M, m[i][x]);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int x = 0; x < CS; ++x) {
+        if (l[i][x] == 0.f) continue;  // a share without a key of the row
+        const float wgt = ex2(m[i][x] - M);
+        L += wgt * l[i][x];
+        acc.x += wgt * o[i][x].x;
+        acc.y += wgt * o[i][x].y;
+        acc.z += wgt * o[i][x].z;
+        acc.w += wgt * o[i][x].w;
+      }
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+      const long long t = row0 + r / p.group, h = head0 + r % p.group;
+      *reinterpret_cast<uint2*>(p.out + t * p.o_row + h * p.o_head + d) =
+          make_uint2(pack16<BF16>(acc.x * inv, acc.y * inv), pack16<BF16>(acc.z * inv, acc.w * inv));
+      if (p.lse && d == 0)
+        p.lse[t * p.lse_row + h * p.lse_head] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
     }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    const long long t = row0 + r / p.group, h = head0 + r % p.group;
-    *reinterpret_cast<uint2*>(p.out + t * p.o_row + h * p.o_head + d) =
-        make_uint2(pack16<BF16>(acc.x * inv, acc.y * inv), pack16<BF16>(acc.z * inv, acc.w * inv));
-    if (p.lse && d == 0)
-      p.lse[t * p.lse_row + h * p.lse_head] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
   }
 }
 
@@ -1052,7 +1062,7 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
         if (!(ok = wait_o(it - 1))) break;
         tc_fence_after();
       }
-      const bool to_cluster = NM == 1 && in_cluster, whole = x.share == 0 && !to_cluster;
+      const bool to_cluster = NM == 1 && p.cs > 1, whole = x.share == 0 && !to_cluster;
       if (warp_valid || to_cluster) {
         // where the row's O goes: out, this CTA's share in the workspace, or
         // (the tile area being free: every load has been used) in shared memory
@@ -1120,9 +1130,11 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);
   }
-  if (NM == 1 && in_cluster && work) {  // the whole cluster's answer
+  if (NM == 1 && p.cs > 1 && work) {  // the whole cluster's answer
     cluster_sync_all();
-    join_cluster<BF16, D>(p, sm, w.s.row0 + w.t0, (w.t1 - w.t0) * p.group, w.kvh * p.group);
+    const int row0 = w.s.row0 + w.t0, rows = (w.t1 - w.t0) * p.group, head0 = w.kvh * p.group;
+    if (p.cs <= 4) join_cluster<BF16, D, 4, 4>(p, sm, row0, rows, head0);
+    else join_cluster<BF16, D, MAX_CLUSTER, 1>(p, sm, row0, rows, head0);
     cluster_sync_all();  // this CTA's share is there until every other has read it
   }
 }
@@ -1306,7 +1318,7 @@ Plan plan_call(const Device& dev, const dflash_paged_cache* c, int rows, int bat
   if (pl.nm == 1 && items * tiles <= CLUSTER_TILES) {
     int cs = 1;
     while (cs < MAX_CLUSTER && cs < tiles && items <= dev.clusters[2 * cs]) cs *= 2;
-    if (cs >= 4 || tiles <= 2 * cs) {
+    if (items <= dev.sms && (cs >= 4 || tiles <= 2 * cs)) {
       pl.cs = cs;
       pl.grid = (int)max_items(rows, batch, tok, c->kv_heads) * cs;
     }

@@ -294,6 +294,34 @@ def test_attention_runs_of_many_small_items_end_alike(ops):
     assert torch.equal(got, out) and pg.cache.read_status() == 0
 
 
+def test_attention_of_many_token_tiles(ops):
+    """More token tiles than a CTA has threads: of one sequence, and of more sequences than threads."""
+    check_attention(ops, (32, 1, 64), [3000], [5], BF16)
+    rows = [33 + i % 18 for i in range(400)]
+    check_attention(ops, (8, 2, 64), rows, [(i * 53) % 200 for i in range(400)], F16)
+
+
+@pytest.mark.parametrize("heads,rows,ctx", [((8, 2, 128), [1, 16, 5], [1000, 700, 64]), ((4, 1, 64), [200, 3], [900, 1500]),
+                                            ((8, 2, 128), [1] * 90, [800] * 90)])
+def test_attention_needs_no_page_before_its_window(ops, heads, rows, ctx):
+    """Pages that every row's window has left are gone from the table and hold NaN."""
+    window, page = 150, 64
+    hq, hkv, dim = heads
+    lens = [a + b for a, b in zip(rows, ctx)]
+    pg = Paged(ops, lens, hkv, dim, page, BF16)
+    cu = i32([sum(rows[:i]) for i in range(len(rows) + 1)])
+    q = torch.randn(sum(rows), hq, dim, generator=gen(4), device="cuda").to(BF16)
+    want = ops.attention(pg.cache, q, cu, i32(ctx), window=window)
+    for b, c in enumerate(ctx):
+        gone = max(c - window + 1, 0) // page  # pages below the first row's first key
+        ids = pg.table[b, :gone].long()
+        pg.kp[ids] = math.nan
+        pg.vp[ids] = math.nan
+        pg.table[b, :gone] = -1
+    assert torch.equal(ops.attention(pg.cache, q, cu, i32(ctx), window=window), want)
+    assert pg.cache.read_status() == 0
+
+
 def test_attention_of_nothing(ops):
     pg = Paged(ops, [5], 2, 64, 64, BF16)
     out = ops.attention(pg.cache, torch.zeros(0, 4, 64, dtype=BF16, device="cuda"), i32([0, 0]), i32([5]))
