@@ -60,9 +60,9 @@ namespace {
 constexpr int KT = 128;  // keys of a tile
 // What an item costs beside its tiles, in tiles: the load of Q, the first and
 // last tile that overlap nothing, the output.  Measured with 1, 2 and 3 (us):
-// a prompt of 8,192 430 / 393 / 396, a window of 1,024 155 / 153 / 153, ragged
-// prompts of 64-wide heads 62.6 / 60.0 / 62.2; NM = 1 with 0, 1 and 2: blocks
-// of 24 requests 16.9 / 15.4 / 15.3, a token each for 64 105.7 / 104.7 / 104.5.
+// a prompt of 8,192 428 / 357 / 358, a window of 1,024 146 / 142 / 142, ragged
+// prompts of 64-wide heads 61.4 / 57.9 / 59.7; NM = 1 with 0, 1 and 2: blocks
+// of 24 requests 16.2 / 14.8 / 14.6, a token each for 64 103.5 / 102.7 / 103.4.
 template <int NM>
 constexpr int SETUP = NM == 2 ? 2 : 1;
 
@@ -79,7 +79,7 @@ struct PagedParams {
   const int* cu;
   const int* ctx;
   const int* kv_len;
-  int rows, batch, hq, hkv, group, causal, window;
+  int rows, batch, hkv, group, causal, window;
   int tok;            // tokens of an M tile
   float scale_log2;   // > 0
   int negate;         // the caller's scale is negative
@@ -103,7 +103,6 @@ struct WsCta {
 constexpr size_t ws_records(int grid) { return 256 + ((size_t)grid * sizeof(WsCta) + 255) / 256 * 256; }
 // One slot: O [D/4][rows] float4, running maxima [rows], sums [rows].
 constexpr size_t ws_slot_floats(int rows, int D) { return (size_t)rows * (D + 2); }  // a multiple of 4
-
 
 // The MMAs of a whole tile under one elect.sync: with one for each MMA the
 // issuing warp is what the tensor core waits for.
@@ -1399,7 +1398,6 @@ int dflash_paged_attention(const dflash_paged_cache* c, const dflash_attention_a
   p.kv_len = a->kv_len;
   p.rows = a->rows;
   p.batch = a->batch;
-  p.hq = a->q_heads;
   p.hkv = c->kv_heads;
   p.group = group;
   p.causal = a->causal != 0;
