@@ -181,8 +181,14 @@ struct PCfg {
   static constexpr int OFF_ITEM = OFF_BAR + 576;     // the loading warp's notes of the next items
   static constexpr int SMEM = 1024 + OFF_ITEM + 128;  // + 1024 for aligning the base
   static constexpr int THREADS = 128 * NM + 64;
-  static constexpr int S_COL = 0;                    // two S buffers of 128 columns
-  static constexpr int O_COL = 256;
+  // S buffers of 128 columns.  AHEAD: one more than M tiles, taken in turn in
+  // issue order, so that S of an M tile's next key tile is there when the
+  // softmax of this one ends.  Two 128-wide O leave no room for it: there each M
+  // tile has its buffer, and S follows the O MMA whose P it overwrites.
+  static constexpr int S_BUFS = D == 64 && NM == 2 ? 3 : 2;
+  static constexpr bool AHEAD = S_BUFS > NM;
+  static constexpr int S_COL = 0;
+  static constexpr int O_COL = 128 * S_BUFS;
   static constexpr uint32_t TMEM_COLS = 512;
 };
 
@@ -621,9 +627,9 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::OFF_BAR);
   uint64_t* full = bars;                // [SLOTS] tile landed
   uint64_t* empty = full + C::SLOTS;    // [SLOTS] tile's MMAs done
-  uint64_t* s_full = empty + C::SLOTS;  // [2] S (and every MMA before it) done
-  uint64_t* p_full = s_full + 2;        // [2] P written
-  uint64_t* o_done = p_full + 2;        // [2] an O MMA done: of M tile m, or (NM = 1) of tiles of one parity
+  uint64_t* s_full = empty + C::SLOTS;  // [2 m + i & 1] S i of M tile m (and every MMA before it) done
+  uint64_t* p_full = s_full + 4;        // [2] P written: of M tile m, or (NM = 1) of tiles of one parity
+  uint64_t* o_done = p_full + 2;        // [2] an O MMA done, likewise
   uint64_t* o_empty = o_done + 2;       // [2] O read out
   uint64_t* q_full = o_empty + 2;       // [QBUFS]
   uint64_t* q_empty = q_full + 2;
@@ -633,7 +639,7 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(item_empty + ITEMS);
   Sched* sched = reinterpret_cast<Sched*>(sm + C::OFF_BAR + 384);
   Item* items = reinterpret_cast<Item*>(sm + C::OFF_ITEM);
-  static_assert((2 * C::SLOTS + 13 + 2 * ITEMS) * 8 + 8 <= 384 && sizeof(Sched) <= 192 && sizeof(Item) * ITEMS == 128,
+  static_assert((2 * C::SLOTS + 15 + 2 * ITEMS) * 8 + 8 <= 384 && sizeof(Sched) <= 192 && sizeof(Item) * ITEMS == 128,
                 "barrier area");
 
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -644,7 +650,8 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
       mbar_init(empty + i, 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(s_full + i, 1);
+      mbar_init(s_full + 2 * i, 1);
+      mbar_init(s_full + 2 * i + 1, 1);
       mbar_init(p_full + i, 4);
       mbar_init(o_done + i, 1);
       mbar_init(o_empty + i, 4);
@@ -818,14 +825,10 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
     int seg = 0;
     Ring<C::SLOTS> kr, vr;  // the next tile of K and of V
     vr.next();
-    uint32_t p_phase = 0;        // bit b: phase of the next P of S buffer b
-    int it = 0;                  // NM = 1: S tiles issued
+    int sb = 0, pb = 0;          // S buffer of the next S and of the next P
+    uint32_t s_odd = 0;          // bit m: parity of M tile m's next S
+    uint32_t p_phase = 0;        // bit b: phase of the next P on barrier b
     int sg[2] = {0, 0};          // segments of each M tile
-    auto issue_s = [&](int m, int buf, int qb, int slot) {
-      const uint64_t qd = q_desc + (uint64_t)((qb * NM + m) * (C::TILE >> 4)), kd = k_desc + (uint64_t)(slot * (C::TILE >> 4));
-      tc_mma_s<D>(tmem + (uint32_t)(C::S_COL + 128 * buf), qd, kd, idesc_s);
-      tc_commit_elect(s_full + buf);
-    };
     bool ok = true;
     int taken = 0;
     Item x;
@@ -837,31 +840,36 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
       if (!wait_all(q_full + qb, (uint32_t)((seg / C::QBUFS) & 1)) || !wait_all(full + kr.s, kr.phase)) break;
       ++seg;
       tc_fence_after();
-      // S of the first tile.  NM = 2: S of a tile follows the O MMA of the one
-      // before, whose P it overwrites; NM = 1: it runs ahead of it, into the other buffer.
-      for (int m = 0; m < nm; ++m) issue_s(m, NM == 2 ? m : it & 1, qb, kr.s);
-      ++it;
-      tc_commit_elect(empty + kr.s);
-      kr.next();
-      kr.next();
-      if (tiles == 1) tc_commit_elect(q_empty + qb);
-      // keys of the sequence behind the start of its last tile, if that tile ends inside a page
-      const int last_v = x.kv - x.key0 - (tiles - 1) * KT;
-      for (int j = 0; j < tiles && ok; ++j) {
-        const bool more = j + 1 < tiles;
-        const int buf1 = NM == 1 ? it - 1 & 1 : 0;
-        if (NM == 1 && more) {
-          if (!(ok = wait_all(full + kr.s, kr.phase))) break;
+      // S of M tile m's key tile j.  The first of each M tile, and with AHEAD one
+      // more, go before the first O MMA; every other follows one.
+      auto issue_s = [&](int m, int j) {
+        if (m == 0 && j > 0) {
+          if (!wait_all(full + kr.s, kr.phase)) return false;
           tc_fence_after();
-          issue_s(0, it & 1, qb, kr.s);
-          ++it;
+        }
+        const int buf = C::AHEAD ? sb : m;
+        tc_mma_s<D>(tmem + (uint32_t)(C::S_COL + 128 * buf), q_desc + (uint64_t)((qb * NM + m) * (C::TILE >> 4)),
+                    k_desc + (uint64_t)(kr.s * (C::TILE >> 4)), idesc_s);
+        tc_commit_elect(s_full + 2 * m + (C::AHEAD ? s_odd >> m & 1u : 0u));
+        if (C::AHEAD) {
+          s_odd ^= 1u << m;
+          sb = sb + 1 == C::S_BUFS ? 0 : sb + 1;
+        }
+        if (m == nm - 1) {
           tc_commit_elect(empty + kr.s);
           kr.next();
           kr.next();
-          if (j + 2 == tiles) tc_commit_elect(q_empty + qb);
+          if (j + 1 == tiles) tc_commit_elect(q_empty + qb);
         }
+        return true;
+      };
+      for (int m = 0; m < nm; ++m) issue_s(m, 0);
+      if (C::AHEAD && tiles > 1 && !(ok = issue_s(0, 1))) break;
+      // keys of the sequence behind the start of its last tile, if that tile ends inside a page
+      const int last_v = x.kv - x.key0 - (tiles - 1) * KT;
+      for (int j = 0; j < tiles && ok; ++j) {
         if (!(ok = wait_all(full + vr.s, vr.phase))) break;
-        if (!more && last_v < KT && (last_v & ((1 << p.shift) - 1))) {
+        if (j + 1 == tiles && last_v < KT && (last_v & ((1 << p.shift) - 1))) {
           // the sequence ends inside a page: what lies behind it (stale,
           // perhaps not finite) must not meet P's zeros in the MMA
           const int v1 = min(KT, ((last_v >> p.shift) + 1) << p.shift);
@@ -874,27 +882,17 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
         }
         const uint64_t vd = v_desc + (uint64_t)(vr.s * (C::TILE >> 4));
         for (int m = 0; m < nm; ++m) {
-          const int buf = NM == 2 ? m : buf1;
           if (j == 0 && sg[m]++ > 0 && !(ok = wait_all(o_empty + m, (uint32_t)((sg[m] - 2) & 1)))) break;
-          if (!(ok = wait_all(p_full + buf, p_phase >> buf & 1u))) break;
+          const int buf = C::AHEAD ? pb : m, bar = NM == 2 ? m : pb;
+          if (!(ok = wait_all(p_full + bar, p_phase >> bar & 1u))) break;
           tc_fence_after();
           tc_mma_o(tmem + (uint32_t)(C::O_COL + D * m), tmem + (uint32_t)(C::S_COL + 128 * buf), vd, idesc_o, j > 0 ? 1u : 0u);
-          p_phase ^= 1u << buf;
-          tc_commit_elect(o_done + buf);
+          p_phase ^= 1u << bar;
+          if (C::AHEAD) pb = pb + 1 == C::S_BUFS ? 0 : pb + 1;
+          tc_commit_elect(o_done + bar);
           if (m == nm - 1) tc_commit_elect(empty + vr.s);
-          if (NM == 2 && more) {
-            if (m == 0) {
-              if (!(ok = wait_all(full + kr.s, kr.phase))) break;
-              tc_fence_after();
-            }
-            issue_s(m, m, qb, kr.s);
-            if (m == nm - 1) {
-              tc_commit_elect(empty + kr.s);
-              kr.next();
-              kr.next();
-              if (j + 2 == tiles) tc_commit_elect(q_empty + qb);
-            }
-          }
+          const int n = !C::AHEAD ? m : m + 1 == nm ? 0 : m + 1, nj = C::AHEAD && n == 0 ? j + 2 : j + 1;
+          if (nj < tiles && !(ok = issue_s(n, nj))) break;
         }
         vr.next();
         vr.next();
@@ -913,19 +911,25 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
     int it = 0;  // S tiles of this M tile
     bool ok = true;
     // The O MMA of S tile i, and with it every one before.  A barrier tells
-    // only whether one phase is over, so it must never be two ahead of a
-    // waiting warp: NM = 2 waits after S i, which follows the O MMA of i - 1 on
-    // the tensor core; NM = 1, whose S runs a tile ahead, has a barrier for
-    // each parity.  The next O MMA on either needs this warp's P.
+    // only whether one phase is over, so it may be neither two ahead of who
+    // waits nor two behind.  NM = 2: every warp knows O i done before it gives
+    // P i + 1: from S i + 1, which follows it, or, where S runs ahead, by waiting
+    // each time.  NM = 1 has a barrier for each parity of P and O instead and
+    // waits for O only where it moves (each time: 8,192 positions 14.8 -> 15.3 us).
+    constexpr bool EACH = NM == 2 && C::AHEAD;
     auto wait_o = [&](int i) {
       return NM == 2 ? wait_all(o_done + m, (uint32_t)(i & 1)) : wait_all(o_done + (i & 1), (uint32_t)((i >> 1) & 1));
     };
+    int sb0 = 0;  // S buffer of the item's first S tile
     int taken = 0;
     Item x;
     while (next_item(taken, x)) {
       const int tiles = x.tiles;
       const int tm = m * p.tok + rt;  // the row's token in the item
-      if (NM == 2 && m == 1 && x.tokens <= p.tok) continue;  // no row in this M tile
+      const int nm = NM == 2 && x.tokens > p.tok ? 2 : 1;
+      int buf = C::AHEAD ? (sb0 + m) % C::S_BUFS : m;
+      sb0 = (sb0 + tiles * nm) % C::S_BUFS;
+      if (m >= nm) continue;  // no row in this M tile
       const bool valid = rt < p.tok && tm < x.tokens;
       const bool warp_valid = __any_sync(0xffffffffu, valid);
       // the keys this row sees; rows that do not exist mask nothing (they are not written)
@@ -937,11 +941,12 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
       }
       float m_run = -INFINITY, l_run = 0.f;
       for (int j = 0; j < tiles; ++j, ++it) {
-        const int buf = NM == 2 ? m : it & 1;
-        const uint32_t par = (uint32_t)((NM == 2 ? it : it >> 1) & 1);
-        if (!(ok = wait_all(s_full + buf, par))) break;
+        if (!(ok = C::AHEAD ? wait_all(s_full + 2 * m + (it & 1), (uint32_t)(it >> 1 & 1))
+                            : wait_all(s_full + 2 * m, (uint32_t)(it & 1))))
+          break;
         tc_fence_after();
         const uint32_t s_base = lane_base + (uint32_t)(C::S_COL + 128 * buf);
+        if (C::AHEAD) buf = buf + nm < C::S_BUFS ? buf + nm : buf + nm - C::S_BUFS;
         if (warp_valid) {
           const int key0 = x.key0 + j * KT;
           const int h = hi - key0, l = lo - key0;
@@ -994,6 +999,7 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
             take(sy);
             mx = max3(fmaxf(m0, m1), m2, m3) * p.scale_log2;
           }
+          if (EACH && !(ok = wait_o(it - 1))) break;
           const bool move = mx > m_run + 8.f;
           if (__any_sync(0xffffffffu, move)) {
             const float m_new = move ? mx : m_run;
@@ -1050,10 +1056,12 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
           unpack_f32x2(add_f32x2(sum0, sum1), a, b);
           l_run += a + b;
           tmem_wait_st();
+        } else if (EACH && !(ok = wait_o(it - 1))) {
+          break;
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + buf);
+        if (lane == 0) mbar_arrive(p_full + (NM == 2 ? m : it & 1));
       }
       if (!ok) break;
       // the segment's O
