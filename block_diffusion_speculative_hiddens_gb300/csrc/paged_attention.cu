@@ -36,8 +36,13 @@
 //   PFLOP/s, 0.84 of the cuBLAS burst rate); a whole prompt of 8,192 360 us.  A
 //   tile's two S and O MMAs are 2,048 cycles, and a tile takes 2,800: what a
 //   row's softmax takes from S to P, and the hand-overs between it, the
-//   issuing warp and the tensor core, which leave that idle in between.
-//   Without any exponential the chunk takes 624 us and 64-wide heads 12 % less.
+//   issuing warp and the tensor core, which leave that idle in between (tensor
+//   pipe 0.74, issue slots 0.40).
+// - The same chunk at 64 wide 480 us, a tile 2,300 cycles: S runs a tile ahead
+//   there (537 without), and what is left is the softmax's own instructions in
+//   sequence (issue slots 0.51, exponentials 0.45, tensor pipe 0.45).
+// - Without any exponential the chunks take 648 (for 662 in that run) and 466 us;
+//   one in four by a polynomial of degree 3 instead 712 and 587.
 // - What moved it (chunk, us): softmax in short loops over TMEM 904 -> 733, one
 //   elect.sync a tile, counted ring places 730 -> 708, 64 columns of S in
 //   flight 708 -> 688 (first pass) and 666 -> 641 (second), warp-uniform values
