@@ -294,6 +294,20 @@ def test_attention_runs_of_many_small_items_end_alike(ops):
     assert torch.equal(got, out) and pg.cache.read_status() == 0
 
 
+@pytest.mark.parametrize("heads", [(8, 2, 64), (16, 2, 128), (5, 5, 64)], ids=["d64", "d128", "d64_mha"])
+def test_attention_of_items_with_one_and_two_m_tiles_in_turn(ops, heads):
+    """Runs that mix items of one and of two M tiles, of one key tile and of
+    several: the output is right, the same in 100 calls, and no wait runs out."""
+    tok = 128 * heads[1] // heads[0]
+    lens = [1, 2 * tok, tok, tok + 1, 3 * tok, 0, 5, 2 * tok + 1, 4 * tok]
+    rows, ctx = [lens[i % 9] for i in range(90)], [(i * 131) % 1100 for i in range(90)]
+    pg, q, out = check_attention(ops, heads, rows, ctx, BF16)
+    cu, cx = i32([sum(rows[:i]) for i in range(91)]), i32(ctx)
+    for _ in range(100):
+        got = ops.attention(pg.cache, q, cu, cx)
+    assert torch.equal(got, out) and pg.cache.read_status() == 0
+
+
 def test_attention_of_many_token_tiles(ops):
     """More token tiles than a CTA has threads: of one sequence, and of more sequences than threads."""
     check_attention(ops, (32, 1, 64), [3000], [5], BF16)
