@@ -16,7 +16,8 @@ The C entry points, their argument structs, limits and device-side checks are
 in include/dflash.h; this module checks the tensors (ValueError) and passes
 their pointers and strides.  Calls go to the current stream of the tensors'
 device (or `stream`), enqueue and return, and may be captured into a graph;
-outputs that are not given are allocated on that stream.
+outputs that are not given are allocated on that stream, those that are given
+overlap nothing else of the call (beyond what a call allows) nor themselves.
 """
 from __future__ import annotations
 
@@ -122,15 +123,29 @@ def _i32(t, what, n, device):
     return t.data_ptr()
 
 
+def _meet(x, y):
+    """Whether two 16-bit views share an element; views of one buffer may
+    interleave without meeting: heads of the same rows."""
+    a, b = x.data_ptr(), y.data_ptr()
+    ea = a + 2 * (1 + sum((n - 1) * s for n, s in zip(x.shape, x.stride())))
+    eb = b + 2 * (1 + sum((n - 1) * s for n, s in zip(y.shape, y.stride())))
+    return a < eb and b < ea and not _disjoint_heads(x, y)
+
+
 def _no_overlap(out, src, what):
-    """An output is its input itself, or apart from it."""
-    if out.data_ptr() != src.data_ptr() or out.stride() != src.stride():
-        a, b = out.data_ptr(), src.data_ptr()
-        ea = a + 2 * (1 + sum((n - 1) * s for n, s in zip(out.shape, out.stride())))
-        eb = b + 2 * (1 + sum((n - 1) * s for n, s in zip(src.shape, src.stride())))
-        # views of one buffer may interleave without meeting: heads of the same rows
-        if a < eb and b < ea and not _disjoint_heads(out, src):
-            raise ValueError(f"{what}: overlaps its input without being it")
+    """An output is its input itself, or apart from it; its heads of all rows lie apart from one another."""
+    near, far = sorted((s, n) for s, n in zip(out.stride()[:2], out.shape[:2]))
+    if near[1] > 1 and near[0] < out.shape[2] or \
+            far[1] > 1 and far[0] < out.shape[2] + (near[1] - 1) * near[0]:
+        raise ValueError(f"{what}: rows and heads overlap one another, strides {list(out.stride())}")
+    if (out.data_ptr() != src.data_ptr() or out.stride() != src.stride()) and _meet(out, src):
+        raise ValueError(f"{what}: overlaps its input without being it")
+
+
+def _apart(out, other, what, name):
+    """An output that the caller gave lies apart from what else the call reads or writes."""
+    if _meet(out, other):
+        raise ValueError(f"{what}: overlaps {name}")
 
 
 def _disjoint_heads(x, y):
@@ -171,8 +186,7 @@ def _out(out, src, rows, heads, dim, what, dtype, device, stream):
         out = _empty((rows, heads, dim), dtype, src, stream)
         return out, (out.data_ptr(), heads * dim, dim)
     at = _rows(out, what, dtype, device, rows, heads, dim)
-    if out is not src:
-        _no_overlap(out, src, what)
+    _no_overlap(out, src, what)
     return out, at
 
 
@@ -193,12 +207,19 @@ def rope(plan: RopePlan, q, k, positions, *, backward: bool = False, q_out=None,
     raw = _raw_stream(stream, device)
     qs = _rows(q, "q", dtype, device)
     rows, hq, dim = q.shape
+    given_q, given_k = q_out is not None, k_out is not None
     q_out, qo = _out(q_out, q, rows, hq, dim, "q_out", dtype, device, stream)
     ks, ko, hk = _NONE, _NONE, 0
     if k is not None:
         ks = _rows(k, "k", dtype, device, rows, None, dim)
         hk = k.shape[1]
         k_out, ko = _out(k_out, k, rows, hk, dim, "k_out", dtype, device, stream)
+        if given_q:
+            _apart(q_out, k, "q_out", "k")
+        if given_k:
+            _apart(k_out, q, "k_out", "q")
+            if given_q:
+                _apart(q_out, k_out, "q_out", "k_out")
     args = _ROPE.pack(*qs, *ks, *qo, *ko, _i32(positions, "positions", rows, device), rows, hq, hk, dim, _DTYPES[dtype],
                       bool(backward), device)
     code = load().dflash_rope(plan._ref, args, raw)
@@ -265,6 +286,9 @@ def append(cache: PagedCache, k, v, cu_rows, ctx_len, *, plan: RopePlan = None, 
     if q is not None:
         qs = _rows(q, "q", dtype, device, rows, None, dim)
         hq = q.shape[1]
+        if q_out is not None:
+            _apart(q_out, k, "q_out", "k")
+            _apart(q_out, v, "q_out", "v")
         q_out, qo = _out(q_out, q, rows, hq, dim, "q_out", dtype, device, stream)
     args = _APPEND.pack(*ks, *vs, *qs, *qo, cu, ctx, rows, b, hq, 0)
     code = load().dflash_paged_append(cache._c, None if plan is None else plan._ref, args, raw)
@@ -293,8 +317,7 @@ def attention(cache: PagedCache, q, cu_rows, ctx_len, *, kv_len=None, causal: bo
         os_ = out.data_ptr(), hq * dim, dim
     else:
         os_ = _rows(out, "out", dtype, device, rows, hq, dim)
-        if out is not q:
-            _no_overlap(out, q, "out")
+        _no_overlap(out, q, "out")
     ls = _NONE
     if lse is not None:
         if lse.dtype is not torch.float32 or lse.get_device() != device or tuple(lse.shape) != (rows, hq):

@@ -489,8 +489,9 @@ DFLASH_API int dflash_rope_init(const dflash_rope_config* cfg, dflash_rope_plan*
 /* Rotate the heads of q and (data non-null) k at positions[t] (DEVICE int32
  * [rows]): the first rotary_dim dims of a head by the plan, the others copied.
  * Any alignment and strides; an output may be its own input (same pointer and
- * strides) and must not overlap it otherwise.  backward = 1 applies the
- * transposed map: the gradient of the inputs from the gradient of the outputs. */
+ * strides) and must overlap neither it otherwise nor the other tensors or
+ * itself.  backward = 1 applies the transposed map: the gradient of the inputs
+ * from the gradient of the outputs. */
 typedef struct dflash_rope_args {
   dflash_rows q, k, q_out, k_out;
   const int32_t* positions;
@@ -538,7 +539,7 @@ DFLASH_API int dflash_paged_append(const dflash_paged_cache* cache, const dflash
  * causal also j <= position, with window w > 0 also j > position - w.  Query
  * head h reads KV head h / (q_heads / kv_heads).  A row that sees no position
  * gets out 0 and lse -inf.  out may be q (same pointer and strides) and must
- * not overlap it otherwise.  lse (optional, float32 [rows][q_heads], strides of
+ * overlap neither it otherwise nor the cache or itself.  lse (optional, float32 [rows][q_heads], strides of
  * its own): the natural logarithm of the row's sum of exponentials.  Only
  * pages that hold a seen position are read, and of the last of them nothing
  * behind kv_len reaches the result; a non-finite value within kv_len reaches

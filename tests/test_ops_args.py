@@ -179,7 +179,7 @@ def _attention(**kw):
 
 
 def _append(**kw):
-    a = dict(k=FakeT([7, 2, 128]), v=FakeT([7, 2, 128]), cu=FakeT([4], I32), ctx=FakeT([3], I32),
+    a = dict(k=FakeT([7, 2, 128], ptr=1 << 28), v=FakeT([7, 2, 128], ptr=1 << 29), cu=FakeT([4], I32), ctx=FakeT([3], I32),
              q=FakeT([7, 4, 128]), q_out=FakeT([7, 4, 128], ptr=1 << 30), stream=Stream())
     a.update(kw)
     return ops.append(_cache(), a.pop("k"), a.pop("v"), a.pop("cu"), a.pop("ctx"), **a)
@@ -188,7 +188,7 @@ def _append(**kw):
 def _rope(**kw):
     class P:
         _ref = None
-    a = dict(q=FakeT([7, 4, 128]), k=FakeT([7, 2, 128]), positions=FakeT([7], I32),
+    a = dict(q=FakeT([7, 4, 128]), k=FakeT([7, 2, 128], ptr=1 << 28), positions=FakeT([7], I32),
              q_out=FakeT([7, 4, 128], ptr=1 << 30), k_out=FakeT([7, 2, 128], ptr=1 << 31), stream=Stream())
     a.update(kw)
     return ops.rope(P(), a.pop("q"), a.pop("k"), a.pop("positions"), **a)
@@ -210,9 +210,33 @@ def test_q_and_k_views_of_one_projection_rotate_in_place_and_apart(calls):
     qkv = dict(stride=(8 * 128, 128, 1))
     q, k = FakeT([7, 4, 128], **qkv), FakeT([7, 2, 128], ptr=0x100000 + 4 * 256, **qkv)
     _rope(q=q, k=k, q_out=q, k_out=k)
-    _rope(q=q, k=k, q_out=FakeT([7, 4, 128], ptr=0x100000 + 4 * 256, **qkv), k_out=k)  # other heads of the same rows
-    with pytest.raises(ValueError, match="overlaps"):
-        _rope(q=q, k=k, q_out=FakeT([7, 4, 128], ptr=0x100000 + 2 * 256, **qkv), k_out=k)
+    wide = dict(stride=(12 * 128, 128, 1))
+    q, k, far = FakeT([7, 4, 128], **wide), *(FakeT([7, n, 128], ptr=0x100000 + h * 256, **wide) for n, h in ((2, 4), (4, 8)))
+    _rope(q=q, k=k, q_out=far, k_out=k)  # other heads of the same rows
+    for kw in (dict(q_out=FakeT([7, 4, 128], ptr=0x100000 + 2 * 256, **wide)),  # half of q
+               dict(q_out=FakeT([7, 4, 128], ptr=0x100000 + 5 * 256, **wide)),  # half of k
+               dict(k_out=FakeT([7, 2, 128], ptr=0x100000 + 3 * 256, **wide)),
+               dict(q_out=far, k_out=FakeT([7, 2, 128], ptr=0x100000 + 9 * 256, **wide))):
+        with pytest.raises(ValueError, match="overlaps"):
+            _rope(q=q, k=k, **kw)
+    for name in "kv":
+        kw = {name: FakeT([7, 2, 128], ptr=(1 << 30) + 512)}
+        with pytest.raises(ValueError, match="q_out: overlaps [kv]$"):
+            _append(**kw)
+
+
+def test_outputs_that_overlap_themselves_are_refused(calls):
+    for s in ((0, 128, 1), (512, 0, 1), (512, 64, 1), (256, 128, 1), (128, 512, 1)):
+        out = FakeT([7, 4, 128], stride=s, ptr=1 << 30)
+        for call in (lambda: _rope(q_out=out), lambda: _append(q_out=out), lambda: _attention(out=out)):
+            with pytest.raises(ValueError, match="one another"):
+                call()
+        with pytest.raises(ValueError, match="one another"):
+            _attention(q=out, out=out)
+    for shape, s in (([7, 4, 128], (128, 7 * 128, 1)), ([1, 4, 128], (0, 128, 1)), ([7, 4, 128], (4096, 136, 1))):
+        q = FakeT(shape)
+        _attention(q=q, out=FakeT(shape, stride=s, ptr=1 << 30))
+        _rope(q=q, k=None, k_out=None, q_out=FakeT(shape, stride=s, ptr=1 << 30), positions=FakeT([shape[0]], I32))
 
 
 BAD = [FakeT([7, 4, 128], torch.float16), FakeT([7, 4, 128], device="cuda:1"), FakeT([7, 4, 128], device="cpu"),
