@@ -15,9 +15,11 @@
 //
 // Bound by memory: each value is read and written once.  8,191 rows of 40
 // heads of 128 (168 MB) take 27.4 us, 6.1 TB/s, 0.90 of the copy rate; 7,500
-// rows appended with their queries (184 MB) 35.2 us, 5.2 TB/s.  A row a CTA with
-// two units of a thread in flight: four rows a CTA took 29.4 and 37.5 us, one
-// or three units in flight 31.3 and 29.6.  A call of 16 rows is 2.5 us of
+// rows appended with their queries (184 MB) 33.4 us, 5.5 TB/s (35.1 with the page
+// looked up by a warp that also computes angles; 32.9, but 3.3 for 3.2 us for 64
+// single rows, with every thread looking up its own).  A row a CTA with two units
+// of a thread in flight: four rows a CTA took 29.4 and 37.5 us, one or three
+// units in flight 31.3 and 29.6.  A call of 16 rows is 2.5 us of
 // launch, load, angles and store.
 #include <algorithm>
 #include <cmath>
@@ -176,8 +178,9 @@ __global__ void __launch_bounds__(ROPE_THREADS) k_rope(const __grid_constant__ R
       if (!w.valid && lane == 0) place[r] = w;
     }
     __syncthreads();
-    if (threadIdx.x < nr && place[threadIdx.x].valid) {
-      RowPlace& w = place[threadIdx.x];
+    const int mine = blockDim.x - 1 - threadIdx.x;  // by the last threads: the first ones have the angles
+    if (mine < nr && place[mine].valid) {
+      RowPlace& w = place[mine];
       const long long pi = w.pos >> p.page_shift;
       const int pg = w.pos >= 0 && pi < p.max_pages ? p.table[w.seq * p.table_stride + pi] : -1;
       if (pg >= 0 && pg < p.n_pages) {
