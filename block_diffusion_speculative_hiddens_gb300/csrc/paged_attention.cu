@@ -758,9 +758,10 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
                        (int)min(max(w.s.ctx + w.t0, -(long long)far), (long long)far), w.s.kv, w.kvh,
                        tiles == w.span.tiles ? 0 : w.off == 0 ? 1 : 2})))
         break;
-      if (tiles == 0) continue;
+      // also of an item without a tile: its window may lie past what the table holds
       if (lane == 0 && (p.kv_len ? (long long)p.kv_len[w.b] : w.s.ctx + w.s.n) > p.cap)
         dev_error(p.status, DFLASH_DEV_PAGE);
+      if (tiles == 0) continue;
       auto load_q = [&] {
         const int qb = seg % C::QBUFS;
         if (seg >= C::QBUFS && !wait_all(q_empty + qb, (uint32_t)((seg / C::QBUFS - 1) & 1))) return false;

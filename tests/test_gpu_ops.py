@@ -611,3 +611,27 @@ def test_calls_on_two_streams_at_once(ops):
     torch.cuda.synchronize()
     for i, (_, want, _) in enumerate(jobs):
         assert all(torch.equal(x, want) for x in got[i])
+
+
+# ------------------------------------------------------------------ the status word
+
+@pytest.mark.parametrize("heads,rows,ctx", [((4, 2, 128), [1, 3], [199, 8000]), ((32, 8, 64), [1] * 40, [199] * 39 + [8000]),
+                                            ((4, 1, 128), [300, 200], [0, 8000])], ids=["clusters", "runs", "runs of two M tiles"])
+def test_attention_whose_window_lies_past_the_table_says_so(ops, heads, rows, ctx):
+    """The last sequence sees no position the table can hold: no tile of work, and reported all the same."""
+    from block_diffusion_speculative_hiddens_gb300.binding import DEV_PAGE
+    hq, hkv, dim = heads
+    lens = [a + b for a, b in zip(rows[:-1], ctx[:-1])] + [200]
+    pg = Paged(ops, lens, hkv, dim, 64, BF16, extra_cols=8)
+    q = torch.randn(sum(rows), hq, dim, generator=gen(1), device="cuda").to(BF16)
+    cu = i32([sum(rows[:i]) for i in range(len(rows) + 1)])
+    out, lse = torch.ones_like(q), torch.ones(sum(rows), hq, device="cuda")
+    ops.attention(pg.cache, q, cu, i32(ctx), window=1024, out=out, lse=lse)
+    assert pg.cache.read_status() == DEV_PAGE
+    assert (out[-rows[-1]:] == 0).all() and torch.isneginf(lse[-rows[-1]:]).all()
+    for b, n in enumerate(rows[:-1]):  # the other sequences are right
+        r = slice(sum(rows[:b]), sum(rows[:b + 1]))
+        o, l, mag, ds, seen = ops_ref.attention(q[r], pg.k[b], pg.v[b], ctx[b], lens[b], True, 1024, dim ** -0.5)
+        to, tl = ops_ref.attention_tolerance(o, l, mag, ds, seen, BF16, dim, pg.v[b].abs().max().item())
+        close(out[r], o, to, ("out", b))
+        close(lse[r], l, tl, ("lse", b))
