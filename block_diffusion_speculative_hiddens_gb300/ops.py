@@ -247,6 +247,12 @@ class PagedCache:
                 page_table.stride(1) != 1:
             raise ValueError(f"page_table: expected int32 [batch, max_pages] with contiguous rows on cuda:{device}, "
                              f"got {list(page_table.shape)} {page_table.dtype} on {page_table.device}")
+        table_stride, width = page_table.stride(0), page_table.shape[1]
+        if table_stride < width:
+            if page_table.shape[0] > 1:
+                raise ValueError(f"page_table: rows overlap, stride {table_stride} for {width} entries; "
+                                 "expanded tables: make them contiguous")
+            table_stride = width  # of a single row
         self.k_pool, self.v_pool, self.page_table = k_pool, v_pool, page_table
         self.status = torch.zeros(1, dtype=torch.int32, device=k_pool.device)
         self.device, self.dtype = device, k_pool.dtype
@@ -254,8 +260,8 @@ class PagedCache:
         self.batch = page_table.shape[0]
         self._c = _CACHE.pack(
             k_pool.data_ptr(), v_pool.data_ptr(), *k_pool.stride()[:3], *v_pool.stride()[:3], page_table.data_ptr(),
-            max(page_table.stride(0), page_table.shape[1]), self.status.data_ptr(), page_table.shape[1], self.n_pages,
-            self.page_size, self.kv_heads, self.head_dim, _DTYPES[self.dtype], device)
+            table_stride, self.status.data_ptr(), width, self.n_pages, self.page_size, self.kv_heads, self.head_dim,
+            _DTYPES[self.dtype], device)
 
     def read_status(self) -> int:
         """DEV_* bits since the last call (synchronises); clears them."""

@@ -299,3 +299,30 @@ def test_packed_structs_match_the_header(tmp_path):
     got = [int(x) for x in subprocess.run([str(tmp_path / "s")], capture_output=True, text=True, check=True).stdout.split()]
     assert got == [ops._ROPE.size, ops._CACHE.size, ops._APPEND.size, ops._ATTENTION.size,
                    ctypes.sizeof(ops.RopeConfig), ctypes.sizeof(ops._Plan)]
+
+
+@pytest.fixture
+def no_device(monkeypatch):
+    """A cache's own memory, without a device."""
+    monkeypatch.setattr(torch, "zeros", lambda *a, **k: FakeT([1], I32))
+
+
+def _table(shape, stride):
+    pool = FakeT([8, 64, 2, 128])
+    cache = ops.PagedCache(pool, FakeT([8, 64, 2, 128], ptr=1 << 30), FakeT(shape, I32, stride=stride, ptr=1 << 34))
+    return ops._CACHE.unpack(cache._c)[9:12:2]  # stride and width of a row
+
+
+@pytest.mark.parametrize("stride", [(0, 1), (1, 1), (3, 1)])
+def test_page_tables_whose_rows_overlap_are_refused(no_device, stride):
+    """An expanded table (one row for all sequences) has no row stride that the calls could use."""
+    for batch in (2, 3, 100):
+        with pytest.raises(ValueError, match="page_table: rows overlap"):
+            _table([batch, 4], stride)
+
+
+def test_page_tables_keep_their_row_stride(no_device):
+    assert _table([3, 4], (4, 1)) == (4, 4)
+    assert _table([3, 4], (16, 1)) == (16, 4)  # a slice of a wider table
+    assert _table([1, 4], (0, 1)) == (4, 4)  # the stride of a single row says nothing
+    assert _table([1, 4], (16, 1)) == (16, 4)
