@@ -93,6 +93,7 @@ _SIGS = {
     # operators of the caller's own target model (ops.py); structs are passed packed
     "dflash_rope_init": (ctypes.c_int, [_vp, _vp]),
     "dflash_rope": (ctypes.c_int, [_vp, ctypes.c_char_p, _vp]),
+    "dflash_paged_read_status": (ctypes.c_int, [ctypes.c_char_p, ctypes.POINTER(ctypes.c_uint32)]),
     "dflash_paged_append": (ctypes.c_int, [ctypes.c_char_p, _vp, ctypes.c_char_p, _vp]),
     "dflash_paged_attention_workspace": (ctypes.c_size_t, [ctypes.c_char_p, ctypes.c_int32, ctypes.c_int32,
                                                            ctypes.c_int32]),

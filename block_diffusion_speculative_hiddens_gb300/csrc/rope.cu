@@ -254,6 +254,9 @@ __global__ void __launch_bounds__(ROPE_THREADS) k_rope(const __grid_constant__ R
   }
 }
 
+// Clears bits that the host has read, and none that were set since.
+__global__ void k_clear_status(uint32_t* status, uint32_t bits) { atomicAnd(status, ~bits); }
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 template <bool APPEND>
@@ -392,6 +395,18 @@ int dflash_rope(const dflash_rope_plan* plan, const dflash_rope_args* a, void* s
   DeviceGuard guard(a->device);
   if (!guard.ok) return DFLASH_ERR_CUDA;
   return launch_rope<false>(p, a->dtype == DFLASH_BF16, vec, static_cast<cudaStream_t>(stream));
+}
+
+int dflash_paged_read_status(const dflash_paged_cache* c, uint32_t* out) {
+  if (!out) return DFLASH_ERR_INVALID_ARG;
+  if (int e = paged_cache_check(c)) return e;
+  DeviceGuard guard(c->device);
+  if (!guard.ok || cudaDeviceSynchronize() != cudaSuccess ||
+      cudaMemcpy(out, c->status, sizeof(uint32_t), cudaMemcpyDeviceToHost) != cudaSuccess)
+    return DFLASH_ERR_CUDA;
+  if (!*out) return DFLASH_OK;
+  k_clear_status<<<1, 1>>>(c->status, *out);
+  return cudaGetLastError() == cudaSuccess && cudaDeviceSynchronize() == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
 }
 
 int dflash_paged_append(const dflash_paged_cache* c, const dflash_rope_plan* plan, const dflash_append_args* a,

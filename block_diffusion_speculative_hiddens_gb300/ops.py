@@ -228,12 +228,23 @@ def rope(plan: RopePlan, q, k, positions, *, backward: bool = False, q_out=None,
     return q_out, k_out
 
 
+def _clear_word(device):
+    """A zero that calls on any stream find, not only those behind the current one.
+    A captured one is the graph's: each replay clears it, ahead of the graph's calls."""
+    with torch.cuda.device(device):
+        word = torch.zeros(1, dtype=torch.int32, device=device)
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream().synchronize()
+    return word
+
+
 class PagedCache:
     """Pools of K and V pages [n_pages, page_size, kv_heads, head_dim] (any
     order in memory: pass a permuted view) and a page table [batch, max_pages]
     int32 whose entry [b, p // page_size] is the page of sequence b's position
     p.  All of them are the caller's; the table's values may change between
-    calls.  `status` collects the device-side checks of the calls on it."""
+    calls.  `status` collects the device-side checks of the calls on it: keep
+    the cache as long as calls or captured graphs use it."""
 
     def __init__(self, k_pool, v_pool, page_table):
         device = _cuda_half(k_pool, "k_pool")
@@ -254,7 +265,7 @@ class PagedCache:
                                  "expanded tables: make them contiguous")
             table_stride = width  # of a single row
         self.k_pool, self.v_pool, self.page_table = k_pool, v_pool, page_table
-        self.status = torch.zeros(1, dtype=torch.int32, device=k_pool.device)
+        self.status = _clear_word(k_pool.device)
         self.device, self.dtype = device, k_pool.dtype
         self.n_pages, self.page_size, self.kv_heads, self.head_dim = k_pool.shape
         self.batch = page_table.shape[0]
@@ -264,10 +275,13 @@ class PagedCache:
             _DTYPES[self.dtype], device)
 
     def read_status(self) -> int:
-        """DEV_* bits since the last call (synchronises); clears them."""
-        v = int(self.status.item())
-        self.status.zero_()
-        return v
+        """DEV_* bits since the last call, and clears them.  Waits for the device:
+        calls on every stream are in.  Not during a capture."""
+        v = ctypes.c_uint32()
+        code = load().dflash_paged_read_status(self._c, ctypes.byref(v))
+        if code:
+            raise DflashError("dflash_paged_read_status", code)
+        return v.value
 
 
 def _batch(cache, cu_rows, ctx_len):

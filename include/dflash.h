@@ -518,6 +518,11 @@ typedef struct dflash_paged_cache {
   int32_t dtype, device;
 } dflash_paged_cache;
 
+/* Wait for the device, return the cache's status word in *out (DFLASH_DEV_*
+ * bits, 0 = clean) and clear the bits that were returned; one that is set
+ * meanwhile stays for the next call.  Not during a capture. */
+DFLASH_API int dflash_paged_read_status(const dflash_paged_cache* cache, uint32_t* out);
+
 /* Append k and v of every row at its position: k rotated by the plan (null:
  * copied).  q (data non-null) is rotated alike into q_out, under dflash_rope's
  * rules.  A row whose position is negative or has no page (beyond the table,

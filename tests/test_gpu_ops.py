@@ -635,3 +635,65 @@ def test_attention_whose_window_lies_past_the_table_says_so(ops, heads, rows, ct
         to, tl = ops_ref.attention_tolerance(o, l, mag, ds, seen, BF16, dim, pg.v[b].abs().max().item())
         close(out[r], o, to, ("out", b))
         close(lse[r], l, tl, ("lse", b))
+
+
+def _reports(ops, cache, stream):
+    """A token whose only page is outside the pool, on `stream`."""
+    q = torch.zeros(1, 4, 64, dtype=BF16, device="cuda")
+    cu, ctx = i32([0, 1]), i32([5])
+    torch.cuda.synchronize()
+    return lambda: ops.attention(cache, q, cu, ctx, stream=stream)
+
+
+def test_status_of_calls_on_another_stream(ops):
+    """read_status waits for every stream, also for what is still queued there."""
+    from block_diffusion_speculative_hiddens_gb300.binding import DEV_PAGE
+    pg = Paged(ops, [6], 2, 64, 64, BF16)
+    pg.table.fill_(-1)
+    side = torch.cuda.Stream()
+    call = _reports(ops, pg.cache, side)
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(40_000_000)  # about 20 ms
+        call()
+        assert pg.cache.read_status() == DEV_PAGE
+        assert pg.cache.read_status() == 0
+
+
+def test_status_of_a_first_call_on_another_stream(ops):
+    """The status word is clear before the cache can be used anywhere."""
+    from block_diffusion_speculative_hiddens_gb300.binding import DEV_PAGE
+    pg = Paged(ops, [6], 2, 64, 64, BF16)
+    pg.table.fill_(-1)
+    side = torch.cuda.Stream()
+    call = _reports(ops, pg.cache, side)
+    call()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(40_000_000)
+    cache = ops.PagedCache(pg.kp, pg.vp, pg.table)
+    q, cu, ctx = torch.empty(1, 4, 64, dtype=BF16, device="cuda"), torch.empty(2, dtype=I32, device="cuda"), \
+        torch.empty(1, dtype=I32, device="cuda")
+    with torch.cuda.stream(side):
+        q.zero_()
+        cu[0], cu[1], ctx[0] = 0, 1, 5
+    ops.attention(cache, q, cu, ctx, stream=side)
+    assert cache.read_status() == DEV_PAGE
+
+
+def test_status_of_a_cache_built_while_a_graph_is_captured(ops):
+    """Its word is cleared by each replay."""
+    from block_diffusion_speculative_hiddens_gb300.binding import DEV_PAGE
+    pg = Paged(ops, [6], 2, 64, 64, BF16)
+    q = torch.zeros(1, 4, 64, dtype=BF16, device="cuda")
+    cu, ctx = i32([0, 1]), i32([5])
+    want = ops.attention(pg.cache, q, cu, ctx)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        cache = ops.PagedCache(pg.kp, pg.vp, pg.table)
+        out = ops.attention(cache, q, cu, ctx)
+    g.replay()
+    assert cache.read_status() == 0 and torch.equal(out, want)
+    pg.table.fill_(-1)
+    g.replay()
+    assert cache.read_status() == DEV_PAGE

@@ -304,7 +304,7 @@ def test_packed_structs_match_the_header(tmp_path):
 @pytest.fixture
 def no_device(monkeypatch):
     """A cache's own memory, without a device."""
-    monkeypatch.setattr(torch, "zeros", lambda *a, **k: FakeT([1], I32))
+    monkeypatch.setattr(ops, "_clear_word", lambda device: FakeT([1], I32))
 
 
 def _table(shape, stride):
@@ -326,3 +326,14 @@ def test_page_tables_keep_their_row_stride(no_device):
     assert _table([3, 4], (16, 1)) == (16, 4)  # a slice of a wider table
     assert _table([1, 4], (0, 1)) == (4, 4)  # the stride of a single row says nothing
     assert _table([1, 4], (16, 1)) == (16, 4)
+
+
+def test_status_entry_refuses_before_any_cuda_call(lib):
+    word = ctypes.c_uint32(7)
+    assert lib.dflash_paged_read_status(None, ctypes.byref(word)) == 1
+    good = (256, 256, 16384, 256, 128, 16384, 256, 128, 256, 4, 256, 4, 8, 64, 2, 128, 1, 0)
+    assert lib.dflash_paged_read_status(ops._CACHE.pack(*good), None) == 1
+    bad = list(good)
+    bad[10] = 0  # no status word
+    assert lib.dflash_paged_read_status(ops._CACHE.pack(*bad), ctypes.byref(word)) == 1
+    assert word.value == 7
