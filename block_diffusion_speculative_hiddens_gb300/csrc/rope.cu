@@ -13,14 +13,15 @@
 // time: the two halves of 8 pairs, or 16 adjacent dims, so a pair never
 // crosses threads and an output may be its own input.
 //
-// Bound by memory: each value is read and written once.  8,191 rows of 40
-// heads of 128 (168 MB) take 27.4 us, 6.1 TB/s, 0.90 of the copy rate; 7,500
-// rows appended with their queries (184 MB) 33.4 us, 5.5 TB/s (35.1 with the page
-// looked up by a warp that also computes angles; 32.9, but 3.3 for 3.2 us for 64
-// single rows, with every thread looking up its own).  A row a CTA with two units
-// of a thread in flight: four rows a CTA took 29.4 and 37.5 us, one or three
-// units in flight 31.3 and 29.6.  A call of 16 rows is 2.5 us of
-// launch, load, angles and store.
+// Bound by memory: each value is read and written once.  Replayed in a graph,
+// 8,191 rows of 40 heads of 128 (168 MB) take 27.7 us, 6.1 TB/s, 0.89 of the copy
+// rate; 7,500 rows appended with their queries (184 MB) 32.8 us, 5.6 TB/s.  A row a
+// CTA with two units of a thread in flight: four rows a CTA took 29.4 and 37.5 us,
+// one or three units in flight 31.3 and 29.6; the page looked up by a warp that
+// also computes angles 35.1 for 33.4 us of appending.  A call of 16 rows is 2.7 us
+// of launch, load, angles and store.
+// A row's sequence is searched 32 at a time by a warp: an append of one row each
+// takes 3.3 us for up to 64 sequences, 4.5 for 256 and 11.5 for 1,024.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -56,7 +57,7 @@ struct RopeParams {
   long long table_stride;
   int max_pages, n_pages, page_shift;
   uint32_t* status;
-  int rows_per_cta;
+  int rows_per_cta, lanes;  // lanes: heads that a pass of the block takes
   uint64_t turn[DFLASH_ROPE_MAX_PAIRS];
 };
 
@@ -111,9 +112,9 @@ __global__ void __launch_bounds__(ROPE_THREADS) k_rope(const __grid_constant__ R
   const int row0 = blockIdx.x * p.rows_per_cta;
   const int nr = min(p.rows_per_cta, p.rows - row0);
   const int U = VEC ? p.D >> 4 : p.D >> 1;      // units of a head
-  const int c = threadIdx.x % U;                // blockDim is a multiple of U
+  const int c = threadIdx.x % U;
   const int H = p.heads[0] + p.heads[1] + (APPEND ? p.heads[2] : 0);
-  const int step = blockDim.x / U;
+  const int step = p.lanes;
   const int rot = VEC ? p.rd >> 4 : p.rd >> 1;  // rotated units of a head
   const bool turned = c < rot;
   // first element of the unit's two parts
@@ -133,7 +134,7 @@ __global__ void __launch_bounds__(ROPE_THREADS) k_rope(const __grid_constant__ R
     int r, which, h;  // row of the CTA (-1: none), tensor, head
   };
   auto load = [&](Unit& u, int it) {
-    u.r = it < nr * H ? it / H : -1;
+    u.r = it >= nr * H ? -1 : nr == 1 ? 0 : it / H;  // a row a CTA needs no division
     if (u.r < 0) return;
     u.h = it - u.r * H;
     u.which = u.h < p.heads[0] ? 0 : u.h < p.heads[0] + p.heads[1] ? 1 : 2;
@@ -149,22 +150,22 @@ __global__ void __launch_bounds__(ROPE_THREADS) k_rope(const __grid_constant__ R
   // row's place and angles are found
   Unit unit[ROPE_AHEAD];
   int it = threadIdx.x / U;
+  if (it >= step) it = nr * H;  // a thread that only fills the last warp
 #pragma unroll
   for (int i = 0; i < ROPE_AHEAD; ++i) load(unit[i], it + i * step);
   if (APPEND) {
     // a warp finds a row's sequence and position; its page is looked up while
     // the angles are computed
-    const int lane = threadIdx.x & 31, warps = (blockDim.x + 31) >> 5;
+    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
     for (int r = threadIdx.x >> 5; r < nr; r += warps) {
       const int t = row0 + r;
-      const uint32_t here = __activemask();  // the last warp may not be full
-      const int width = __popc(here);
       RowPlace w = {};
-      for (int b0 = 0; b0 < p.batch; b0 += width) {
+      __syncwarp();  // the loads above, and the last row's search, may have parted the lanes
+      for (int b0 = 0; b0 < p.batch; b0 += 32) {
         const int b = b0 + lane;
         const bool in = b < p.batch;
         const int lo = in ? p.cu[b] : 0, hi = in ? p.cu[b + 1] : 0, ctx = in ? p.ctx[b] : 0;
-        const uint32_t found = __ballot_sync(here, in && t >= lo && t < hi);
+        const uint32_t found = __ballot_sync(0xffffffffu, in && t >= lo && t < hi);
         if (!found) continue;
         if (lane == __ffs(found) - 1) {
           w.valid = 1;
@@ -267,10 +268,10 @@ int launch_rope(RopeParams& p, bool bf16_, bool vec, cudaStream_t s) {
   const int H = p.heads[0] + p.heads[1] + p.heads[2], per = ROPE_THREADS / U;  // heads a pass, at most
   p.rows_per_cta = std::max(1, std::min(ROPE_MAX_ROWS, ROPE_AHEAD * per / std::max(H, 1)));
   const int items = p.rows_per_cta * H;
-  const int lanes = std::min(per, std::max((items + ROPE_AHEAD - 1) / ROPE_AHEAD, (64 + U - 1) / U));
+  p.lanes = std::min(per, std::max((items + ROPE_AHEAD - 1) / ROPE_AHEAD, (64 + U - 1) / U));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((p.rows + p.rows_per_cta - 1) / p.rows_per_cta));
-  cfg.blockDim = dim3((unsigned)(U * lanes));
+  cfg.blockDim = dim3((unsigned)((U * p.lanes + 31) / 32 * 32));  // whole warps: the append's search takes one a row
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

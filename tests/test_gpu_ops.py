@@ -697,3 +697,23 @@ def test_status_of_a_cache_built_while_a_graph_is_captured(ops):
     pg.table.fill_(-1)
     g.replay()
     assert cache.read_status() == DEV_PAGE
+
+
+@pytest.mark.parametrize("hq,hkv,dim", [(0, 1, 6), (1, 1, 10), (5, 1, 22), (3, 2, 80), (7, 1, 112), (2, 2, 2)])
+def test_append_finds_its_sequence_in_blocks_of_uneven_warps(ops, hq, hkv, dim):
+    """Heads whose blocks end in a warp that is not full, rows that share a block, more sequences than lanes."""
+    rows = [i % 3 for i in range(150)]
+    ctx = [(i * 7) % 50 for i in range(150)]
+    pg = Paged(ops, [a + b for a, b in zip(rows, ctx)], hkv, dim, 16, BF16, fill=3.0)
+    t = sum(rows)
+    k, v = (torch.randn(t, hkv, dim, generator=gen(s), device="cuda").to(BF16) for s in (1, 2))
+    q = torch.randn(t, hq, dim, generator=gen(3), device="cuda").to(BF16) if hq else None
+    kp, vp = pg.kp.clone(), pg.vp.clone()
+    cu = [sum(rows[:i]) for i in range(151)]
+    got = ops.append(pg.cache, k, v, i32(cu), i32(ctx), q=q)
+    for b, n in enumerate(rows):
+        pos = ctx[b] + torch.arange(n, device="cuda")
+        at = pg.table[b].long()[pos // 16], pos % 16
+        kp[at], vp[at] = k[cu[b]:cu[b + 1]], v[cu[b]:cu[b + 1]]
+    assert torch.equal(kp, pg.kp) and torch.equal(vp, pg.vp) and pg.cache.read_status() == 0
+    assert got is None if q is None else torch.equal(got, q)  # without a plan: copied

@@ -337,3 +337,11 @@ def test_status_entry_refuses_before_any_cuda_call(lib):
     bad[10] = 0  # no status word
     assert lib.dflash_paged_read_status(ops._CACHE.pack(*bad), ctypes.byref(word)) == 1
     assert word.value == 7
+
+
+def test_no_kernel_asks_which_lanes_are_active():
+    """A warp's lanes may be apart at any point; masks come from the block's shape."""
+    import glob
+    for f in glob.glob(os.path.join(_build.CSRC, "*.cu*")) + glob.glob(os.path.join(_build.CSRC, "*.h")):
+        with open(f) as src:
+            assert "__activemask" not in src.read(), f
