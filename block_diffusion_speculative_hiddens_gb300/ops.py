@@ -306,10 +306,11 @@ def append(cache: PagedCache, k, v, cu_rows, ctx_len, *, plan: RopePlan = None, 
     if q is not None:
         qs = _rows(q, "q", dtype, device, rows, None, dim)
         hq = q.shape[1]
-        if q_out is not None:
+        given = q_out is not None
+        q_out, qo = _out(q_out, q, rows, hq, dim, "q_out", dtype, device, stream)
+        if given:
             _apart(q_out, k, "q_out", "k")
             _apart(q_out, v, "q_out", "v")
-        q_out, qo = _out(q_out, q, rows, hq, dim, "q_out", dtype, device, stream)
     args = _APPEND.pack(*ks, *vs, *qs, *qo, cu, ctx, rows, b, hq, 0)
     code = load().dflash_paged_append(cache._c, None if plan is None else plan._ref, args, raw)
     if code:

@@ -345,3 +345,12 @@ def test_no_kernel_asks_which_lanes_are_active():
     for f in glob.glob(os.path.join(_build.CSRC, "*.cu*")) + glob.glob(os.path.join(_build.CSRC, "*.h")):
         with open(f) as src:
             assert "__activemask" not in src.read(), f
+
+
+@pytest.mark.parametrize("bad", [FakeT([512], ptr=1 << 28), FakeT([7, 512], ptr=1 << 28), FakeT([], ptr=1 << 28),
+                                 FakeT([7, 4, 128], torch.float32, ptr=(1 << 28) - 512)], ids=["1d", "2d", "0d", "f32"])
+def test_appends_output_is_checked_before_it_is_compared(calls, bad):
+    """Its shape and type are refused as such, wherever it lies."""
+    with pytest.raises(ValueError, match="q_out: expected"):
+        _append(q_out=bad)
+    assert calls == []
