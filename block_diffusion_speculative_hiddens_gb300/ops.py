@@ -220,6 +220,8 @@ def rope(plan: RopePlan, q, k, positions, *, backward: bool = False, q_out=None,
             _apart(k_out, q, "k_out", "q")
             if given_q:
                 _apart(q_out, k_out, "q_out", "k_out")
+    elif given_k:
+        raise ValueError("k_out: given without k")
     args = _ROPE.pack(*qs, *ks, *qo, *ko, _i32(positions, "positions", rows, device), rows, hq, hk, dim, _DTYPES[dtype],
                       bool(backward), device)
     code = load().dflash_rope(plan._ref, args, raw)
@@ -295,7 +297,7 @@ def append(cache: PagedCache, k, v, cu_rows, ctx_len, *, plan: RopePlan = None, 
     """Write k and v [rows, kv_heads, head_dim] of a ragged batch into the cache
     at positions ctx_len[b] and on, k rotated by `plan` (None: as it is).  q
     [rows, q_heads, head_dim], if given, is rotated alike; returns q_out (None
-    without q)."""
+    without q, which takes no q_out)."""
     device, dtype, dim = cache.device, cache.dtype, cache.head_dim
     raw = _raw_stream(stream, device)
     ks = _rows(k, "k", dtype, device, None, cache.kv_heads, dim)
@@ -311,6 +313,8 @@ def append(cache: PagedCache, k, v, cu_rows, ctx_len, *, plan: RopePlan = None, 
         if given:
             _apart(q_out, k, "q_out", "k")
             _apart(q_out, v, "q_out", "v")
+    elif q_out is not None:
+        raise ValueError("q_out: given without q")
     args = _APPEND.pack(*ks, *vs, *qs, *qo, cu, ctx, rows, b, hq, 0)
     code = load().dflash_paged_append(cache._c, None if plan is None else plan._ref, args, raw)
     if code:

@@ -354,3 +354,12 @@ def test_appends_output_is_checked_before_it_is_compared(calls, bad):
     with pytest.raises(ValueError, match="q_out: expected"):
         _append(q_out=bad)
     assert calls == []
+
+
+def test_outputs_without_their_input_are_refused(calls):
+    """They would come back unwritten."""
+    with pytest.raises(ValueError, match="q_out: given without q"):
+        _append(q=None)
+    with pytest.raises(ValueError, match="k_out: given without k"):
+        _rope(k=None)
+    assert calls == []
