@@ -59,6 +59,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "overlap.h"
 
 namespace {
 
@@ -1387,11 +1388,22 @@ int dflash_paged_attention(const dflash_paged_cache* c, const dflash_attention_a
     return DFLASH_ERR_INVALID_ARG;
   if (a->batch > 8192) return DFLASH_ERR_CAPACITY;  // the sequences' first pairs lie in one M tile's shared memory
   if ((reinterpret_cast<uintptr_t>(a->workspace) & 255) || a->workspace_bytes < 0) return DFLASH_ERR_WORKSPACE;
+  const int hq = a->q_heads;
+  const Strided q = strided_rows(a->q, a->rows, hq, D), out = strided_rows(a->out, a->rows, hq, D),
+                lse = strided(a->lse, 4, {{4 * a->lse_row_stride, a->rows}, {4 * a->lse_head_stride, hq}}),
+                kp = strided_pool(c, false), vp = strided_pool(c, true), table = strided_table(c, a->batch),
+                cu = strided_ints(a->cu_rows, a->batch + 1ll), ctx = strided_ints(a->ctx_len, a->batch),
+                kv = strided_ints(a->kv_len, a->batch),
+                status = strided_ints(reinterpret_cast<const int32_t*>(c->status), 1);
+  if (!apart({out, lse}, {input_of(a->out, a->q, a->rows, hq, D), kp, vp, table, cu, ctx, kv, status}) || meet(lse, q))
+    return DFLASH_ERR_INVALID_ARG;
   const Device* dev = device_of(c->device);
   if (!dev) return DFLASH_ERR_CUDA;
   const int group = a->q_heads / c->kv_heads;
   const Plan pl = plan_call(*dev, c, a->rows, a->batch, a->q_heads);
   if (pl.ws && (!a->workspace || (size_t)a->workspace_bytes < pl.ws)) return DFLASH_ERR_WORKSPACE;
+  if (!apart({strided(a->workspace, (long long)pl.ws, {})}, {out, lse, q, kp, vp, table, cu, ctx, kv, status}))
+    return DFLASH_ERR_INVALID_ARG;
   PagedParams p = {};
   p.out = static_cast<uint16_t*>(a->out.data);
   p.o_row = a->out.row_stride;

@@ -28,6 +28,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "overlap.h"
 
 namespace {
 
@@ -388,6 +389,9 @@ int dflash_rope(const dflash_rope_plan* plan, const dflash_rope_args* a, void* s
     p.out[i] = {static_cast<uint16_t*>(out[i]->data), out[i]->row_stride, out[i]->head_stride};
     vec = vec && vec_ok(*in[i]) && vec_ok(*out[i]);
   }
+  const Strided qo = strided_rows(a->q_out, a->rows, p.heads[0], D), ko = strided_rows(a->k_out, a->rows, p.heads[1], D);
+  const Strided q = input_of(a->q_out, a->q, a->rows, p.heads[0], D), k = input_of(a->k_out, a->k, a->rows, p.heads[1], D);
+  if (!apart({qo, ko}, {q, k, strided_ints(a->positions, a->rows)})) return DFLASH_ERR_INVALID_ARG;
   p.rows = a->rows;
   p.D = D;
   p.backward = a->backward != 0;
@@ -431,6 +435,14 @@ int dflash_paged_append(const dflash_paged_cache* c, const dflash_rope_plan* pla
     p.in[0] = {static_cast<const uint16_t*>(a->q.data), a->q.row_stride, a->q.head_stride};
     p.out[0] = {static_cast<uint16_t*>(a->q_out.data), a->q_out.row_stride, a->q_out.head_stride};
   }
+  const Strided kp = strided_pool(c, false), vp = strided_pool(c, true), table = strided_table(c, a->batch),
+                cu = strided_ints(a->cu_rows, a->batch + 1ll), ctx = strided_ints(a->ctx_len, a->batch),
+                status = strided_ints(reinterpret_cast<const int32_t*>(c->status), 1);
+  if (!apart({kp, vp}, {table, cu, ctx, status}) ||
+      !apart({strided_rows(a->q_out, a->rows, p.heads[0], D)},
+             {input_of(a->q_out, a->q, a->rows, p.heads[0], D), strided_rows(a->k, a->rows, c->kv_heads, D),
+              strided_rows(a->v, a->rows, c->kv_heads, D), kp, vp, table, cu, ctx, status}))
+    return DFLASH_ERR_INVALID_ARG;
   p.pool[0] = {static_cast<uint16_t*>(c->k), c->k_pos_stride, c->k_head_stride};
   p.pool[1] = {static_cast<uint16_t*>(c->v), c->v_pos_stride, c->v_head_stride};
   p.page_stride[0] = c->k_page_stride;

@@ -16,8 +16,9 @@ The C entry points, their argument structs, limits and device-side checks are
 in include/dflash.h; this module checks the tensors (ValueError) and passes
 their pointers and strides.  Calls go to the current stream of the tensors'
 device (or `stream`), enqueue and return, and may be captured into a graph;
-outputs that are not given are allocated on that stream, those that are given
-overlap nothing else of the call (beyond what a call allows) nor themselves.
+outputs that are not given are allocated on that stream.  Those that are given
+may be their own input (in place); over anything else of the call, or over
+themselves, they are refused (ValueError, or DflashError from the C entry).
 """
 from __future__ import annotations
 

@@ -437,7 +437,11 @@ DFLASH_API int dflash_harness_verify(dflash_handle* h, const int32_t* slots, int
  * dimension is contiguous.  `device` is the ordinal that every pointer and
  * the stream belong to; the caller's current device is left as it was.
  * Calls keep nothing between them and may overlap on different streams, each
- * with a workspace of its own; they are legal inside stream capture. */
+ * with a workspace of its own; they are legal inside stream capture.  What a
+ * call writes lies apart from itself and from everything else that it is given,
+ * but for an output that is its own input (same pointer and strides): anything
+ * else is DFLASH_ERR_INVALID_ARG.  Tensors may interleave (heads of one buffer's
+ * rows, pools that alternate). */
 #define DFLASH_F16 0
 #define DFLASH_BF16 1
 
@@ -488,9 +492,7 @@ DFLASH_API int dflash_rope_init(const dflash_rope_config* cfg, dflash_rope_plan*
 
 /* Rotate the heads of q and (data non-null) k at positions[t] (DEVICE int32
  * [rows]): the first rotary_dim dims of a head by the plan, the others copied.
- * Any alignment and strides; an output may be its own input (same pointer and
- * strides) and must overlap neither it otherwise nor the other tensors or
- * itself.  backward = 1 applies the transposed map: the gradient of the inputs
+ * Any alignment and strides; an output may be its own input.  backward = 1 applies the transposed map: the gradient of the inputs
  * from the gradient of the outputs. */
 typedef struct dflash_rope_args {
   dflash_rows q, k, q_out, k_out;
@@ -528,7 +530,8 @@ DFLASH_API int dflash_paged_read_status(const dflash_paged_cache* cache, uint32_
  * rules.  A row whose position is negative or has no page (beyond the table,
  * or an entry outside the pool) is not written and sets DFLASH_DEV_PAGE; its
  * q is still rotated.  head_dim even, up to 256.  Rows of one call must have
- * different places. */
+ * different places, and k and v, if they lie in the pools, places that the call
+ * does not write. */
 typedef struct dflash_append_args {
   dflash_rows k, v, q, q_out;
   const int32_t* cu_rows;
@@ -543,8 +546,7 @@ DFLASH_API int dflash_paged_append(const dflash_paged_cache* cache, const dflash
  * row t sees: 0 <= j < kv_len[b] (null: ctx_len[b] + the sequence's rows), with
  * causal also j <= position, with window w > 0 also j > position - w.  Query
  * head h reads KV head h / (q_heads / kv_heads).  A row that sees no position
- * gets out 0 and lse -inf.  out may be q (same pointer and strides) and must
- * overlap neither it otherwise nor the cache or itself.  lse (optional, float32 [rows][q_heads], strides of
+ * gets out 0 and lse -inf.  out may be q.  lse (optional, float32 [rows][q_heads], strides of
  * its own): the natural logarithm of the row's sum of exponentials.  Only
  * pages that hold a seen position are read, and of the last of them nothing
  * behind kv_len reaches the result; a non-finite value within kv_len reaches

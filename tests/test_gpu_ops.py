@@ -717,3 +717,37 @@ def test_append_finds_its_sequence_in_blocks_of_uneven_warps(ops, hq, hkv, dim):
         kp[at], vp[at] = k[cu[b]:cu[b + 1]], v[cu[b]:cu[b + 1]]
     assert torch.equal(kp, pg.kp) and torch.equal(vp, pg.vp) and pg.cache.read_status() == 0
     assert got is None if q is None else torch.equal(got, q)  # without a plan: copied
+
+
+def test_outputs_over_other_tensors_of_the_call_are_refused(ops):
+    """In the pools, over a workspace, an lse over itself or the output: nothing is queued, nothing changes."""
+    from block_diffusion_speculative_hiddens_gb300.binding import DflashError
+    pg = Paged(ops, [3000, 3000], 2, 64, 64, BF16, order="psh")
+    q = torch.randn(300, 4, 64, generator=gen(1), device="cuda").to(BF16)
+    cu, ctx = i32([0, 100, 300]), i32([2900, 2800])
+    kv = pg.k[0][:1].expand(300, 2, 64).contiguous()
+    inside = pg.kp[:10].view(-1)[:300 * 256].view(300, 4, 64)
+    ws = torch.zeros(ops.attention_workspace(pg.cache, 300, 2, 4), dtype=torch.uint8, device="cuda")
+    need = 300 * 4 * 64 * 2
+    before = pg.kp.clone(), pg.vp.clone(), q.clone()
+    for call in (lambda: ops.attention(pg.cache, q, cu, ctx, out=inside),
+                 lambda: ops.append(pg.cache, kv, kv, cu, ctx, q=q, q_out=inside),
+                 lambda: ops.attention(pg.cache, q, cu, ctx, out=ws[:need].view(BF16).view(300, 4, 64), workspace=ws),
+                 lambda: ops.attention(pg.cache, q, cu, ctx, lse=ws[4096:4096 + 4800].view(torch.float32).view(300, 4), workspace=ws),
+                 lambda: ops.attention(pg.cache, q, cu, ctx, lse=torch.zeros(300, 1, device="cuda").expand(300, 4)),
+                 lambda: ops.attention(pg.cache, q, cu, ctx, lse=q.view(-1)[:2400].view(torch.float32).view(300, 4)),
+                 lambda: ops.append(ops.PagedCache(pg.kp, pg.kp, pg.table), kv, kv, cu, ctx)):
+        with pytest.raises(DflashError) as e:
+            call()
+        assert e.value.code == 1
+    torch.cuda.synchronize()
+    assert all(torch.equal(x.nan_to_num(7), y.nan_to_num(7)) for x, y in zip((pg.kp, pg.vp, q), before))
+    # beside one another they are taken: an lse and an output behind the workspace's bytes, K and V of one pool
+    big = torch.zeros(ws.numel() + need + 4800, dtype=torch.uint8, device="cuda")
+    out, lse = big[ws.numel():-4800].view(BF16).view(300, 4, 64), big[-4800:].view(torch.float32).view(300, 4)
+    ops.attention(pg.cache, q, cu, ctx, out=out, lse=lse, workspace=big[:ws.numel()])
+    assert torch.equal(out, ops.attention(pg.cache, q, cu, ctx))
+    ops.attention(pg.cache, q, cu, ctx, out=out, lse=lse, workspace=big)  # of a larger one only the needed bytes are used
+    assert torch.equal(out, ops.attention(pg.cache, q, cu, ctx))
+    same = ops.attention(ops.PagedCache(pg.kp, pg.kp, pg.table), q, cu, ctx)
+    assert torch.equal(same, ops.attention(ops.PagedCache(pg.kp, pg.kp.clone(), pg.table), q, cu, ctx))

@@ -363,3 +363,108 @@ def test_outputs_without_their_input_are_refused(calls):
     with pytest.raises(ValueError, match="k_out: given without k"):
         _rope(k=None)
     assert calls == []
+
+
+# A device that no machine has: a call that passes its checks ends there (4), before anything is queued.
+NOWHERE = 1000
+
+
+def _bytes(view, size=2):
+    """Every byte of a view (address, count and stride of each dimension in elements), and whether one is there twice."""
+    at, dims = view
+    where = [at]
+    for n, s in dims:
+        where = [w + size * s * i for w in where for i in range(n)]
+    every = [w + j for w in where for j in range(size)]
+    return set(every), len(set(every)) < len(every)
+
+
+def test_rope_refuses_outputs_that_share_memory(lib):
+    """Random strides of rows and heads against the sets of bytes behind them: written bytes are written once, and
+    read by nothing but the output's own input (in place)."""
+    import random
+    rng = random.Random(5)
+    plan = ops.RopePlan(2, 1e4)
+    seen = {1: 0, 4: 0}
+    for trial in range(6000):
+        rows, hq, hk, d = rng.randint(1, 5), rng.randint(1, 4), rng.randint(1, 3), rng.choice([2, 4, 6])
+        base = 1 << 20
+
+        def rows_of(h):
+            kind = rng.random()
+            head = d * rng.choice([1, 1, 1, 2, 3])
+            row = head * h + d * rng.choice([0, 0, 1, 3, 7, 13])
+            if kind < 0.25:  # heads first
+                row, head = head, head * rows + d * rng.choice([0, 1, 4])
+            elif kind < 0.3:
+                row, head = rng.randint(0, 20), rng.randint(0, 20)
+            return base + 2 * rng.choice([d * rng.randint(0, 60), rng.randint(0, 300)]), row, head
+        q, k = rows_of(hq), rows_of(hk)
+        qo = q if rng.random() < 0.4 else rows_of(hq)
+        ko = k if rng.random() < 0.4 else rows_of(hk)
+        if rng.random() < 0.3:  # heads of one buffer's rows
+            wide = d * (hq + hk) * 2
+            q, k = (base, wide, d), (base + 2 * d * hq, wide, d)
+            qo = rng.choice([q, (base + 2 * d * (hq + hk), wide, d), (base + 2 * d * (hq + hk - 1), wide, d)])
+            ko = rng.choice([k, (base + 2 * d * (2 * hq + hk), wide, d)])
+        pos = 1 << 24 if rng.random() < 0.9 else base + 4 * rng.randint(0, 300)
+
+        def view(x, h):
+            return x[0], ((rows, x[1]), (h, x[2]), (d, 1))
+
+        def same(x, y, h):
+            return x[0] == y[0] and (rows == 1 or x[1] == y[1]) and (h == 1 or x[2] == y[2])
+        (bq, _), (bk, _) = _bytes(view(q, hq)), _bytes(view(k, hk))
+        (bqo, twice), (bko, twice_k) = _bytes(view(qo, hq)), _bytes(view(ko, hk))
+        bp, _ = _bytes((pos, ((rows, 1),)), 4)
+        wrong = twice or twice_k or bqo & bko or bqo & bk or bko & bq or (bqo | bko) & bp or \
+            (bqo & bq and not same(qo, q, hq)) or (bko & bk and not same(ko, k, hk))
+        a = ops._ROPE.pack(*q, *k, *qo, *ko, pos, rows, hq, hk, d, 1, 0, NOWHERE)
+        got = lib.dflash_rope(plan._ref, a, None)
+        seen[got] += 1
+        if got == 1 and not wrong:  # strides that are not nested are refused without a closer look
+            strides = [sorted((s, n) for n, s in view(x, h)[1] if n > 1) for x, h in ((qo, hq), (ko, hk))]
+            assert any(s < 1 + sum((n - 1) * t for t, n in st[:i]) for st in strides for i, (s, _) in enumerate(st))
+        else:
+            assert got == (1 if wrong else 4), (trial, q, k, qo, ko, rows, hq, hk, d)
+    assert min(seen.values()) > 500
+
+
+def _paged(hq=2, k=1 << 24, v=1 << 25, ks=(2048, 128, 64), vs=(2048, 128, 64), table=1 << 26, pages=5, stride=4):
+    return ops._CACHE.pack(k, v, *ks, *vs, table, stride, 1 << 27, 4, pages, 16, 2, 64, 1, NOWHERE)
+
+
+def test_paged_calls_refuse_outputs_that_share_memory(lib):
+    rows, t = lambda at, row=256, head=64: (at, row, head), 7
+    none = (0, 0, 0)
+
+    def attention(out=rows(1 << 21), lse=none, q=rows(1 << 20), cache=None, cu=1 << 28, ctx=1 << 29, kv=0):
+        a = ops._ATTENTION.pack(*q, *out, *lse, cu, ctx, kv, 0, 0, t, 2, 4, 1, 0, 0.125)
+        return lib.dflash_paged_attention(cache or _paged(), a, None)
+
+    def append(q_out=rows(1 << 21), k=rows(1 << 22, 128), v=rows(1 << 23, 128), cache=None):
+        a = ops._APPEND.pack(*k, *v, *rows(1 << 20), *q_out, 1 << 28, 1 << 29, t, 2, 4, 0)
+        return lib.dflash_paged_append(cache or _paged(), None, a, None)
+    good = [attention(), attention(out=rows(1 << 20)), attention(lse=(1 << 22, 4, 1)), append(), append(q_out=rows(1 << 20)),
+            attention(out=rows(1 << 21, 64, 64 * t)), attention(lse=(1 << 22, 1, t)),
+            # pools that alternate by page, by position and by head; K and V of one pool, which only the append may not have
+            append(cache=_paged(ks=(4096, 128, 64), vs=(4096, 128, 64), v=(1 << 24) + 4096)),
+            append(cache=_paged(ks=(4096, 256, 64), vs=(4096, 256, 64), v=(1 << 24) + 256)),
+            append(cache=_paged(ks=(4096, 256, 128), vs=(4096, 256, 128), v=(1 << 24) + 128)),
+            append(cache=_paged(ks=(64, 64 * 5, 64 * 5 * 16), vs=(64, 64 * 5, 64 * 5 * 16))),
+            attention(cache=_paged(v=1 << 24)),
+            # out behind the heads of the pool's positions
+            attention(cache=_paged(ks=(16 * 640, 640, 64)), out=rows((1 << 24) + 256, 640), q=rows(1 << 20))]
+    assert good == [4] * len(good), good
+    bad = [attention(out=rows((1 << 24) - 512 * t + 2)), attention(out=rows((1 << 25) + 5 * 4096 - 2)),
+           attention(out=rows((1 << 26) + 28)), attention(out=rows((1 << 27))), attention(out=rows((1 << 28) + 8)),
+           attention(out=rows((1 << 29) - 2 * 1024)), attention(kv=(1 << 21) + 128),
+           attention(lse=((1 << 21) + 64, 4, 1)), attention(lse=((1 << 20) + 3580, 4, 1)), attention(lse=((1 << 24), 4, 1)),
+           attention(lse=(1 << 22, 0, 1)), attention(lse=(1 << 22, 4, 0)), attention(lse=(1 << 22, 3, 1)),
+           attention(lse=((1 << 28) + 8, 4, 1)), attention(out=rows(1 << 21, 192)), attention(out=rows((1 << 20) + 128)),
+           attention(out=rows(1 << 20, 256, 128)),
+           append(q_out=rows((1 << 24) + 128)), append(q_out=rows((1 << 22) + 512)), append(q_out=rows((1 << 23) + 64)),
+           append(q_out=rows((1 << 20) + 128)), append(q_out=rows((1 << 26) + 16)),
+           append(cache=_paged(v=1 << 24)), append(cache=_paged(v=(1 << 24) + 4096)), append(cache=_paged(ks=(0, 128, 64))),
+           append(cache=_paged(ks=(2048, 64, 64))), append(cache=_paged(ks=(64, 64 * 4, 64 * 4 * 16)))]
+    assert bad == [1] * len(bad), bad
