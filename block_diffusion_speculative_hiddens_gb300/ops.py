@@ -19,6 +19,8 @@ device (or `stream`), enqueue and return, and may be captured into a graph;
 outputs that are not given are allocated on that stream.  Those that are given
 may be their own input (in place); over anything else of the call, or over
 themselves, they are refused (ValueError, or DflashError from the C entry).
+The calls record nothing for autograd: tensors that require a gradient are
+refused while gradients are recorded.
 """
 from __future__ import annotations
 
@@ -102,8 +104,20 @@ class RopePlan:
         self.amplitude = self._c.amplitude
 
 
+def _graded(t):
+    return getattr(t, "requires_grad", False)
+
+
+def _no_gradient(what):
+    """Autograd records nothing of a call: it is refused rather than cut out of a graph that is being recorded."""
+    if torch.is_grad_enabled():
+        raise ValueError(f"{what}: requires a gradient, which this call does not record; use torch.no_grad()")
+
+
 def _rows(t, what, dtype, device, rows=None, heads=None, dim=None):
     """A [rows, heads, head_dim] tensor's (pointer, row stride, head stride)."""
+    if _graded(t):
+        _no_gradient(what)
     shape, stride = t.shape, t.stride()
     if t.dtype is dtype and t.get_device() == device and len(shape) == 3 and stride[2] == 1 and \
             (rows is None or shape[0] == rows) and (heads is None or shape[1] == heads) and \
@@ -203,7 +217,7 @@ def rope(plan: RopePlan, q, k, positions, *, backward: bool = False, q_out=None,
     at positions [rows] int32; returns (q_out, k_out), new contiguous tensors
     unless given (an input itself: in place).  Any strides of rows and heads.
     backward=True applies the transposed rotation: the inputs' gradient from
-    the outputs'."""
+    the outputs', for a caller's own autograd function."""
     device, dtype = _cuda_half(q, "q"), q.dtype
     raw = _raw_stream(stream, device)
     qs = _rows(q, "q", dtype, device)
@@ -249,6 +263,8 @@ class PagedCache:
     calls.  `status` collects the device-side checks of the calls on it: keep
     the cache as long as calls or captured graphs use it."""
 
+    _graded = None  # a pool that requires a gradient
+
     def __init__(self, k_pool, v_pool, page_table):
         device = _cuda_half(k_pool, "k_pool")
         for what, t in (("k_pool", k_pool), ("v_pool", v_pool)):
@@ -268,6 +284,7 @@ class PagedCache:
                                  "expanded tables: make them contiguous")
             table_stride = width  # of a single row
         self.k_pool, self.v_pool, self.page_table = k_pool, v_pool, page_table
+        self._graded = "k_pool" if _graded(k_pool) else "v_pool" if _graded(v_pool) else None
         self.status = _clear_word(k_pool.device)
         self.device, self.dtype = device, k_pool.dtype
         self.n_pages, self.page_size, self.kv_heads, self.head_dim = k_pool.shape
@@ -300,6 +317,8 @@ def append(cache: PagedCache, k, v, cu_rows, ctx_len, *, plan: RopePlan = None, 
     [rows, q_heads, head_dim], if given, is rotated alike; returns q_out (None
     without q, which takes no q_out)."""
     device, dtype, dim = cache.device, cache.dtype, cache.head_dim
+    if cache._graded:
+        _no_gradient(cache._graded)
     raw = _raw_stream(stream, device)
     ks = _rows(k, "k", dtype, device, None, cache.kv_heads, dim)
     rows = k.shape[0]
@@ -333,6 +352,8 @@ def attention(cache: PagedCache, q, cu_rows, ctx_len, *, kv_len=None, causal: bo
     uint8, attention_workspace() bytes (0 for small calls); by default allocated
     for the call."""
     device, dtype, dim = cache.device, cache.dtype, cache.head_dim
+    if cache._graded:
+        _no_gradient(cache._graded)
     raw = _raw_stream(stream, device)
     qs = _rows(q, "q", dtype, device, None, None, dim)
     rows, hq, _ = q.shape
@@ -349,6 +370,8 @@ def attention(cache: PagedCache, q, cu_rows, ctx_len, *, kv_len=None, causal: bo
         if lse.dtype is not torch.float32 or lse.get_device() != device or tuple(lse.shape) != (rows, hq):
             raise ValueError(f"lse: expected float32 [{rows}, {hq}] on cuda:{device}, got {list(lse.shape)} {lse.dtype} "
                              f"on {lse.device}")
+        if _graded(lse):
+            _no_gradient("lse")
         ls = (lse.data_ptr(), lse.stride(0), lse.stride(1))
     lib = load()
     if workspace is None:

@@ -468,3 +468,48 @@ def test_paged_calls_refuse_outputs_that_share_memory(lib):
            append(cache=_paged(v=1 << 24)), append(cache=_paged(v=(1 << 24) + 4096)), append(cache=_paged(ks=(0, 128, 64))),
            append(cache=_paged(ks=(2048, 64, 64))), append(cache=_paged(ks=(64, 64 * 4, 64 * 4 * 16)))]
     assert bad == [1] * len(bad), bad
+
+
+def _graded(shape, **kw):
+    t = FakeT(shape, **kw)
+    t.requires_grad = True
+    return t
+
+
+def test_tensors_that_require_a_gradient_are_refused_while_gradients_are_recorded(calls):
+    """The calls are not differentiable by autograd: the graph would be dropped without a word."""
+    tries = [(lambda: _rope(q=_graded([7, 4, 128])), "q"), (lambda: _rope(k=_graded([7, 2, 128], ptr=1 << 28)), "k"),
+             (lambda: _rope(q_out=_graded([7, 4, 128], ptr=1 << 30)), "q_out"),
+             (lambda: _rope(k_out=_graded([7, 2, 128], ptr=1 << 31)), "k_out"),
+             (lambda: _append(q=_graded([7, 4, 128])), "q"), (lambda: _append(k=_graded([7, 2, 128], ptr=1 << 28)), "k"),
+             (lambda: _append(v=_graded([7, 2, 128], ptr=1 << 29)), "v"),
+             (lambda: _append(q_out=_graded([7, 4, 128], ptr=1 << 30)), "q_out"),
+             (lambda: _attention(q=_graded([7, 4, 128])), "q"),
+             (lambda: _attention(out=_graded([7, 4, 128], ptr=1 << 30)), "out"),
+             (lambda: _attention(lse=_graded([7, 4], dtype=torch.float32)), "lse")]
+    for call, name in tries:
+        with pytest.raises(ValueError, match="^%s: requires a gradient" % name):
+            call()
+    assert [c for c in calls if "workspace" not in c] == []
+    with torch.no_grad():
+        for call, _ in tries:
+            call()
+    with torch.inference_mode():
+        tries[0][0]()
+    assert len([c for c in calls if "workspace" not in c]) == len(tries) + 1
+
+
+@pytest.mark.parametrize("which", ["k_pool", "v_pool"])
+def test_pools_that_require_a_gradient_are_refused_while_gradients_are_recorded(calls, no_device, which):
+    pools = {"k_pool": FakeT([8, 64, 2, 128], ptr=1 << 35), "v_pool": FakeT([8, 64, 2, 128], ptr=1 << 36)}
+    pools[which].requires_grad = True
+    cache = ops.PagedCache(*pools.values(), FakeT([3, 4], I32, ptr=1 << 37))
+    q, cu, ctx = FakeT([7, 4, 128]), FakeT([4], I32), FakeT([3], I32)
+    k, v = FakeT([7, 2, 128], ptr=1 << 28), FakeT([7, 2, 128], ptr=1 << 29)
+    for call in (lambda: ops.append(cache, k, v, cu, ctx, stream=Stream()),
+                 lambda: ops.attention(cache, q, cu, ctx, out=FakeT([7, 4, 128], ptr=1 << 30),
+                                       workspace=FakeT([256], torch.uint8), stream=Stream())):
+        with pytest.raises(ValueError, match="^%s: requires a gradient" % which):
+            call()
+        with torch.no_grad():
+            call()
