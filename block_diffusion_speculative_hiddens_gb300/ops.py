@@ -56,6 +56,12 @@ _ATTENTION = struct.Struct("@" + 2 * _ROWS + "PqqPPPPq5if0q")
 _NONE = (0, 0, 0)
 
 
+def _int32(v, what):
+    if v != int(v) or not -2 ** 31 <= v < 2 ** 31:
+        raise ValueError(f"{what}: expected a 32-bit whole number, got {v}")
+    return int(v)
+
+
 class RopePlan:
     """The rotation of a model's heads: `rotary_dim` leading dims in pairs
     (i, i + rotary_dim/2), or (2i, 2i+1) if interleaved, at angle
@@ -70,6 +76,7 @@ class RopePlan:
     Held on the host; calls pass it to their kernels by value."""
 
     def __init__(self, rotary_dim: int, theta: float = 1e4, *, interleaved: bool = False, scaling: dict = None):
+        rotary_dim = _int32(rotary_dim, "rotary_dim")
         s = dict(scaling or {"kind": "none"})
         kind = s.pop("kind", None)
         if kind not in _KINDS:
@@ -89,7 +96,8 @@ class RopePlan:
                 raise ValueError(f"scaling: {len(s['factors'])} factors for {rotary_dim // 2} pairs")
             factors = (ctypes.c_double * len(s["factors"]))(*s["factors"])
         cfg = RopeConfig(rotary_dim=rotary_dim, interleaved=int(bool(interleaved)), scaling=_KINDS[kind],
-                         original_len=int(s.get("original_len", 0)), theta=theta, factor=s.get("factor", 1.0),
+                         original_len=_int32(s.get("original_len", 0), "original_len"), theta=theta,
+                         factor=s.get("factor", 1.0),
                          beta_fast=s.get("beta_fast", 32.0), beta_slow=s.get("beta_slow", 1.0),
                          low_freq=s.get("low_freq_factor", 1.0), high_freq=s.get("high_freq_factor", 4.0),
                          attention_factor=s.get("attention_factor", 0.0),

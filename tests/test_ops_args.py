@@ -513,3 +513,19 @@ def test_pools_that_require_a_gradient_are_refused_while_gradients_are_recorded(
             call()
         with torch.no_grad():
             call()
+
+
+@pytest.mark.parametrize("kw", [dict(rotary_dim=2 ** 32 + 64), dict(rotary_dim=-2 ** 32 + 64),
+                                dict(scaling={"kind": "yarn", "factor": 4.0, "original_len": 2 ** 32 + 4096}),
+                                dict(scaling={"kind": "llama3", "factor": 4.0, "original_len": 2 ** 31}),
+                                dict(scaling={"kind": "yarn", "factor": 4.0, "original_len": 4096.5})])
+def test_plan_refuses_whole_numbers_that_do_not_fit(lib, kw):
+    """They were cut to 32 bits, or to a whole number, and another rotation came back."""
+    with pytest.raises(ValueError, match="32-bit whole number"):
+        ops.RopePlan(kw.pop("rotary_dim", 64), 1e4, **kw)
+
+
+def test_plan_takes_whole_numbers_of_other_types(lib):
+    want = ops.RopePlan(64, 1e4, scaling={"kind": "yarn", "factor": 4.0, "original_len": 4096})
+    got = ops.RopePlan(torch.tensor(64).item(), 1e4, scaling={"kind": "yarn", "factor": 4.0, "original_len": 4096.0})
+    assert bytes(got._c) == bytes(want._c)
