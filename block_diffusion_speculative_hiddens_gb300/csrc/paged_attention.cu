@@ -55,6 +55,7 @@
 //   tiles (826 for 716).
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <mutex>
 
 #include "common.cuh"
@@ -64,6 +65,7 @@
 namespace {
 
 constexpr int KT = 128;  // keys of a tile
+constexpr float LOG2E = 1.4426950408889634f;
 // What an item costs beside its tiles, in tiles: the load of Q, the first and
 // last tile that overlap nothing, the output.  Measured with 1, 2 and 3 (us):
 // a prompt of 8,192 428 / 357 / 358, a window of 1,024 146 / 142 / 142, ragged
@@ -1377,7 +1379,7 @@ size_t dflash_paged_attention_workspace(const dflash_paged_cache* c, int32_t row
 }
 
 int dflash_paged_attention(const dflash_paged_cache* c, const dflash_attention_args* a, void* stream) {
-  if (!a || a->rows < 0 || a->batch < 0 || a->window < 0 || !(a->scale == a->scale)) return DFLASH_ERR_INVALID_ARG;
+  if (!a || a->rows < 0 || a->batch < 0 || a->window < 0 || !std::isfinite(a->scale * LOG2E)) return DFLASH_ERR_INVALID_ARG;
   if (int e = paged_cache_check(c)) return e;
   const int D = c->head_dim;
   if (!shape_ok(c, a->q_heads)) return DFLASH_ERR_SHAPE;
@@ -1430,7 +1432,7 @@ int dflash_paged_attention(const dflash_paged_cache* c, const dflash_attention_a
   p.window = a->window;
   p.tok = 128 / group;
   // a scale of zero weighs every key alike; the tiny one does, and keeps a mask's -inf
-  const float scale = a->scale * 1.4426950408889634f;
+  const float scale = a->scale * LOG2E;
   p.negate = scale < 0.f;
   p.scale_log2 = scale == 0.f ? 1e-30f : p.negate ? -scale : scale;
   p.status = c->status;

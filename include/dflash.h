@@ -551,7 +551,7 @@ DFLASH_API int dflash_paged_append(const dflash_paged_cache* cache, const dflash
  * pages that hold a seen position are read, and of the last of them nothing
  * behind kv_len reaches the result; a non-finite value within kv_len reaches
  * rows that mask it only through v.
- * Supported: head_dim 64 or 128, q_heads a multiple of kv_heads, at most 32
+ * Supported: scale finite (and times 1.4427), head_dim 64 or 128, q_heads a multiple of kv_heads, at most 32
  * times; q, out and the pools 16-byte aligned with strides that are multiples
  * of 8 elements.  A page that is not in the pool reads as zeros and sets
  * DFLASH_DEV_PAGE; a position beyond the table is not seen and sets it too.

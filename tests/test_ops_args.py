@@ -529,3 +529,11 @@ def test_plan_takes_whole_numbers_of_other_types(lib):
     want = ops.RopePlan(64, 1e4, scaling={"kind": "yarn", "factor": 4.0, "original_len": 4096})
     got = ops.RopePlan(torch.tensor(64).item(), 1e4, scaling={"kind": "yarn", "factor": 4.0, "original_len": 4096.0})
     assert bytes(got._c) == bytes(want._c)
+
+
+def test_scales_without_a_softmax_are_refused(lib):
+    """Infinite, or infinite once in the logarithm's base: every score would be infinite or NaN."""
+    c = _paged()
+    for scale, code in ((math.inf, 1), (-math.inf, 1), (3e38, 1), (-3e38, 1), (math.nan, 1), (1e38, 4), (0.0, 4), (-0.1, 4)):
+        a = ops._ATTENTION.pack(1 << 20, 256, 64, 1 << 21, 256, 64, 0, 0, 0, 1 << 28, 1 << 29, 0, 0, 0, 1, 1, 4, 1, 0, scale)
+        assert lib.dflash_paged_attention(c, a, None) == code, scale
