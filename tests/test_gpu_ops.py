@@ -751,3 +751,88 @@ def test_outputs_over_other_tensors_of_the_call_are_refused(ops):
     assert torch.equal(out, ops.attention(pg.cache, q, cu, ctx))
     same = ops.attention(ops.PagedCache(pg.kp, pg.kp, pg.table), q, cu, ctx)
     assert torch.equal(same, ops.attention(ops.PagedCache(pg.kp, pg.kp.clone(), pg.table), q, cu, ctx))
+
+
+# ------------------------------------------------------------------ calls at the documentation's edges
+
+@pytest.mark.parametrize("cols", [0, 20, 500])
+@pytest.mark.parametrize("heads,rows,ctx", [((32, 8, 128), [16], [2048]), ((16, 2, 64), [16, 1, 3], [700, 2000, 0]),
+                                            ((8, 2, 128), [200, 16], [0, 900])])
+def test_attention_over_tables_wider_than_their_sequences(ops, heads, rows, ctx, cols):
+    """The table's width chooses the launch, never the answer; its unused entries are not read."""
+    hq, hkv, dim = heads
+    lens = [a + b for a, b in zip(rows, ctx)]
+    pg = Paged(ops, lens, hkv, dim, 64, BF16, extra_cols=cols)
+    q = torch.randn(sum(rows), hq, dim, generator=gen(1), device="cuda").to(BF16)
+    cu = [sum(rows[:i]) for i in range(len(rows) + 1)]
+    lse = torch.zeros(hq, sum(rows), device="cuda").t()  # heads first
+    out = ops.attention(pg.cache, q, i32(cu), i32(ctx), lse=lse)
+    for b in range(len(rows)):
+        r = slice(cu[b], cu[b + 1])
+        o, l, mag, ds, seen = ops_ref.attention(q[r], pg.k[b], pg.v[b], ctx[b], lens[b], True, 0, dim ** -0.5)
+        to, tl = ops_ref.attention_tolerance(o, l, mag, ds, seen, BF16, dim, pg.v[b].abs().max().item())
+        close(out[r], o, to, ("out", b))
+        close(lse[r], l, tl, ("lse", b))
+    assert pg.cache.read_status() == 0
+
+
+@pytest.mark.parametrize("heads", [(4, 2, 64), (8, 1, 128)], ids=["d64", "d128"])
+def test_largest_batch(ops, heads):
+    """8,192 sequences, none to three rows each: append and attention."""
+    hq, hkv, dim = heads
+    n = 8192
+    rows, ctx = [(i * 5) % 4 for i in range(n)], [(i * 3) % 14 for i in range(n)]
+    kp, vp = (torch.full((n + 3, 16, hkv, dim), math.nan, dtype=BF16, device="cuda") for _ in range(2))
+    table = torch.randperm(n + 3, generator=gen(1), device="cuda")[:n].to(I32)[:, None].contiguous()  # a page each
+    cache = ops.PagedCache(kp, vp, table)
+    cu = torch.tensor([0] + rows, device="cuda").cumsum(0).to(I32)
+    t = sum(rows)
+    # every sequence's positions hold the same keys: rows at one position differ in their queries alone
+    k, v = (torch.randn(16, hkv, dim, generator=gen(s), device="cuda").to(BF16) for s in (3, 4))
+    kp[:], vp[:] = k, v
+    q = torch.randn(t, hq, dim, generator=gen(5), device="cuda").to(BF16)
+    seq = torch.repeat_interleave(torch.arange(n, device="cuda"), torch.tensor(rows, device="cuda"))
+    pos = i32(ctx)[seq].long() + torch.arange(t, device="cuda") - cu.long()[seq]
+    got = ops.append(cache, k[pos], v[pos], cu, i32(ctx), q=q)
+    assert torch.equal(got, q) and cache.read_status() == 0
+    out = ops.attention(cache, q, cu, i32(ctx))
+    assert cache.read_status() == 0
+    for p in range(16):  # rows at position p see the keys 0..p, whoever they belong to
+        at = pos == p
+        if at.any():
+            o, l, mag, ds, seen = ops_ref.attention(q[at], k[:p + 1], v[:p + 1], p, p + 1, False, 0, dim ** -0.5)
+            close(out[at], o, ops_ref.attention_tolerance(o, l, mag, ds, seen, BF16, dim, v.abs().max().item())[0], p)
+
+
+def test_batches_of_empty_sequences(ops):
+    """Rows but no sequence that has one: nothing is written, in every form of the launch."""
+    for rows, batch, dim, cols in ((3, 2, 64, 0), (200, 2, 128, 0), (500, 300, 128, 0), (40, 300, 64, 600)):
+        pg = Paged(ops, [70] * batch, 2, dim, 64, BF16, extra_cols=cols)
+        k, v = pg.kp.clone(), pg.vp.clone()
+        x = torch.ones(rows, 4, dim, dtype=BF16, device="cuda")
+        out, q_out = x * 2, x * 3
+        cu, ctx = i32([0] * (batch + 1)), i32([5] * batch)
+        ops.append(pg.cache, x[:, :2], x[:, 2:], cu, ctx, q=x, q_out=q_out)
+        ops.attention(pg.cache, x, cu, ctx, out=out)
+        assert (out == 2).all() and (q_out == 3).all() and pg.cache.read_status() == 0
+        assert torch.equal(pg.kp.nan_to_num(9), k.nan_to_num(9)) and torch.equal(pg.vp.nan_to_num(9), v.nan_to_num(9))
+
+
+def test_inputs_expanded_over_rows_and_heads(ops):
+    """Inputs may share memory with themselves: one row for all, one head for all."""
+    plan = ops.RopePlan(128, 1e4)
+    for rows, ctx in (([16], [300]), ([1, 250], [900, 20])):
+        pg = Paged(ops, [a + b for a, b in zip(rows, ctx)], 2, 128, 64, BF16)
+        cu, cx, t = i32([0] + [sum(rows[:i + 1]) for i in range(len(rows))]), i32(ctx), sum(rows)
+        pos = torch.arange(t, device="cuda").to(I32)
+        base = torch.randn(t, 8, 128, generator=gen(1), device="cuda").to(BF16)
+        for q in (base[:1].expand(t, 8, 128), base[:, :1].expand(t, 8, 128), base[:1, :1].expand(t, 8, 128)):
+            assert torch.equal(ops.attention(pg.cache, q, cu, cx), ops.attention(pg.cache, q.contiguous(), cu, cx))
+            assert torch.equal(ops.rope(plan, q, None, pos)[0], ops.rope(plan, q.contiguous(), None, pos)[0])
+            k = q[:, :2]
+            for x in (k, k.contiguous()):
+                ops.append(pg.cache, x, x, cu, cx, plan=plan)
+                now = (pg.kp.nan_to_num(9), pg.vp.nan_to_num(9))
+                first = now if x is k else first
+            assert all(torch.equal(a, b) for a, b in zip(first, now))
+    assert pg.cache.read_status() == 0
