@@ -21,14 +21,18 @@
 //               the row's O is rescaled in TMEM): P is the same softmax up to a
 //               power of two that the sum shares, and stays inside f16.  P is
 //               rounded to the operands' 16 bits, as the tensor core takes it;
-//               maxima, sums and O are float32.
+//               maxima, sums and O are float32.  Outputs are then 0.0022 of
+//               their size from the 64-bit result in bf16 and 0.00028 in f16,
+//               where the output's own rounding alone gives 0.0017 and 0.0002.
 //   O += P V    tcgen05.mma with P as the TMEM A operand (over the S it came
 //               from) and V as it lies in the cache (N-major).
 // The tensor core runs one thread's MMAs in issue order, so S of the next tile
 // may overwrite the P that the O MMA before it read.
 // Warps: 4 NM softmax, one issuing MMAs, one loading.
 //
-// Bounds and measurements (GB300; 32 query and 8 KV heads of 128, bf16):
+// Bounds and measurements (GB300; 32 query and 8 KV heads of 128, bf16; replayed
+// in a graph from idle, near the highest clock: among other calls the clock falls
+// and the chunk takes 724 to 743 us, the whole prompt 385):
 // - One token each for 64 requests of 512 to 4,096 positions reads 605 MB in
 //   100 us (6.0 TB/s, 0.89 of the copy rate); the runs themselves keep 0.95,
 //   finding them, the first load and the merge take 9 us.
@@ -65,6 +69,7 @@
 namespace {
 
 constexpr int KT = 128;  // keys of a tile
+constexpr int MAX_BATCH = 8192;  // sequences of a call
 constexpr float LOG2E = 1.4426950408889634f;
 // What an item costs beside its tiles, in tiles: the load of Q, the first and
 // last tile that overlap nothing, the output.  Measured with 1, 2 and 3 (us):
@@ -649,6 +654,7 @@ __global__ void __launch_bounds__(PCfg<D, NM>::THREADS, 1)
   Item* items = reinterpret_cast<Item*>(sm + C::OFF_ITEM);
   static_assert((2 * C::SLOTS + 15 + 2 * ITEMS) * 8 + 8 <= 384 && sizeof(Sched) <= 192 && sizeof(Item) * ITEMS == 128,
                 "barrier area");
+  static_assert(C::THREADS * sizeof(Seq) + (MAX_BATCH + 1) * sizeof(int) <= C::OFF_BAR, "tile area");
 
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   constexpr int MMA_WARP = 4 * NM, LOAD_WARP = 4 * NM + 1;
@@ -1388,7 +1394,8 @@ int dflash_paged_attention(const dflash_paged_cache* c, const dflash_attention_a
       !rows_ok({c->k, c->k_pos_stride, c->k_head_stride}) || !rows_ok({c->v, c->v_pos_stride, c->v_head_stride}) ||
       c->k_page_stride % 8 || c->v_page_stride % 8)
     return DFLASH_ERR_INVALID_ARG;
-  if (a->batch > 8192) return DFLASH_ERR_CAPACITY;  // the sequences' first pairs lie in one M tile's shared memory
+  // the sequences' first pairs, up to 33 KB, lie behind `seqs` in the tile area, which holds nothing else then
+  if (a->batch > MAX_BATCH) return DFLASH_ERR_CAPACITY;
   if ((reinterpret_cast<uintptr_t>(a->workspace) & 255) || a->workspace_bytes < 0) return DFLASH_ERR_WORKSPACE;
   const int hq = a->q_heads;
   const Strided q = strided_rows(a->q, a->rows, hq, D), out = strided_rows(a->out, a->rows, hq, D),

@@ -2,8 +2,9 @@
 paged cache, and the attention of new tokens over it.
 
 The library drafts and accepts; verifying is the caller's target, of any depth
-and in the caller's own engine.  In every layer of it these three calls go
-from the projections' q, k and v to the attention's output:
+and in the caller's own engine.  In every layer of it these calls go from the
+projections' q, k and v (or, in a layer that normalises each head of q and k,
+from what that norm gives) to the attention's output:
 
     plan = RopePlan(128, 1e6)                              # once a model
     cache = PagedCache(k_pool, v_pool, page_table)         # once a layer
@@ -16,11 +17,13 @@ The C entry points, their argument structs, limits and device-side checks are
 in include/dflash.h; this module checks the tensors (ValueError) and passes
 their pointers and strides.  Calls go to the current stream of the tensors'
 device (or `stream`), enqueue and return, and may be captured into a graph;
-outputs that are not given are allocated on that stream.  Those that are given
-may be their own input (in place); over anything else of the call, or over
-themselves, they are refused (ValueError, or DflashError from the C entry).
-The calls record nothing for autograd: tensors that require a gradient are
-refused while gradients are recorded.
+outputs that are not given are allocated on that stream.  With `stream`, the
+tensors are ready on it and stay allocated until it is done, as for any work on
+a stream of one's own.  Outputs that are given may be their own input (in
+place); over anything else of the call, or over themselves, they are refused
+(ValueError, or DflashError from the C entry).  The calls record nothing for
+autograd: tensors that require a gradient are refused while gradients are
+recorded.
 """
 from __future__ import annotations
 
@@ -391,8 +394,8 @@ def attention(cache: PagedCache, q, cu_rows, ctx_len, *, kv_len=None, causal: bo
                          f"{workspace.device}")
     else:
         nbytes = workspace.numel()
-    args = _ATTENTION.pack(*qs, *os_, *ls, cu, ctx, kv, 0 if workspace is None else workspace.data_ptr(), nbytes, rows, b, hq, bool(causal), window,
-                           dim ** -0.5 if scale is None else scale)
+    args = _ATTENTION.pack(*qs, *os_, *ls, cu, ctx, kv, 0 if workspace is None else workspace.data_ptr(), nbytes,
+                           rows, b, hq, bool(causal), window, dim ** -0.5 if scale is None else scale)
     code = lib.dflash_paged_attention(cache._c, args, raw)
     if code:
         raise DflashError("dflash_paged_attention", code)

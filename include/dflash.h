@@ -492,8 +492,12 @@ DFLASH_API int dflash_rope_init(const dflash_rope_config* cfg, dflash_rope_plan*
 
 /* Rotate the heads of q and (data non-null) k at positions[t] (DEVICE int32
  * [rows]): the first rotary_dim dims of a head by the plan, the others copied.
- * Any alignment and strides; an output may be its own input.  backward = 1 applies the transposed map: the gradient of the inputs
- * from the gradient of the outputs. */
+ * Any alignment and strides, but 16-byte accesses only where head_dim and
+ * rotary_dim are multiples of 16, pointers 16-byte aligned and strides multiples
+ * of 8, for all tensors of the call; 2-byte ones otherwise, at about 0.4 of the
+ * speed.  The append below moves its values the same way.  An output may be its
+ * own input.  backward = 1 applies the transposed map: the gradient of the
+ * inputs from the gradient of the outputs. */
 typedef struct dflash_rope_args {
   dflash_rows q, k, q_out, k_out;
   const int32_t* positions;
@@ -529,7 +533,9 @@ DFLASH_API int dflash_paged_read_status(const dflash_paged_cache* cache, uint32_
  * copied).  q (data non-null) is rotated alike into q_out, under dflash_rope's
  * rules.  A row whose position is negative or has no page (beyond the table,
  * or an entry outside the pool) is not written and sets DFLASH_DEV_PAGE; its
- * q is still rotated.  head_dim even, up to 256.  Rows of one call must have
+ * q is still rotated.  head_dim even, up to 256.  A row's sequence is searched
+ * among all of the batch: thousands of sequences are better appended in parts.
+ * Rows of one call must have
  * different places, and k and v, if they lie in the pools, places that the call
  * does not write. */
 typedef struct dflash_append_args {
@@ -549,8 +555,9 @@ DFLASH_API int dflash_paged_append(const dflash_paged_cache* cache, const dflash
  * gets out 0 and lse -inf.  out may be q.  lse (optional, float32 [rows][q_heads], strides of
  * its own): the natural logarithm of the row's sum of exponentials.  Only
  * pages that hold a seen position are read, and of the last of them nothing
- * behind kv_len reaches the result; a non-finite value within kv_len reaches
- * rows that mask it only through v.
+ * behind kv_len reaches the result.  Within kv_len a k that is not finite
+ * reaches the rows that see it alone, but a v that is not finite may also reach
+ * rows that mask its position (their weight for it is 0, times infinity).
  * Supported: scale finite (and times 1.4427), head_dim 64 or 128, q_heads a multiple of kv_heads, at most 32
  * times; q, out and the pools 16-byte aligned with strides that are multiples
  * of 8 elements.  A page that is not in the pool reads as zeros and sets

@@ -836,3 +836,24 @@ def test_inputs_expanded_over_rows_and_heads(ops):
                 first = now if x is k else first
             assert all(torch.equal(a, b) for a, b in zip(first, now))
     assert pg.cache.read_status() == 0
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf], ids=["nan", "inf"])
+@pytest.mark.parametrize("heads,n,ctx,window", [((8, 2, 128), 16, 300, 0), ((8, 2, 128), 16, 20000, 0), ((8, 2, 64), 200, 100, 0),
+                                                ((16, 2, 128), 300, 0, 0), ((8, 2, 64), 200, 900, 70)])
+def test_keys_that_are_not_finite_reach_the_rows_that_see_them_alone(ops, heads, n, ctx, window, bad):
+    hq, hkv, dim = heads
+    pg = Paged(ops, [ctx + n], hkv, dim, 64, BF16, extra_cols=500)
+    q = torch.randn(n, hq, dim, generator=gen(1), device="cuda").to(BF16)
+    cu, cx = i32([0, n]), i32([ctx])
+    want = ops.attention(pg.cache, q, cu, cx, window=window)
+    j = ctx + n // 2
+    pg.kp[pg.table[0, j // 64].long(), j % 64] = bad
+    got = ops.attention(pg.cache, q, cu, cx, window=window)
+    sees = torch.arange(n, device="cuda") >= n // 2
+    if window:
+        sees &= torch.arange(n, device="cuda") < n // 2 + window
+    assert torch.equal(got[~sees], want[~sees])
+    if bad != bad:
+        assert torch.isnan(got[sees]).all()
+    assert pg.cache.read_status() == 0
