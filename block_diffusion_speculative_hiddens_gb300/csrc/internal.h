@@ -231,11 +231,20 @@ struct DeviceGuard {
     ok = cudaGetDevice(&before) == cudaSuccess;
     if (ok && before == device) before = -1;  // nothing to give back
     else if (ok) ok = cudaSetDevice(device) == cudaSuccess;
+    if (!ok) before = -1, cudaGetLastError();
   }
   ~DeviceGuard() {
     if (before >= 0) cudaSetDevice(before);
   }
 };
+
+// A CUDA call's status as the library's.  The error is the caller's to handle:
+// it is not left for the next check of somebody else's launch.
+inline int cuda_status(cudaError_t e) {
+  if (e == cudaSuccess) return DFLASH_OK;
+  cudaGetLastError();
+  return DFLASH_ERR_CUDA;
+}
 
 inline int page_shift(int page_size) {
   int s = 0;

@@ -1365,13 +1365,13 @@ int launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, con
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pl.cs ? 2 : 1;
-  if (cudaLaunchKernelEx(&cfg, k_paged_attn<BF16, D, NM>, q, k, v, p) != cudaSuccess) return DFLASH_ERR_CUDA;
+  if (int e = cuda_status(cudaLaunchKernelEx(&cfg, k_paged_attn<BF16, D, NM>, q, k, v, p))) return e;
   if (pl.cs || pl.grid == 1) return DFLASH_OK;
   cudaLaunchConfig_t mc = cfg;
   mc.gridDim = dim3((unsigned)(pl.grid - 1), 8);
   mc.blockDim = dim3(MERGE_ROWS * D / 4);
   mc.dynamicSmemBytes = (size_t)pl.grid * 2 * MERGE_ROWS * sizeof(float);
-  return cudaLaunchKernelEx(&mc, k_paged_merge<BF16, D, NM>, p, pl.grid) == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
+  return cuda_status(cudaLaunchKernelEx(&mc, k_paged_merge<BF16, D, NM>, p, pl.grid));
 }
 
 }  // namespace

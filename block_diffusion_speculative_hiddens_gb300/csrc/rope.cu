@@ -284,7 +284,7 @@ int launch_rope(RopeParams& p, bool bf16_, bool vec, cudaStream_t s) {
                      : cudaLaunchKernelEx(&cfg, k_rope<true, false, APPEND>, p);
   else e = vec ? cudaLaunchKernelEx(&cfg, k_rope<false, true, APPEND>, p)
                : cudaLaunchKernelEx(&cfg, k_rope<false, false, APPEND>, p);
-  return e == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
+  return cuda_status(e);
 }
 
 void set_plan(RopeParams& p, const dflash_rope_plan* plan) {
@@ -406,12 +406,18 @@ int dflash_paged_read_status(const dflash_paged_cache* c, uint32_t* out) {
   if (!out) return DFLASH_ERR_INVALID_ARG;
   if (int e = paged_cache_check(c)) return e;
   DeviceGuard guard(c->device);
-  if (!guard.ok || cudaDeviceSynchronize() != cudaSuccess ||
-      cudaMemcpy(out, c->status, sizeof(uint32_t), cudaMemcpyDeviceToHost) != cudaSuccess)
-    return DFLASH_ERR_CUDA;
-  if (!*out) return DFLASH_OK;
-  k_clear_status<<<1, 1>>>(c->status, *out);
-  return cudaGetLastError() == cudaSuccess && cudaDeviceSynchronize() == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
+  if (!guard.ok) return DFLASH_ERR_CUDA;
+  uint32_t bits = 0;
+  if (int e = cuda_status(cudaDeviceSynchronize())) return e;
+  if (int e = cuda_status(cudaMemcpy(&bits, c->status, sizeof(bits), cudaMemcpyDeviceToHost))) return e;
+  if (bits) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = cfg.blockDim = dim3(1);
+    if (int e = cuda_status(cudaLaunchKernelEx(&cfg, k_clear_status, c->status, bits))) return e;
+    if (int e = cuda_status(cudaDeviceSynchronize())) return e;
+  }
+  *out = bits;
+  return DFLASH_OK;
 }
 
 int dflash_paged_append(const dflash_paged_cache* c, const dflash_rope_plan* plan, const dflash_append_args* a,

@@ -857,3 +857,32 @@ def test_keys_that_are_not_finite_reach_the_rows_that_see_them_alone(ops, heads,
     if bad != bad:
         assert torch.isnan(got[sees]).all()
     assert pg.cache.read_status() == 0
+
+
+@pytest.mark.parametrize("device", [17, 1000])
+def test_a_device_that_is_not_there_leaves_no_error_behind(ops, lib, device):
+    """The call says so, and what runs next does not take the error for its own."""
+    import ctypes
+    pg = Paged(ops, [6], 2, 64, 64, BF16)
+    pg.table.fill_(-1)
+    q, cu, ctx = torch.zeros(1, 4, 64, dtype=BF16, device="cuda"), i32([0, 1]), i32([5])
+    k, q_out, plan = torch.zeros(1, 2, 64, dtype=BF16, device="cuda"), torch.zeros_like(q), ops.RopePlan(64, 1e4)
+    rows = lambda t: (t.data_ptr(), t.stride(0), t.stride(1))
+    none = (0, 0, 0)
+    there = list(ops._CACHE.unpack(pg.cache._c))
+    gone = ops._CACHE.pack(*there[:-1], device)
+    word = ctypes.c_uint32(9)
+    calls = [lambda: lib.dflash_rope(plan._ref, ops._ROPE.pack(*rows(q), *none, *rows(q_out), *none, ctx.data_ptr(), 1, 4, 0, 64, 1,
+                                                               0, device), None),
+             lambda: lib.dflash_paged_append(gone, None, ops._APPEND.pack(*rows(k), *rows(k), *none, *none, cu.data_ptr(),
+                                                                          ctx.data_ptr(), 1, 1, 0, 0), None),
+             lambda: lib.dflash_paged_attention(gone, ops._ATTENTION.pack(*rows(q), *rows(q_out), 0, 0, 0, cu.data_ptr(),
+                                                                          ctx.data_ptr(), 0, 0, 0, 1, 1, 4, 1, 0, 0.1), None),
+             lambda: lib.dflash_paged_read_status(gone, ctypes.byref(word))]
+    for call in calls:
+        assert call() == 4
+        assert (torch.ones(5, device="cuda") * 2).sum().item() == 10
+        call()
+        ops.attention(pg.cache, q, cu, ctx)  # its page is not in the pool
+        assert pg.cache.read_status() == 4
+    assert word.value == 9
