@@ -18,7 +18,7 @@
 // rate; 7,500 rows appended with their queries (184 MB) 32.8 us, 5.6 TB/s.  A row a
 // CTA with two units of a thread in flight: four rows a CTA took 29.4 and 37.5 us,
 // one or three units in flight 31.3 and 29.6; the page looked up by a warp that
-// also computes angles 35.1 for 33.4 us of appending.  A call of 16 rows is 2.7 us
+// also computes angles 35.1 for 33.4 us of appending.  A call of 16 rows is 2.6 us
 // of launch, load, angles and store.
 // A row's sequence is searched 32 at a time by a warp: an append of one row each
 // takes 3.3 us for up to 64 sequences, 4.5 for 256 and 11.5 for 1,024.

@@ -46,7 +46,7 @@ extern "C" {
 
 typedef enum {
   DFLASH_OK = 0,
-  DFLASH_ERR_INVALID_ARG = 1, /* null pointer, negative size, batch > max_batch */
+  DFLASH_ERR_INVALID_ARG = 1, /* null pointer, negative size, batch > max_batch, outputs that share memory */
   DFLASH_ERR_SHAPE = 2,       /* shape the kernels do not support */
   DFLASH_ERR_CAPACITY = 3,    /* rows > max_rows, or the page pool is exhausted (device) */
   DFLASH_ERR_CUDA = 4,        /* a CUDA runtime call or kernel launch failed */
@@ -533,11 +533,10 @@ DFLASH_API int dflash_paged_read_status(const dflash_paged_cache* cache, uint32_
  * copied).  q (data non-null) is rotated alike into q_out, under dflash_rope's
  * rules.  A row whose position is negative or has no page (beyond the table,
  * or an entry outside the pool) is not written and sets DFLASH_DEV_PAGE; its
- * q is still rotated.  head_dim even, up to 256.  A row's sequence is searched
- * among all of the batch: thousands of sequences are better appended in parts.
- * Rows of one call must have
- * different places, and k and v, if they lie in the pools, places that the call
- * does not write. */
+ * q is still rotated.  head_dim even, up to 256.  Rows of one call must have
+ * different places; k and v that lie in the pools lie where the call does not
+ * write.  Each row's sequence is searched among the whole batch: thousands of
+ * sequences are better appended in parts. */
 typedef struct dflash_append_args {
   dflash_rows k, v, q, q_out;
   const int32_t* cu_rows;
@@ -552,16 +551,17 @@ DFLASH_API int dflash_paged_append(const dflash_paged_cache* cache, const dflash
  * row t sees: 0 <= j < kv_len[b] (null: ctx_len[b] + the sequence's rows), with
  * causal also j <= position, with window w > 0 also j > position - w.  Query
  * head h reads KV head h / (q_heads / kv_heads).  A row that sees no position
- * gets out 0 and lse -inf.  out may be q.  lse (optional, float32 [rows][q_heads], strides of
- * its own): the natural logarithm of the row's sum of exponentials.  Only
- * pages that hold a seen position are read, and of the last of them nothing
- * behind kv_len reaches the result.  Within kv_len a k that is not finite
- * reaches the rows that see it alone, but a v that is not finite may also reach
- * rows that mask its position (their weight for it is 0, times infinity).
- * Supported: scale finite (and times 1.4427), head_dim 64 or 128, q_heads a multiple of kv_heads, at most 32
- * times; q, out and the pools 16-byte aligned with strides that are multiples
- * of 8 elements.  A page that is not in the pool reads as zeros and sets
- * DFLASH_DEV_PAGE; a position beyond the table is not seen and sets it too.
+ * gets out 0 and lse -inf.  out may be q.  lse (optional, float32
+ * [rows][q_heads], strides of its own): the natural logarithm of the row's sum
+ * of exponentials.  Only pages that hold a seen position are read, and of the
+ * last of them nothing behind kv_len reaches the result.  Within kv_len a k that
+ * is not finite reaches the rows that see it alone, but a v that is not finite
+ * may also reach rows that mask its position (0 times infinity).
+ * Supported: scale finite, also times 1.4427; head_dim 64 or 128; q_heads a
+ * multiple of kv_heads, at most 32 times; q, out and the pools 16-byte aligned
+ * with strides that are multiples of 8 elements.  A page that is not in the
+ * pool reads as zeros and sets DFLASH_DEV_PAGE; a position beyond the table is
+ * not seen and sets it too.
  * workspace: DEVICE, 256-byte aligned, dflash_paged_attention_workspace
  * bytes (0 where the call needs none: it may be null), for this call alone
  * until it is done.  At most 8192 sequences a call (DFLASH_ERR_CAPACITY). */
