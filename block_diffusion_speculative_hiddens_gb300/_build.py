@@ -15,7 +15,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdflash.so")
-SOURCES = ["gemm.cu", "attention.cu", "small.cu", "api.cu", "rope.cu", "paged_attention.cu"]
+SOURCES = ["gemm.cu", "attention.cu", "small.cu", "api.cu", "rope.cu", "paged_attention.cu", "pages.cu", "beam.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-Xcompiler", "-fvisibility=hidden"]

@@ -98,6 +98,13 @@ _SIGS = {
     "dflash_paged_attention_workspace": (ctypes.c_size_t, [ctypes.c_char_p, ctypes.c_int32, ctypes.c_int32,
                                                            ctypes.c_int32]),
     "dflash_paged_attention": (ctypes.c_int, [ctypes.c_char_p, ctypes.c_char_p, _vp]),
+    "dflash_pool_read_status": (ctypes.c_int, [ctypes.c_char_p, ctypes.POINTER(ctypes.c_uint32)]),
+    "dflash_pages_resize": (ctypes.c_int, [ctypes.c_char_p, _vp, _vp, ctypes.c_int32, _vp]),
+    "dflash_pages_fork": (ctypes.c_int, [ctypes.c_char_p, _vp, _vp]),
+    "dflash_pages_compact": (ctypes.c_int, [ctypes.c_char_p, _vp, ctypes.c_int32, _vp, _vp]),
+    "dflash_pages_copy": (ctypes.c_int, [ctypes.c_char_p, ctypes.c_int32, _vp, ctypes.c_int32, _vp]),
+    "dflash_beam_select_workspace": (ctypes.c_size_t, [ctypes.c_int32] * 5),
+    "dflash_beam_select": (ctypes.c_int, [ctypes.c_char_p, _vp]),
 }
 
 _LIB = None

@@ -221,7 +221,7 @@ cudaError_t launch_harness_verify(const int* slots, int batch, int S, const int*
                                   const int* ctx_len, int max_slots, unsigned long long* stamp,
                                   unsigned* blocks_done, cudaStream_t s);
 
-// ---- operators of the caller's own target model (rope.cu, paged_attention.cu)
+// ---- operators of the caller's own target model (rope.cu, paged_attention.cu, pages.cu, beam.cu)
 
 // Makes `device` current for a call and gives the caller's back.
 struct DeviceGuard {
@@ -260,6 +260,10 @@ inline int paged_cache_check(const dflash_paged_cache* c) {
   if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1))) return DFLASH_ERR_SHAPE;
   return DFLASH_OK;
 }
+
+// Waits for the device, returns a status word in *out and clears the bits that
+// it returns (rope.cu).
+int read_status_word(uint32_t* status, int device, uint32_t* out);
 
 // A tiled TMA map over 16-bit values, 128-byte swizzle: `rank` sizes and boxes
 // (innermost first, box[0] = 64), rank - 1 strides in bytes.  False: the

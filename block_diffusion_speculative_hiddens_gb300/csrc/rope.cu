@@ -303,6 +303,23 @@ bool vec_ok(const dflash_rows& r) { return aligned16(r.data) && r.row_stride % 8
 
 }  // namespace
 
+// Waits for the device, returns a status word and clears the bits that it returns.
+int read_status_word(uint32_t* status, int device, uint32_t* out) {
+  DeviceGuard guard(device);
+  if (!guard.ok) return DFLASH_ERR_CUDA;
+  uint32_t bits = 0;
+  if (int e = cuda_status(cudaDeviceSynchronize())) return e;
+  if (int e = cuda_status(cudaMemcpy(&bits, status, sizeof(bits), cudaMemcpyDeviceToHost))) return e;
+  if (bits) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = cfg.blockDim = dim3(1);
+    if (int e = cuda_status(cudaLaunchKernelEx(&cfg, k_clear_status, status, bits))) return e;
+    if (int e = cuda_status(cudaDeviceSynchronize())) return e;
+  }
+  *out = bits;
+  return DFLASH_OK;
+}
+
 extern "C" {
 
 int dflash_rope_init(const dflash_rope_config* c, dflash_rope_plan* plan) {
@@ -405,19 +422,7 @@ int dflash_rope(const dflash_rope_plan* plan, const dflash_rope_args* a, void* s
 int dflash_paged_read_status(const dflash_paged_cache* c, uint32_t* out) {
   if (!out) return DFLASH_ERR_INVALID_ARG;
   if (int e = paged_cache_check(c)) return e;
-  DeviceGuard guard(c->device);
-  if (!guard.ok) return DFLASH_ERR_CUDA;
-  uint32_t bits = 0;
-  if (int e = cuda_status(cudaDeviceSynchronize())) return e;
-  if (int e = cuda_status(cudaMemcpy(&bits, c->status, sizeof(bits), cudaMemcpyDeviceToHost))) return e;
-  if (bits) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = cfg.blockDim = dim3(1);
-    if (int e = cuda_status(cudaLaunchKernelEx(&cfg, k_clear_status, c->status, bits))) return e;
-    if (int e = cuda_status(cudaDeviceSynchronize())) return e;
-  }
-  *out = bits;
-  return DFLASH_OK;
+  return read_status_word(c->status, c->device, out);
 }
 
 int dflash_paged_append(const dflash_paged_cache* c, const dflash_rope_plan* plan, const dflash_append_args* a,

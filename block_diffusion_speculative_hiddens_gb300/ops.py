@@ -1,5 +1,5 @@
 """Operators of a caller's own target model: rotary positions, the append to a
-paged cache, and the attention of new tokens over it.
+paged cache, the attention of new tokens over it; the cache's pages; beam search.
 
 The library drafts and accepts; verifying is the caller's target, of any depth
 and in the caller's own engine.  In every layer of it these calls go from the
@@ -13,6 +13,19 @@ from what that norm gives) to the attention's output:
 
 for a ragged batch of single tokens, verify blocks and prompt chunks: rows
 cu_rows[b] .. cu_rows[b+1]-1 are sequence b's, at positions ctx_len[b] and on.
+
+Which sequence holds which page, around a step of the whole model:
+
+    pool = PagePool(page_table, n_pages, page_size)        # once a model
+    copy_pages(caches, resize(pool, new_lens))             # room for the new tokens; every layer's cache
+    ...                                                    # the layers: append, attention
+    resize(pool, confirmed)                                # what was not confirmed is given back
+
+and of a beam search, whose sequences go on from one another:
+
+    scores, parents, tokens = beam_select(logits, scores)
+    fork(pool, parents)
+
 The C entry points, their argument structs, limits and device-side checks are
 in include/dflash.h; this module checks the tensors (ValueError) and passes
 their pointers and strides.  Calls go to the current stream of the tensors'
@@ -56,7 +69,10 @@ _ROPE = struct.Struct("@" + 4 * _ROWS + "P7i0q")
 _CACHE = struct.Struct("@PP6qPqP7i0q")
 _APPEND = struct.Struct("@" + 4 * _ROWS + "PP4i0q")
 _ATTENTION = struct.Struct("@" + 2 * _ROWS + "PqqPPPPq5if0q")
+_POOL = struct.Struct("@PPqPP6i0q")
+_BEAM = struct.Struct("@PqPPPPPPPq8i0q")
 _NONE = (0, 0, 0)
+_LOGITS = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 
 
 def _int32(v, what):
@@ -256,11 +272,11 @@ def rope(plan: RopePlan, q, k, positions, *, backward: bool = False, q_out=None,
     return q_out, k_out
 
 
-def _clear_word(device):
+def _clear_word(device, n=1):
     """A zero that calls on any stream find, not only those behind the current one.
     A captured one is the graph's: each replay clears it, ahead of the graph's calls."""
     with torch.cuda.device(device):
-        word = torch.zeros(1, dtype=torch.int32, device=device)
+        word = torch.zeros(n, dtype=torch.int32, device=device)
         if not torch.cuda.is_current_stream_capturing():
             torch.cuda.current_stream().synchronize()
     return word
@@ -284,16 +300,7 @@ class PagedCache:
                                  f"one device, got {list(t.shape)} {t.dtype} on {t.device}")
             if t.stride(3) != 1:
                 raise ValueError(f"{what}: the head dimension has stride {t.stride(3)}, expected 1")
-        if page_table.dim() != 2 or page_table.dtype is not torch.int32 or page_table.get_device() != device or \
-                page_table.stride(1) != 1:
-            raise ValueError(f"page_table: expected int32 [batch, max_pages] with contiguous rows on cuda:{device}, "
-                             f"got {list(page_table.shape)} {page_table.dtype} on {page_table.device}")
-        table_stride, width = page_table.stride(0), page_table.shape[1]
-        if table_stride < width:
-            if page_table.shape[0] > 1:
-                raise ValueError(f"page_table: rows overlap, stride {table_stride} for {width} entries; "
-                                 "expanded tables: make them contiguous")
-            table_stride = width  # of a single row
+        table_stride, width = _page_table(page_table, device)
         self.k_pool, self.v_pool, self.page_table = k_pool, v_pool, page_table
         self._graded = "k_pool" if _graded(k_pool) else "v_pool" if _graded(v_pool) else None
         self.status = _clear_word(k_pool.device)
@@ -405,3 +412,210 @@ def attention(cache: PagedCache, q, cu_rows, ctx_len, *, kv_len=None, causal: bo
 def attention_workspace(cache: PagedCache, rows: int, batch: int, q_heads: int) -> int:
     """Bytes of workspace that attention() of this shape needs."""
     return load().dflash_paged_attention_workspace(cache._c, rows, batch, q_heads)
+
+
+# ---- the pages of a cache
+
+def _page_table(t, device):
+    """A page table's row stride and width."""
+    if t.dim() != 2 or t.dtype is not torch.int32 or t.get_device() != device or t.stride(1) != 1:
+        raise ValueError(f"page_table: expected int32 [batch, max_pages] with contiguous rows on cuda:{device}, "
+                         f"got {list(t.shape)} {t.dtype} on {t.device}")
+    stride, width = t.stride(0), t.shape[1]
+    if stride < width:
+        if t.shape[0] > 1:
+            raise ValueError(f"page_table: rows overlap, stride {stride} for {width} entries; "
+                             "expanded tables: make them contiguous")
+        stride = width  # of a single row
+    return stride, width
+
+
+class PagePool:
+    """Who holds which page of a paged cache: page_table [batch, max_pages] int32
+    (the one that each layer's PagedCache was given), the lengths `lens` [batch]
+    int32 of its sequences, in positions, and `refs` [n_pages] int32, the holders of
+    each page.  refs and lens are new and zero -- nothing held -- unless given.  All
+    three may be read, and changed by the caller, between calls in stream order: a
+    page with refs 0 is free, one below 0 is never handed out, written or moved.
+    Calls on one pool follow one another.  `status` collects their device-side
+    checks."""
+
+    def __init__(self, page_table, n_pages: int, page_size: int, *, refs=None, lens=None):
+        device = page_table.get_device()
+        if device < 0:
+            raise ValueError(f"page_table: expected a CUDA tensor, got {page_table.dtype} on {page_table.device}")
+        stride, width = _page_table(page_table, device)
+        n_pages, page_size, batch = _int32(n_pages, "n_pages"), _int32(page_size, "page_size"), page_table.shape[0]
+        if refs is not None:
+            _i32(refs, "refs", n_pages, device)
+        if lens is not None:
+            _i32(lens, "lens", batch, device)
+        if n_pages < 1 or page_size not in (16, 32, 64, 128, 256):
+            raise ValueError(f"expected at least one page of 16, 32, 64, 128 or 256 positions, got {n_pages} of {page_size}")
+        self.page_table, self.n_pages, self.page_size, self.batch, self.device = page_table, n_pages, page_size, batch, device
+        self.refs = _clear_word(page_table.device, n_pages) if refs is None else refs
+        self.lens = _clear_word(page_table.device, batch) if lens is None else lens
+        self.status = _clear_word(page_table.device, 2)
+        self._c = _POOL.pack(self.refs.data_ptr(), page_table.data_ptr(), stride, self.lens.data_ptr(),
+                             self.status.data_ptr(), n_pages, page_size, width, batch, device, 0)
+
+    def read_status(self) -> int:
+        """DEV_* bits since the last call, and clears them.  Waits for the device:
+        calls on every stream are in.  Not during a capture."""
+        v = ctypes.c_uint32()
+        code = load().dflash_pool_read_status(self._c, ctypes.byref(v))
+        if code:
+            raise DflashError("dflash_pool_read_status", code)
+        return v.value
+
+
+def _moves(moves, least, pool, stream):
+    """Room for page copies -- the caller's, checked, or new -- and how many it takes."""
+    if moves is None:
+        return _empty((1 + least, 3), torch.int32, pool.page_table, stream), least
+    if moves.dtype is not torch.int32 or moves.get_device() != pool.device or len(moves.shape) != 2 or \
+            moves.shape[1] != 3 or moves.shape[0] < 1 + least or not moves.is_contiguous():
+        raise ValueError(f"moves: expected contiguous int32 [at least {1 + least}, 3] on cuda:{pool.device}, got "
+                         f"{list(moves.shape)} {moves.dtype} on {moves.device}")
+    return moves, moves.shape[0] - 1
+
+
+def resize(pool: PagePool, new_lens, *, moves=None, stream=None):
+    """Every sequence to its new length, new_lens [batch] int32 positions (0: it
+    ends): pages are given back or taken, the lowest free first, and a sequence that
+    grows inside a page which others hold gets a copy of it.  Returns the copies to
+    make, moves int32 [1 + batch, 3]: their number in row 0, then (source page,
+    destination page, positions) -- for copy_pages, ahead of the first append.  Not
+    enough free pages: nothing changes, DEV_CAPACITY in the pool's status."""
+    raw = _raw_stream(stream, pool.device)
+    new = _i32(new_lens, "new_lens", pool.batch, pool.device)
+    moves, capacity = _moves(moves, pool.batch, pool, stream)
+    code = load().dflash_pages_resize(pool._c, new, moves.data_ptr(), capacity, raw)
+    if code:
+        raise DflashError("dflash_pages_resize", code)
+    return moves
+
+
+def fork(pool: PagePool, parents, *, stream=None):
+    """Sequence b goes on as sequence parents[b] ([batch] int32; -1: it ends) of
+    before the call: it holds the same pages, at the same length, and gives up its
+    own.  Nothing is copied until resize finds one of them growing."""
+    raw = _raw_stream(stream, pool.device)
+    code = load().dflash_pages_fork(pool._c, _i32(parents, "parents", pool.batch, pool.device), raw)
+    if code:
+        raise DflashError("dflash_pages_fork", code)
+
+
+def compact(pool: PagePool, *, moves=None, remap=None, stream=None):
+    """Move the pages in use to the front: the held ones behind the first as many
+    pages as are in use go to the free ones among those.  Returns (moves, remap):
+    the copies to make, as of resize but [1 + n_pages // 2, 3], and each page's new
+    number, int32 [n_pages] (-1: it was free)."""
+    raw = _raw_stream(stream, pool.device)
+    moves, capacity = _moves(moves, pool.n_pages // 2, pool, stream)
+    if remap is None:
+        remap = _empty((pool.n_pages,), torch.int32, pool.page_table, stream)
+    code = load().dflash_pages_compact(pool._c, moves.data_ptr(), capacity, _i32(remap, "remap", pool.n_pages, pool.device),
+                                       raw)
+    if code:
+        raise DflashError("dflash_pages_compact", code)
+    return moves, remap
+
+
+def copy_pages(caches, moves, *, stream=None):
+    """Make the copies that resize or compact returned, in a PagedCache or in a
+    list of them, one a layer: alike but for their pools' places and strides."""
+    if isinstance(caches, PagedCache):
+        caches = (caches,)
+    if not caches:
+        raise ValueError("caches: expected at least one")
+    for c in caches:
+        if c._graded:
+            _no_gradient(c._graded)
+    device = caches[0].device
+    raw = _raw_stream(stream, device)
+    if moves.dtype is not torch.int32 or moves.get_device() != device or len(moves.shape) != 2 or moves.shape[1] != 3 or \
+            moves.shape[0] < 1 or not moves.is_contiguous():
+        raise ValueError(f"moves: expected contiguous int32 [1 + copies, 3] on cuda:{device}, got {list(moves.shape)} "
+                         f"{moves.dtype} on {moves.device}")
+    packed = caches[0]._c if len(caches) == 1 else b"".join([c._c for c in caches])
+    code = load().dflash_pages_copy(packed, len(caches), moves.data_ptr(), moves.shape[0] - 1, raw)
+    if code:
+        raise DflashError("dflash_pages_copy", code)
+
+
+# ---- beam search
+
+def beam_select(logits, scores, n: int = None, *, done=None, done_token: int = 0, out=None, status=None, workspace=None,
+                stream=None):
+    """The n best (default: as many as beams) continuations of each request among
+    its beams: logits [batch * beams, vocab] f16, bf16 or f32, scores [batch, beams]
+    float32; a token's score is its beam's plus its log-softmax.  done [batch, beams]
+    bool: these beams go on with done_token at their own score.  Returns (scores
+    float32, parents int32, tokens int32), each [batch, n], best first, ties to the
+    lowest beam and token; parents are rows of logits, as fork takes them; where
+    fewer are offered (-inf logits and scores are not), -inf, -1 and -1.  out: these
+    three, contiguous; scores itself may be the first if n is the number of beams.
+    status: an int32 word for DEV_NAN, such as a cache's or pool's `status`.
+    workspace: uint8, beam_workspace() bytes; by default allocated for the call."""
+    device = logits.get_device()
+    if logits.dtype not in _LOGITS or device < 0 or len(logits.shape) != 2 or logits.stride(1) != 1:
+        raise ValueError(f"logits: expected float16, bfloat16 or float32 [batch * beams, vocab] with contiguous rows on a "
+                         f"CUDA device, got {list(logits.shape)} {logits.dtype} on {logits.device}")
+    if _graded(logits) or _graded(scores):
+        _no_gradient("logits" if _graded(logits) else "scores")
+    raw = _raw_stream(stream, device)
+    rows, vocab = logits.shape
+    if scores.dtype is not torch.float32 or scores.get_device() != device or len(scores.shape) != 2 or \
+            scores.shape[0] * scores.shape[1] != rows or not scores.is_contiguous():
+        raise ValueError(f"scores: expected contiguous float32 [batch, beams], {rows} values, on cuda:{device}, got "
+                         f"{list(scores.shape)} {scores.dtype} on {scores.device}")
+    batch, beams = scores.shape
+    n = beams if n is None else _int32(n, "n")
+    if done is not None and (done.dtype not in (torch.bool, torch.uint8) or done.get_device() != device or
+                             done.shape != scores.shape or not done.is_contiguous()):
+        raise ValueError(f"done: expected contiguous bool {[batch, beams]} on cuda:{device}, got {list(done.shape)} "
+                         f"{done.dtype} on {done.device}")
+    if status is not None and (status.dtype is not torch.int32 or status.get_device() != device or status.numel() < 1):
+        raise ValueError(f"status: expected an int32 word on cuda:{device}, got {status.dtype} on {status.device}")
+    if out is None:
+        if n < 1:
+            raise ValueError(f"n: expected at least 1, got {n}")
+        o = _empty((3, batch, n), torch.int32, logits, stream)
+        at, step = o.data_ptr(), 4 * batch * n
+        ptrs = at, at + step, at + 2 * step
+        o, p, t = o.unbind()
+        out = o.view(torch.float32), p, t
+    else:
+        for what, t, dtype in zip(("scores", "parents", "tokens"), out, (torch.float32, torch.int32, torch.int32)):
+            if t.dtype is not dtype or t.get_device() != device or tuple(t.shape) != (batch, n) or not t.is_contiguous():
+                raise ValueError(f"out: expected contiguous {dtype} {[batch, n]} on cuda:{device} for {what}, got "
+                                 f"{list(t.shape)} {t.dtype} on {t.device}")
+            if _graded(t):
+                _no_gradient("out")
+        out = tuple(out)
+        ptrs = tuple(t.data_ptr() for t in out)
+    lib = load()
+    if workspace is None:
+        nbytes = lib.dflash_beam_select_workspace(batch, beams, vocab, n, _LOGITS[logits.dtype])
+        if nbytes:
+            workspace = _empty(nbytes, torch.uint8, logits, stream)
+    elif workspace.dtype is not torch.uint8 or workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace: expected contiguous uint8 on cuda:{device}, got {workspace.dtype} on "
+                         f"{workspace.device}")
+    else:
+        nbytes = workspace.numel()
+    args = _BEAM.pack(logits.data_ptr(), logits.stride(0), scores.data_ptr(), 0 if done is None else done.data_ptr(), *ptrs,
+                      0 if status is None else status.data_ptr(), 0 if workspace is None else workspace.data_ptr(), nbytes,
+                      batch, beams, vocab, n, _int32(done_token, "done_token"), _LOGITS[logits.dtype], device, 0)
+    code = lib.dflash_beam_select(args, raw)
+    if code:
+        raise DflashError("dflash_beam_select", code)
+    return out
+
+
+def beam_workspace(batch: int, beams: int, vocab: int, n: int, dtype) -> int:
+    """Bytes of workspace that beam_select() of this shape needs."""
+    if dtype not in _LOGITS:
+        raise ValueError(f"dtype: expected float16, bfloat16 or float32, got {dtype}")
+    return load().dflash_beam_select_workspace(batch, beams, vocab, n, _LOGITS[dtype])

@@ -582,6 +582,130 @@ DFLASH_API size_t dflash_paged_attention_workspace(const dflash_paged_cache* cac
                                                    int32_t q_heads);
 DFLASH_API int dflash_paged_attention(const dflash_paged_cache* cache, const dflash_attention_args* args, void* stream);
 
+/* ---- beam search and the pages of a paged cache ---------------------------
+ * What a caller that serves its own target needs around the calls above: who
+ * holds which page (dflash_page_pool), the pages of sequences that grow, shrink
+ * and end (resize), that go on from one another (fork), the copies of pages that
+ * this takes (copy), moving the pages in use to the front of the pools (compact),
+ * and the choice of the next beams among all their continuations (beam_select).
+ * The conventions are those of the calls above; calls on one pool follow one
+ * another (one stream, or events between streams).
+ *
+ * A pool's state.  lens[b] positions of sequence b are held: the first
+ * ceil(lens[b] / page_size) entries of its table row are pages, the rest of the
+ * row does not matter (entries that a call gives up become -1).  refs[p] is the
+ * number of entries that hold page p: 0 is free, and below 0 pinned -- such a
+ * page is never handed out, counted, written or moved, whoever holds it.  A
+ * caller's own holders of a page (a prefix kept for later requests) count too:
+ * add them to refs.  All of it is the caller's memory, zeros (refs, lens) for an
+ * empty pool; between calls it may read and change it in stream order.
+ * Positions below lens[b] may lie in pages that other sequences hold: they are
+ * read only.  To write at positions lens[b] and on, resize to the new length
+ * first; after fewer were confirmed, resize back. */
+#define DFLASH_POOL_MAX_BATCH 8192
+#define DFLASH_POOL_MAX_PAGES (1 << 24)
+
+typedef struct dflash_page_pool {
+  int32_t* refs;         /* DEVICE [n_pages] */
+  int32_t* page_table;   /* DEVICE [batch][table_stride] */
+  int64_t table_stride;  /* elements */
+  int32_t* lens;         /* DEVICE [batch] */
+  uint32_t* status;      /* DEVICE [2]: DFLASH_DEV_* bits, and a word of the calls' own, 0 between them */
+  int32_t n_pages;       /* 1..DFLASH_POOL_MAX_PAGES */
+  int32_t page_size;     /* 16, 32, 64, 128 or 256 */
+  int32_t max_pages;     /* entries of a table row */
+  int32_t batch;         /* rows of the table: 1..DFLASH_POOL_MAX_BATCH */
+  int32_t device, reserved;
+} dflash_page_pool;
+
+/* As dflash_paged_read_status, for the pool's word. */
+DFLASH_API int dflash_pool_read_status(const dflash_page_pool* pool, uint32_t* out);
+
+/* Page copies, as resize and compact leave them and copy takes them: DEVICE
+ * int32 [1 + capacity][3].  Row 0 holds their number (and two zeros); then one
+ * (source page, destination page, positions) a row, the rest (-1, -1, 0). */
+
+/* Sequence b, of all `batch`, now has new_lens[b] positions (DEVICE int32).  A
+ * shorter one gives up the pages behind its new end.  A longer one takes new
+ * pages, and if its last page is not full and others hold it too, a page of its
+ * own in its place, with a copy of what that held: moves gets (page, its new
+ * page, the positions held).  Where only growing sequences hold such a page, the
+ * lowest of them keeps it.  Pages are taken the lowest free first, sequence by
+ * sequence in order, a copy's page before the new ones; pages given up in a call
+ * are free from the next one on.  Run dflash_pages_copy before anything is
+ * written to the new lengths.
+ * If fewer pages are free than the call takes, nothing changes at all, moves is
+ * empty and DFLASH_DEV_CAPACITY is set.  A sequence whose new length does not fit
+ * its table row (DFLASH_DEV_CAPACITY) or whose old or new length is negative or,
+ * the old one, past the row (DFLASH_DEV_ARG) stays as it is, alone.  A held entry
+ * outside the pool, or given up where nobody holds it, is left out of the count
+ * and sets DFLASH_DEV_PAGE.  capacity >= batch, else DFLASH_ERR_CAPACITY. */
+DFLASH_API int dflash_pages_resize(const dflash_page_pool* pool, const int32_t* new_lens, int32_t* moves, int32_t capacity,
+                                   void* stream);
+
+/* Sequence b, of all `batch`, goes on as sequence parents[b] (DEVICE int32) of
+ * before the call: its pages and length; what it held itself is given up.  -1: it
+ * ends and is empty.  Any map: a beam search's, a prompt's row handed to many, a
+ * permutation.  A parent outside [-1, batch), or one whose length does not fit
+ * the table row, leaves the sequence as it is and sets DFLASH_DEV_ARG.  No page
+ * is copied: resize does that for the sequences that grow. */
+DFLASH_API int dflash_pages_fork(const dflash_page_pool* pool, const int32_t* parents, void* stream);
+
+/* Move pages so that those in use are the first ones of the pools, as far as
+ * pinned ones let them: with U pages in use (refs not 0), the held pages at U and
+ * on go to the free ones below U, both in ascending order.  refs and the table
+ * follow; moves gets the copies (all positions), remap (DEVICE int32 [n_pages])
+ * each old page's new place, its own where it stayed, -1 where it was free: for
+ * page numbers that the caller keeps elsewhere.  Run dflash_pages_copy before the
+ * cache is used again.  capacity >= n_pages / 2, else DFLASH_ERR_CAPACITY. */
+DFLASH_API int dflash_pages_compact(const dflash_page_pool* pool, int32_t* moves, int32_t capacity, int32_t* remap,
+                                    void* stream);
+
+/* Copy pages within the k and v pools of each of n_caches caches (one a layer;
+ * alike but for pointers and strides; a HOST array, read during the call): the
+ * first `positions` positions of each page in moves, at most moves[0][0] and
+ * capacity of them.  No page is the destination of two copies, or a source and a
+ * destination.  A page outside the pools is not copied and sets DFLASH_DEV_PAGE
+ * in the first cache's status. */
+DFLASH_API int dflash_pages_copy(const dflash_paged_cache* caches, int32_t n_caches, const int32_t* moves,
+                                 int32_t capacity, void* stream);
+
+/* The n best continuations of each of `batch` requests among its `beams` running
+ * sequences: row k of request b goes on with token v at
+ *   scores[b][k] + logits[b * beams + k][v] - log sum_w exp(logits[b * beams + k][w]),
+ * best first.  Scores are compared in 64 bits; of equal ones the lowest k goes
+ * first, of one beam's the larger logit, then the lower token.  The sums of
+ * exponentials are held in 32 bits a thread and 64 beyond.
+ * A beam with done set offers itself alone: done_token, at its score.  A score of
+ * -inf is a beam without continuations, a logit of -inf a token that is not
+ * offered; NaN and +inf count as -inf and set DFLASH_DEV_NAN.  Where fewer than n
+ * are offered the rest get score -inf, parent and token -1.
+ * parents[b][i] is the row b * beams + k, as fork takes it (n = beams).
+ * scores_out may be scores if n = beams.
+ * workspace: DEVICE, 256-byte aligned, dflash_beam_select_workspace bytes, for this
+ * call alone until it is done. */
+#define DFLASH_F32 2
+#define DFLASH_BEAM_MAX 64    /* beams */
+#define DFLASH_BEAM_MAX_N 128 /* n */
+
+typedef struct dflash_beam_args {
+  const void* logits;    /* DEVICE [batch * beams][vocab], f16, bf16 or f32 */
+  int64_t row_stride;    /* elements */
+  const float* scores;   /* DEVICE [batch][beams] */
+  const uint8_t* done;   /* DEVICE [batch][beams], or null */
+  float* scores_out;     /* DEVICE [batch][n] */
+  int32_t* parents;      /* DEVICE [batch][n] */
+  int32_t* tokens;       /* DEVICE [batch][n] */
+  uint32_t* status;      /* DEVICE word, or null */
+  void* workspace;
+  int64_t workspace_bytes;
+  int32_t batch, beams, vocab, n; /* beams * vocab < 2^31 */
+  int32_t done_token;             /* in [0, vocab) where done is given */
+  int32_t dtype, device, reserved;
+} dflash_beam_args;
+DFLASH_API size_t dflash_beam_select_workspace(int32_t batch, int32_t beams, int32_t vocab, int32_t n, int32_t dtype);
+DFLASH_API int dflash_beam_select(const dflash_beam_args* args, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
