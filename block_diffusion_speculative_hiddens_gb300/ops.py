@@ -581,11 +581,9 @@ def beam_select(logits, scores, n: int = None, *, done=None, done_token: int = 0
     if out is None:
         if n < 1:
             raise ValueError(f"n: expected at least 1, got {n}")
-        o = _empty((3, batch, n), torch.int32, logits, stream)
-        at, step = o.data_ptr(), 4 * batch * n
-        ptrs = at, at + step, at + 2 * step
-        o, p, t = o.unbind()
-        out = o.view(torch.float32), p, t
+        shape = batch, n
+        out = (_empty(shape, torch.float32, logits, stream), _empty(shape, torch.int32, logits, stream),
+               _empty(shape, torch.int32, logits, stream))
     else:
         for what, t, dtype in zip(("scores", "parents", "tokens"), out, (torch.float32, torch.int32, torch.int32)):
             if t.dtype is not dtype or t.get_device() != device or tuple(t.shape) != (batch, n) or not t.is_contiguous():
@@ -594,7 +592,6 @@ def beam_select(logits, scores, n: int = None, *, done=None, done_token: int = 0
             if _graded(t):
                 _no_gradient("out")
         out = tuple(out)
-        ptrs = tuple(t.data_ptr() for t in out)
     lib = load()
     if workspace is None:
         nbytes = lib.dflash_beam_select_workspace(batch, beams, vocab, n, _LOGITS[logits.dtype])
@@ -605,7 +602,8 @@ def beam_select(logits, scores, n: int = None, *, done=None, done_token: int = 0
                          f"{workspace.device}")
     else:
         nbytes = workspace.numel()
-    args = _BEAM.pack(logits.data_ptr(), logits.stride(0), scores.data_ptr(), 0 if done is None else done.data_ptr(), *ptrs,
+    args = _BEAM.pack(logits.data_ptr(), logits.stride(0), scores.data_ptr(), 0 if done is None else done.data_ptr(),
+                      out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(),
                       0 if status is None else status.data_ptr(), 0 if workspace is None else workspace.data_ptr(), nbytes,
                       batch, beams, vocab, n, _int32(done_token, "done_token"), _LOGITS[logits.dtype], device, 0)
     code = lib.dflash_beam_select(args, raw)
