@@ -26,18 +26,21 @@
 
 namespace {
 
-#ifndef BEAM_SLOTS
-#define BEAM_SLOTS (152 * 4)
-#endif
 #ifndef BEAM_AHEAD
 #define BEAM_AHEAD 4
+#define BEAM_MINB 4
+#endif
+#ifndef BEAM_JT
+#define BEAM_JT 512
 #endif
 constexpr int SCAN_THREADS = 256;
+constexpr int SCAN_CTAS = BEAM_MINB;      // of an SM
 constexpr int AHEAD = BEAM_AHEAD;          // vectors of a thread in flight
-constexpr int SEGMENTS = 4;       // of a part, with a maximum each
-constexpr int MAX_SPLITS = 64;    // parts of a row
+constexpr int SEGMENTS = 8;       // of a part, with a maximum each
+constexpr int AGAIN = 2;          // vectors of a thread that are looked at again at once
+constexpr int MAX_SPLITS = 32;    // parts of a row: a lane each when they are joined
 constexpr int MAX_LISTS = 1024;   // parts of a request's rows
-constexpr int JOIN_THREADS = 512;
+constexpr int JOIN_THREADS = BEAM_JT;
 constexpr int LIST_LANES = 8;     // of the join that look through a list together
 constexpr int KEEP = 640;         // keys that a selection holds: a push of one a thread, and what was kept before it
 
@@ -123,6 +126,7 @@ template <int T> struct Vec;
 template <> struct Vec<DFLASH_F32> {
   static constexpr int N = 4, SIZE = 4;
   static constexpr uint32_t NONE = 0xff800000u;  // -inf
+  DFL_DEV static float one(const char* p) { return *reinterpret_cast<const float*>(p); }
   DFL_DEV static void floats(const uint4& v, float* x) {
     x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y), x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
   }
@@ -139,6 +143,7 @@ template <> struct Vec<DFLASH_F32> {
 template <> struct Vec<DFLASH_BF16> {
   static constexpr int N = 8, SIZE = 2;
   static constexpr uint32_t NONE = 0xff80ff80u;
+  DFL_DEV static float one(const char* p) { return __bfloat162float(*reinterpret_cast<const bf16*>(p)); }
   DFL_DEV static void floats(const uint4& v, float* x) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -157,6 +162,7 @@ template <> struct Vec<DFLASH_BF16> {
 template <> struct Vec<DFLASH_F16> {
   static constexpr int N = 8, SIZE = 2;
   static constexpr uint32_t NONE = 0xfc00fc00u;
+  DFL_DEV static float one(const char* p) { return __half2float(*reinterpret_cast<const f16*>(p)); }
   DFL_DEV static void floats(const uint4& v, float* x) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -192,7 +198,7 @@ struct Row {
   int vocab;
   // vectors [1, inner()) lie inside
   DFL_DEV int inner() const { return vocab / Vec<T>::N - 1; }
-  DFL_DEV uint4 load_inner(int i) const {
+  DFL_DEV uint4 load(int i) const {  // one of those
     const char* at = data + (long long)i * 16;
     if (ALIGNED) return __ldg(reinterpret_cast<const uint4*>(at));
     const unsigned shift = (unsigned)(reinterpret_cast<uintptr_t>(data) & 15);
@@ -208,24 +214,7 @@ struct Row {
       default: return cut<3>(w, (shift & 3) * 8);
     }
   }
-  DFL_DEV uint4 load_end(int i) const {
-    constexpr int N = Vec<T>::N, SIZE = Vec<T>::SIZE;
-    const char* at = data + (long long)i * 16;
-    const int left = vocab - i * N;  // values from here on
-    uint32_t w[4] = {Vec<T>::NONE, Vec<T>::NONE, Vec<T>::NONE, Vec<T>::NONE};
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      if (j >= left) break;
-      if (SIZE == 4) {
-        w[j] = *reinterpret_cast<const uint32_t*>(at + 4 * j);
-      } else {
-        const uint32_t h = *reinterpret_cast<const uint16_t*>(at + 2 * j);
-        w[j >> 1] = j & 1 ? (w[j >> 1] & 0xffffu) | h << 16 : (w[j >> 1] & 0xffff0000u) | h;
-      }
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-  }
-  DFL_DEV uint4 load(int i) const { return i > 0 && i < inner() ? load_inner(i) : load_end(i); }
+  DFL_DEV float at(int token) const { return Vec<T>::one(data + (long long)token * Vec<T>::SIZE); }
 };
 
 // Groups whose maxima bound the n-th largest: enough for about n to 1.4 n values
@@ -237,40 +226,54 @@ DFL_DEV float pow2_or_0(float e) {  // 2^e for whole e <= 0, 0 where it is too s
   return e < -120.0f ? 0.0f : __uint_as_float((uint32_t)(127 + (int)e) << 23);
 }
 
+// Lanes that rank one of `count` values together: a power of two, up to a warp.
+DFL_DEV int rank_lanes(int threads, int count) {
+  const int per = threads / max(count, 1);
+  return per < 2 ? 1 : min(32, 1 << (31 - __clz(per)));
+}
+
 template <int T, bool ALIGNED>
-#ifndef BEAM_MINB
-#define BEAM_MINB 4
-#endif
-__global__ void __launch_bounds__(SCAN_THREADS, BEAM_MINB) k_beam_scan(const BeamParams p) {
+__global__ void __launch_bounds__(SCAN_THREADS, SCAN_CTAS) k_beam_scan(const BeamParams p) {
   constexpr int N = Vec<T>::N;
   constexpr int WARPS = SCAN_THREADS / 32;
+  constexpr int BATCH = AHEAD * SCAN_THREADS;  // vectors of AHEAD rounds; a round is a vector a thread
   const float INF = __uint_as_float(0x7f800000u);
-  __shared__ float top_of[SEGMENTS * SCAN_THREADS];  // threads' largest logits of a part's quarters
+  __shared__ float top_of[SEGMENTS * SCAN_THREADS];  // threads' largest logits in a part's segments
   __shared__ float group_top[SCAN_THREADS];
   __shared__ float warp_top[WARPS], warp_q[WARPS];
-  __shared__ unsigned long long total;
+  __shared__ unsigned long long warp_sum[WARPS];
   __shared__ float bound_s;
   __shared__ uint16_t chosen[SEGMENTS * SCAN_THREADS];  // those that hold candidates
   __shared__ unsigned long long keys[KEEP], sorted[DFLASH_BEAM_MAX_N];
-  __shared__ int ranks[KEEP];
   __shared__ int count_s, chosen_s;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int row = blockIdx.x / p.splits, split = blockIdx.x - row * p.splits;
+  const int row = blockIdx.x / p.splits, part = blockIdx.x - row * p.splits;
+  const Row<T, ALIGNED> in = {p.logits + row * p.row_bytes, p.vocab};
+  const int vecs = (p.vocab + N - 1) / N, inner = in.inner();
+  const int v0 = part * p.part, v1 = min(vecs, v0 + p.part), end = min(v1, inner);
+  const int batches = (v1 - v0 + BATCH - 1) / BATCH, seg_len = (batches + SEGMENTS - 1) / SEGMENTS;
+  const uint4 none = make_uint4(Vec<T>::NONE, Vec<T>::NONE, Vec<T>::NONE, Vec<T>::NONE);
   pdl_launch_dependents();
   pdl_wait();
-  const float score = p.scores[row];
-  if (!(score > -INF) || score == INF || (p.done && p.done[row])) return;  // no logits are asked for
-  const Row<T, ALIGNED> in = {p.logits + row * p.row_bytes, p.vocab};
-  const int vecs = (p.vocab + N - 1) / N;
-  const int v0 = split * p.part, v1 = min(vecs, v0 + p.part);
 
   // ---- the sum and the largest logit
+  // The loads of a batch are on their way while the one before is summed.  What
+  // does not lie wholly inside the row is left to end_vector.
+  uint4 next[AHEAD];
+  int k = v0 + tid;  // of the next batch
+  auto fetch = [&]() {
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j, k += SCAN_THREADS) next[j] = k > 0 && k < end ? in.load(k) : none;
+  };
+  fetch();
+  const float score = p.scores[row];
+  const bool done = p.done && p.done[row];
+  if (!(score > -INF) || score == INF || done) return;  // no logits are asked for
   float top = -INF, q = -1e30f;
   Pair sum2 = pair(0.0f, 0.0f);
   const Pair hi2 = pair(LOG2E_HI, LOG2E_HI), lo2 = pair(LOG2E_LO, LOG2E_LO);
-  auto take = [&](auto& v) {  // some vectors
-    const float m = Vec<T>::top(v);
+  auto see = [&](float m) {  // a maximum, before its terms
     top = fmaxf(top, m);
     const float t = m * LOG2E_HI;
     if (t > q + 2.0f) {  // terms stay below 2^2.5
@@ -278,173 +281,179 @@ __global__ void __launch_bounds__(SCAN_THREADS, BEAM_MINB) k_beam_scan(const Bea
       sum2 = fma2(sum2, pair(f, f), pair(0.0f, 0.0f));
       q = to;
     }
-    const Pair ref = pair(-q, -q);
-#pragma unroll
-    for (int j = 0; j < (int)(sizeof(v) / sizeof(uint4)); ++j) {
-      float x[N];
-      Vec<T>::floats(v[j], x);
-#pragma unroll
-      for (int e = 0; e < N; e += 2) {
-        const Pair x2 = pair(x[e], x[e + 1]);
-        float a, b;
-        unpair(fma2(x2, lo2, fma2(x2, hi2, ref)), a, b);
-        sum2 = add2(sum2, pair(ex2(a), ex2(b)));
-      }
-    }
   };
-  // Batches of AHEAD rounds; a round is a vector a thread.  What does not lie wholly
-  // inside the row goes vector by vector: which batches do goes by their index alone.
-  constexpr int BATCH = AHEAD * SCAN_THREADS;
-  const int batches = (v1 - v0 + BATCH - 1) / BATCH, seg_len = (batches + SEGMENTS - 1) / SEGMENTS;
-  int seg = 0, left = seg_len;  // batches to the segment's end
-  auto batch_done = [&]() {
-    if (--left) return;
-    top_of[seg++ * SCAN_THREADS + tid] = top;
-    top = -INF;
-    left = seg_len;
+  auto add = [&](float x0, float x1) {
+    const Pair x2 = pair(x0, x1), ref = pair(-q, -q);
+    float a, b;
+    unpair(fma2(x2, lo2, fma2(x2, hi2, ref)), a, b);
+    sum2 = add2(sum2, pair(ex2(a), ex2(b)));
   };
-  auto ends = [&](int b) {
-    for (int j = 0; j < AHEAD; ++j) {
-      const int k = v0 + (b * AHEAD + j) * SCAN_THREADS + tid;
-      if (k >= v1) break;
-      const uint4 v[1] = {in.load(k)};
-      take(v);
-    }
-    batch_done();
-  };
-  const int b1 = max(0, (min(v1, in.inner()) - v0) / BATCH);  // batches inside end here
-  int b = 0;
-  if (v0 == 0) ends(b++);
-  if (b < b1) {
-    uint4 v[AHEAD];
-    auto fetch = [&]() {
-#pragma unroll
-      for (int j = 0; j < AHEAD; ++j) v[j] = in.load_inner(v0 + (b * AHEAD + j) * SCAN_THREADS + tid);
-    };
-    fetch();
-    for (;;) {
+  for (int b = 0, seg = 0; seg < SEGMENTS; ++seg) {
+    for (const int last = min(batches, b + seg_len); b < last; ++b) {
       uint4 now[AHEAD];
 #pragma unroll
-      for (int j = 0; j < AHEAD; ++j) now[j] = v[j];
-      const bool more = ++b < b1;
-      if (more) fetch();
-      take(now);
-      batch_done();
-      if (!more) break;
-    }
-  }
-  while (b < batches) ends(b++);
-  for (; seg < SEGMENTS; ++seg, top = -INF) top_of[seg * SCAN_THREADS + tid] = top;
-  auto whole_top = [&]() {
-    float m = top_of[tid];
+      for (int j = 0; j < AHEAD; ++j) now[j] = next[j];
+      if (b + 1 < batches) fetch();
+      see(Vec<T>::top(now));
 #pragma unroll
-    for (int i = 1; i < SEGMENTS; ++i) m = fmaxf(m, top_of[i * SCAN_THREADS + tid]);
-    return m;
-  };
-  top = whole_top();  // its own values
-  float s0, s1;
-  unpair(sum2, s0, s1);
-  float s = s0 + s1;
-  auto block_tops = [&](float a, float b) {
-    for (int d = 16; d; d >>= 1) {
-      a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
-      b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, d));
+      for (int j = 0; j < AHEAD; ++j) {
+        float x[N];
+        Vec<T>::floats(now[j], x);
+#pragma unroll
+        for (int e = 0; e < N; e += 2) add(x[e], x[e + 1]);
+      }
     }
-    if (lane == 0) warp_top[warp] = a, warp_q[warp] = b;
+    top_of[seg * SCAN_THREADS + tid] = top;
+    top = -INF;
+  }
+  // the row's ends, after the rest whatever its alignment
+#pragma unroll 1
+  for (int i = v0 == 0 ? 0 : max(inner, v0); i < v1; i = max(inner, i + 1)) {  // three vectors at most
+    if ((i - v0) % SCAN_THREADS != tid) continue;
+    float x[N], m0 = -INF;
+#pragma unroll
+    for (int e = 0; e < N; ++e) x[e] = i * N + e < p.vocab ? in.at(i * N + e) : -INF;
+#pragma unroll
+    for (int e = 0; e < N; ++e) m0 = fmaxf(m0, x[e]);
+    top = -INF;
+    see(m0);
+#pragma unroll
+    for (int e = 0; e < N; e += 2) add(x[e], x[e + 1]);
+    float& m = top_of[(i - v0) / (seg_len * BATCH) * SCAN_THREADS + tid];
+    m = fmaxf(m, top);
+  }
+
+  // ---- joined over the block: the sum, and the group maxima
+  const int G = groups_for(p.n), per = SCAN_THREADS / G;  // threads of a group: 4, 2, 1
+  const int g = tid / per;
+  auto tops = [&]() {  // a thread's, then its group's and warp's
+    top = top_of[tid];
+#pragma unroll
+    for (int i = 1; i < SEGMENTS; ++i) top = fmaxf(top, top_of[i * SCAN_THREADS + tid]);
+    float m = top;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      if (d == per && tid % per == 0) group_top[g] = m;
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    }
+    if (lane == 0) warp_top[warp] = m;
   };
-  block_tops(top, s > 0.0f ? q : -1e30f);
-  if (tid == 0) total = 0, count_s = chosen_s = 0;
-  const bool odd = __syncthreads_or(!(s < 1e37f));
+  tops();
+  float s;
+  {
+    float s1;
+    unpair(sum2, s, s1);
+    s += s1;
+  }
+  float most = s > 0.0f ? q : -1e30f;
+#pragma unroll
+  for (int d = 16; d; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+  auto fixed_sum = [&](float v) {
+    unsigned long long f = __float2ull_rn(v * (float)(1ull << FIX));
+#pragma unroll
+    for (int d = 16; d; d >>= 1) f += __shfl_xor_sync(0xffffffffu, f, d);
+    if (lane == 0) warp_sum[warp] = f;
+  };
+  const bool odd = !(s < 1e37f);
+  fixed_sum(odd ? 0.0f : s * pow2_or_0(q - most));
+  if (lane == 0) warp_q[warp] = most;
+  if (tid == 0) count_s = chosen_s = 0;
+  const bool any_odd = __syncthreads_or(odd);
   float part_top = warp_top[0], part_q = warp_q[0];
 #pragma unroll
   for (int w = 1; w < WARPS; ++w) part_top = fmaxf(part_top, warp_top[w]), part_q = fmaxf(part_q, warp_q[w]);
-  // NaN, infinity, or logits whose exponent does not fit: once more, against the largest finite one
-  const bool plain = !odd && (part_top == -INF || part_q > -1e30f);
+  const bool plain = !any_odd && (part_top == -INF || part_q > -1e30f);
   if (!plain) {
+    // NaN, infinity, or logits whose exponent does not fit: once more, against the largest finite one
     auto clean = [&](float x) { return x <= FLT_MAX ? x : -INF; };
-    bool bad = false;
-    for (int i = 0; i < SEGMENTS; ++i) {
-      float m = -INF;
-      for (int r = i * seg_len * AHEAD; r < (i + 1) * seg_len * AHEAD; ++r) {
-        const int k = v0 + r * SCAN_THREADS + tid;
-        if (k >= v1) break;
-        float x[N];
-        Vec<T>::floats(in.load(k), x);
+    auto each = [&](int from, int to, auto&& f) {  // this thread's logits of some rounds
+#pragma unroll 1
+      for (int r = from; r < to; ++r) {
+        const int i = v0 + r * SCAN_THREADS + tid;
+        if (i >= v1) break;
+        if (i > 0 && i < inner) {
+          float x[N];
+          Vec<T>::floats(in.load(i), x);
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-          bad |= !(x[e] <= FLT_MAX);
-          m = fmaxf(m, clean(x[e]));
+          for (int e = 0; e < N; ++e) f(x[e]);
+        } else {
+#pragma unroll 1
+          for (int token = i * N; token < min(p.vocab, (i + 1) * N); ++token) f(in.at(token));
         }
       }
+    };
+    bool bad = false;
+#pragma unroll 1
+    for (int i = 0; i < SEGMENTS; ++i) {
+      float m = -INF;
+      each(i * seg_len * AHEAD, (i + 1) * seg_len * AHEAD, [&](float x) {
+        bad |= !(x <= FLT_MAX);
+        m = fmaxf(m, clean(x));
+      });
       top_of[i * SCAN_THREADS + tid] = m;
     }
-    top = whole_top();
     if (bad) flag_nan(p.status);
     __syncthreads();
-    block_tops(top, 0.0f);
+    tops();
     __syncthreads();
     part_top = warp_top[0];
 #pragma unroll
     for (int w = 1; w < WARPS; ++w) part_top = fmaxf(part_top, warp_top[w]);
     s = 0.0f;
-    if (part_top > -INF) {
-      for (int i = v0 + tid; i < v1; i += SCAN_THREADS) {
-        float x[N];
-        Vec<T>::floats(in.load(i), x);
-#pragma unroll
-        for (int e = 0; e < N; ++e) s += expf(clean(x[e]) - part_top);
-      }
-    }
+    if (part_top > -INF) each(0, batches * AHEAD, [&](float x) { s += expf(clean(x) - part_top); });
+    if (lane == 0) warp_q[warp] = 0.0f;
+    part_q = 0.0f;
+    fixed_sum(s);
+    __syncthreads();
   }
-  const float scale = plain ? pow2_or_0(q - part_q) : 1.0f;
-  unsigned long long fixed = __float2ull_rn(s * scale * (float)(1ull << FIX));
-  for (int d = 16; d; d >>= 1) fixed += __shfl_xor_sync(0xffffffffu, fixed, d);
-  if (lane == 0 && fixed) atomicAdd(&total, fixed);
 
-  // ---- a bound below n of the part's logits
-  const int G = groups_for(p.n), per = SCAN_THREADS / G;  // threads of a group: 4, 2, 1
-  float g_top = top;
-  if (per >= 2) g_top = fmaxf(g_top, __shfl_xor_sync(0xffffffffu, g_top, 1));
-  if (per >= 4) g_top = fmaxf(g_top, __shfl_xor_sync(0xffffffffu, g_top, 2));
-  const int g = tid / per;
-  if (tid % per == 0) group_top[g] = g_top;
-  __syncthreads();
-  int above = 0;
-  for (int u = tid % per; u < G; u += per) above += group_top[u] > g_top || (group_top[u] == g_top && u < g);
-  if (per >= 2) above += __shfl_xor_sync(0xffffffffu, above, 1);
-  if (per >= 4) above += __shfl_xor_sync(0xffffffffu, above, 2);
-  if (above == p.n - 1) bound_s = g_top;  // of one group
+  // ---- a bound below n of the part's logits: the n-th largest group maximum
+  {
+    const float mine = group_top[g];
+    int above = 0;
+#pragma unroll 8
+    for (int u = tid % per; u < G; u += per) {
+      const float o = group_top[u];
+      above += (o > mine) | ((o == mine) & (u < g));
+    }
+    if (per >= 2) above += __shfl_xor_sync(0xffffffffu, above, 1);
+    if (per >= 4) above += __shfl_xor_sync(0xffffffffu, above, 2);
+    if (above == p.n - 1) bound_s = mine;  // of one group
+  }
+  if (tid == 0) {
+    unsigned long long sum = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w)
+      if (part_q - warp_q[w] < 63.0f) sum += warp_sum[w] >> (int)(part_q - warp_q[w]);
+    const PartSum r = {sum, part_q, part_top, plain, 0};
+    p.sums[row * p.splits + part] = r;
+  }
   __syncthreads();
   const float bound = fmaxf(bound_s, -FLT_MAX);  // -inf: no token
-  if (tid == 0) {
-    PartSum r = {total, part_q, part_top, plain, 0};
-    p.sums[row * p.splits + split] = r;
-  }
 
-  // ---- the threads' quarters that can hold one of the n, and their logits again
+  // ---- the threads' segments that can hold one of the n, and their logits again
   if (top >= bound)
     for (int i = 0; i < SEGMENTS; ++i)
       if (top_of[i * SCAN_THREADS + tid] >= bound) chosen[atomicAdd(&chosen_s, 1)] = (uint16_t)(i * SCAN_THREADS + tid);
   __syncthreads();
   const int n_chosen = chosen_s;
   unsigned long long least = (unsigned long long)ordered(bound) << 32;  // keys at or below are not wanted
-  auto prune = [&]() {  // the n largest keys, sorted
-    __syncthreads();
-    const int count = count_s;
-    const int width = min(SCAN_THREADS, max(32, (count + 31) & ~31)), parts = SCAN_THREADS / width;  // threads of a key
-    for (int i = tid; i < count; i += SCAN_THREADS) ranks[i] = 0;
-    __syncthreads();
-    const int part = tid / width;
-    for (int i = tid - part * width; i < count && part < parts; i += width) {
-      const unsigned long long k = keys[i];
+  auto ranked = [&](int count, auto&& f) {  // every key with its rank
+    const int lanes = rank_lanes(SCAN_THREADS, count), at = tid & (lanes - 1);
+#pragma unroll 1
+    for (int i0 = 0; i0 < count; i0 += SCAN_THREADS / lanes) {
+      const int i = i0 + tid / lanes;
+      const unsigned long long key = keys[min(i, count - 1)];
       int rank = 0;
 #pragma unroll 4
-      for (int j = part; j < count; j += parts) rank += keys[j] > k;
-      if (rank) atomicAdd(&ranks[i], rank);
+      for (int j = at; j < count; j += lanes) rank += keys[j] > key;
+      for (int d = lanes >> 1; d; d >>= 1) rank += __shfl_xor_sync(0xffffffffu, rank, d);
+      if (at == 0 && i < count && rank < p.n) f(key, rank);
     }
-    __syncthreads();
-    for (int i = tid; i < count; i += SCAN_THREADS)
-      if (ranks[i] < p.n) sorted[ranks[i]] = keys[i];
+  };
+  auto prune = [&]() {  // to the n largest keys
+    const int count = count_s;
+    ranked(count, [&](unsigned long long key, int rank) { sorted[rank] = key; });
     __syncthreads();
     const int kept = min(count, p.n);
     for (int i = tid; i < kept; i += SCAN_THREADS) keys[i] = sorted[i];
@@ -452,271 +461,286 @@ __global__ void __launch_bounds__(SCAN_THREADS, BEAM_MINB) k_beam_scan(const Bea
     if (tid == 0) count_s = kept;
     __syncthreads();
   };
-  const int rounds = seg_len * AHEAD;  // of a quarter
-  const int items = rounds * n_chosen;
-  for (int i0 = 0; i0 < items; i0 += SCAN_THREADS) {
-    const int it = i0 + tid;
-    unsigned long long key[N];
-    bool any = false;
+  const int rounds = seg_len * AHEAD, items = rounds * n_chosen;  // rounds of a segment
+#pragma unroll 1
+  for (int i0 = 0; i0 < items; i0 += AGAIN * SCAN_THREADS) {
+    int token[AGAIN];
+    unsigned wanted = 0;  // of their tokens
+    uint4 v[AGAIN];
+    bool whole[AGAIN];
 #pragma unroll
-    for (int e = 0; e < N; ++e) key[e] = 0;
-    if (it < items) {
-      const int r = it / n_chosen, c = chosen[it - r * n_chosen];
+    for (int j = 0; j < AGAIN; ++j) {
+      const int it = i0 + j * SCAN_THREADS + tid, r = it / n_chosen;
+      token[j] = 0;
+      whole[j] = false;
+      if (it >= items) continue;
+      const int c = chosen[it - r * n_chosen];
       const int i = v0 + (c / SCAN_THREADS * rounds + r) * SCAN_THREADS + c % SCAN_THREADS;
-      if (i < v1) {
-        float x[N];
-        Vec<T>::floats(in.load(i), x);
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-          if (!(x[e] >= bound && x[e] <= FLT_MAX)) continue;
-          key[e] = (unsigned long long)ordered(x[e]) << 32 | (0xffffffffu - (uint32_t)(i * N + e));
-          any |= key[e] > least;
-        }
-      }
+      token[j] = i * N;
+      whole[j] = i > 0 && i < end;
+      if (whole[j]) v[j] = in.load(i);
+      else if (i < v1) wanted |= ((1u << min(N, p.vocab - token[j])) - 1) << j * N;
     }
-    const int pushers = __syncthreads_count(any);
-    if (pushers == 0) continue;
-    if (count_s + pushers * N <= KEEP) {
-      __syncthreads();  // count_s is read by all
 #pragma unroll
-      for (int e = 0; e < N; ++e)
-        if (key[e] > least) keys[atomicAdd(&count_s, 1)] = key[e];
-    } else {  // many at once: one a thread at a time, as many as fit
+    for (int j = 0; j < AGAIN; ++j) {
+      if (!whole[j]) continue;
+      float x[N];
+      Vec<T>::floats(v[j], x);
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        __syncthreads();
+      for (int e = 0; e < N; ++e) wanted |= (x[e] >= bound) << (j * N + e);
+    }
+    auto visit = [&](unsigned w, auto&& push) {
+#pragma unroll 1
+      for (; w; w &= w - 1) {
+        const int bit = __ffs(w) - 1, t = (AGAIN > 1 && bit >= N ? token[AGAIN - 1] : token[0]) + bit % N;
+        const float x = in.at(t);
+        const unsigned long long key = (unsigned long long)ordered(x) << 32 | (0xffffffffu - (uint32_t)t);
+        if (x >= bound && x <= FLT_MAX && key > least) push(key);
+      }
+    };
+    const int before = count_s;
+    __syncthreads();
+    bool full = false;
+    visit(wanted, [&](unsigned long long key) {
+      const int o = atomicAdd(&count_s, 1);
+      if (o < KEEP) keys[o] = key;
+      else full = true;
+    });
+    if (__syncthreads_or(full)) {  // too many at once: again from `before`, in turns of one a thread
+      if (tid == 0) count_s = before;
+      __syncthreads();
+#pragma unroll 1
+      for (int e = 0; e < AGAIN * N; ++e) {
         if (count_s + SCAN_THREADS > KEEP) prune();  // leaves at most DFLASH_BEAM_MAX_N
         __syncthreads();
-        if (key[e] > least) keys[atomicAdd(&count_s, 1)] = key[e];
+        visit(wanted & 1u << e, [&](unsigned long long key) { keys[atomicAdd(&count_s, 1)] = key; });
+        __syncthreads();
       }
     }
-    __syncthreads();
   }
-  prune();
-  unsigned long long* best = p.best + (long long)(row * p.splits + split) * p.n;
-  const int kept = count_s;
-  for (int i = tid; i < p.n; i += SCAN_THREADS) best[i] = i < kept ? keys[i] : 0;
+  // the n best, sorted
+  unsigned long long* best = p.best + (long long)(row * p.splits + part) * p.n;
+  const int count = count_s;
+  ranked(count, [&](unsigned long long key, int rank) { best[rank] = key; });
+  for (int i = count + tid; i < p.n; i += SCAN_THREADS) best[i] = 0;
 }
 
 // ------------------------------------------------------------------ the join
 
-// The natural logarithm to about 2^-42, by the series of 2 atanh((m - 1) / (m + 1)) for m in [0.7, 1.42): a third of
-// the 64-bit operations of log(), which run at a 64th of the 32-bit rate.
-DFL_DEV double ln(unsigned long long v) {
+// The natural logarithm to 2^-27, as a sum of two floats and `e` ln 2: the series of 2 atanh(z), z = (m - 1) /
+// (m + 1), m in [0.7, 1.42), with the quotient to 46 bits by error-free sums and products (Dekker, Knuth).  64-bit
+// operations run at a 64th of the 32-bit rate: log() took 1.1 us of a 5 us join.
+struct Log {
+  float hi, lo;
+  int e;
+};
+DFL_DEV Log ln(unsigned long long v) {  // v > 0
   int e = 63 - __clzll((long long)v);
-  double m = (double)v;  // v < 2^63: in [2^e, 2^(e + 1)], its exponent replaced below
-  m = __longlong_as_double(__double_as_longlong(m) - ((long long)e << 52));
-  if (m > 1.414) m *= 0.5, ++e;
-  const double d = m + 1.0;
-  double r = (double)(1.0f / (float)d);
-  r = r * (2.0 - d * r);
-  r = r * (2.0 - d * r);
-  const double z = (m - 1.0) * r, w = z * z;
-  double s = 1.0 / 15;
-  s = s * w + 1.0 / 13;
-  s = s * w + 1.0 / 11;
-  s = s * w + 1.0 / 9;
-  s = s * w + 1.0 / 7;
-  s = s * w + 1.0 / 5;
-  s = s * w + 1.0 / 3;
-  s = s * w + 1.0;
-  return 2.0 * z * s + e * LN2;
+  const unsigned long long top = v << (63 - e);                 // its 64 leading bits
+  float mh = (float)(uint32_t)(top >> 40), ml = (float)(uint32_t)(top >> 16 & 0xffffffu);  // 24 and 24 more
+  mh *= 0x1p-23f, ml *= 0x1p-47f;                               // [1, 2)
+  if (mh > 1.414f) mh *= 0.5f, ml *= 0.5f, ++e;
+  const float n = mh - 1.0f, d = mh + 1.0f, dl = (mh - (d - 1.0f)) + ml;  // n exact; d + dl = m + 1
+  const float r = 1.0f / d, q = n * r;
+  const float ql = ((fmaf(-q, d, n) + ml) - q * dl) * r;
+  const float w = q * q;
+  float s = 1.0f / 13;
+  s = fmaf(s, w, 1.0f / 11);
+  s = fmaf(s, w, 1.0f / 9);
+  s = fmaf(s, w, 1.0f / 7);
+  s = fmaf(s, w, 1.0f / 5);
+  s = fmaf(s, w, 1.0f / 3);
+  return {2.0f * q, 2.0f * (ql + q * (s * w)), e};
 }
 
-struct Cand {
-  unsigned long long score;  // ordered; 0: none
-  unsigned long long key;    // of the logit and token in its row
-  int beam;
+// A candidate: its score's order, and what goes before among equal scores: the
+// lower beam, of one beam the larger logit (64 bits lose what is below 2^-53 of a
+// score), then the lower token.  No two are equal.
+struct __align__(16) Cand {
+  unsigned long long score;  // 0: none
+  unsigned long long tie;    // 63 - beam, the logit's order, 2^24 - 1 - token
 };
-// The larger score; of equal ones the lower beam, of one beam the larger logit
-// (64 bits lose what is below 2^-53 of a score), then the lower token.
-DFL_DEV bool better(const Cand& a, const Cand& b) {
-  return a.score > b.score || (a.score == b.score && (a.beam < b.beam || (a.beam == b.beam && a.key > b.key)));
+DFL_DEV bool better(const Cand& a, const Cand& b) {  // without branches
+  return (a.score > b.score) | ((a.score == b.score) & (a.tie > b.tie));
+}
+DFL_DEV Cand cand(double score, int beam, uint32_t logit, uint32_t token) {
+  return {ordered(score), (unsigned long long)(DFLASH_BEAM_MAX - 1 - beam) << 56 | (unsigned long long)logit << 24 | (0xffffffu - token)};
+}
+DFL_DEV int beam_of(const Cand& c) { return DFLASH_BEAM_MAX - 1 - (int)(c.tie >> 56); }
+DFL_DEV int token_of(const Cand& c) { return 0xffffff - (int)(c.tie & 0xffffffu); }
+
+DFL_DEV float warp_max(float v) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+  return v;
+}
+
+// A part's sum against the row's largest reference r, where the references are not
+// all powers of two.
+__device__ __noinline__ unsigned long long sum_of_any(const PartSum& part, bool some, double& r) {
+  const double mine = !some ? -DBL_MAX : part.base2 ? part.q * LN2 : (double)part.top;
+  r = mine;
+  for (int d = 16; d; d >>= 1) r = fmax(r, __shfl_xor_sync(0xffffffffu, r, d));
+  return some ? (unsigned long long)((double)part.sum * exp(mine - r)) : 0;
 }
 
 __global__ void __launch_bounds__(JOIN_THREADS) k_beam_join(const BeamParams p) {
-  constexpr int WARPS = JOIN_THREADS / 32;
+  constexpr int WARPS = JOIN_THREADS / 32, PER = MAX_LISTS / JOIN_THREADS;  // lists of a thread
   const float INF = __uint_as_float(0x7f800000u);
   enum { DEAD, RUNS, ENDED };
   __shared__ double base[DFLASH_BEAM_MAX], ref[DFLASH_BEAM_MAX];  // score = base + (logit - ref)
-  __shared__ unsigned long long sum_of[DFLASH_BEAM_MAX];
   __shared__ float floor_of[DFLASH_BEAM_MAX];                    // logits below it do not reach the bound
   __shared__ uint8_t state[DFLASH_BEAM_MAX];
   __shared__ unsigned long long head_score[MAX_LISTS];
   __shared__ Cand group_head[JOIN_THREADS];
-  __shared__ int above[JOIN_THREADS];
   __shared__ Cand bound_s;
   __shared__ uint16_t chosen[MAX_LISTS];
-  __shared__ unsigned long long score_of[KEEP], key_of[KEEP];
-  __shared__ uint8_t beam_of[KEEP];
-  __shared__ int ranks[KEEP];
-  __shared__ Cand sorted[DFLASH_BEAM_MAX_N];
+  __shared__ Cand kept[KEEP], sorted[DFLASH_BEAM_MAX_N];
   __shared__ int count_s, chosen_s;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, b = blockIdx.x;
   const int S = p.splits, lists = p.beams * S;
-  pdl_launch_dependents();
-  pdl_wait();
-  if (tid == 0) {
-    count_s = chosen_s = 0;
-    bound_s = {0, 0, DFLASH_BEAM_MAX};
-  }
-  above[tid] = 0;
   const unsigned long long* best = p.best + (long long)b * lists * p.n;
-  // The depth at which the lists are compared: with fewer than four lists a
-  // candidate asked for, deeper, so that few of the lists are above the bound.
+  // Few candidates are all ranked.  Of more, the lists are compared at a depth:
+  // with fewer than four lists a candidate asked for, deeper, so that few of the
+  // lists are above the bound.
+  const bool few = lists * p.n <= JOIN_THREADS;
   int depth = 1;
+#pragma unroll 1
   while (depth < p.n && lists < 4 * ((p.n + depth - 1) / depth)) depth *= 2;
   depth = min(depth, p.n);
-  const int nth = (p.n + depth - 1) / depth;
-  const bool few = lists * p.n <= JOIN_THREADS / 2;  // candidates: all of them are ranked
-  const unsigned long long mine_key = few && tid < lists * p.n ? best[tid] : 0;
-  // the lists' best keys and those at the depth, on their way while the sums are joined
-  unsigned long long head[MAX_LISTS / JOIN_THREADS], deep[MAX_LISTS / JOIN_THREADS];
-#pragma unroll
-  for (int i = 0; i < MAX_LISTS / JOIN_THREADS; ++i) {
-    const int l = tid + i * JOIN_THREADS;
-    head[i] = l < lists && !few ? best[(long long)l * p.n] : 0;  // of a beam that does not run: not looked at
-    deep[i] = l < lists && !few ? best[(long long)l * p.n + depth - 1] : 0;
+  const int nth = (p.n + depth - 1) / depth, G = groups_for(nth);
+  if (tid == 0) {
+    count_s = chosen_s = 0;
+    bound_s = {0, 0};
   }
-  // ---- each beam's sum
+  pdl_launch_dependents();
+  pdl_wait();
+  // the first candidates are on their way while the sums are joined; those of a beam that does not run are not looked at
+  unsigned long long head[PER], deep[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int l = tid + i * JOIN_THREADS;
+    head[i] = deep[i] = 0;
+    if (l >= (few ? lists * p.n : lists)) continue;
+    head[i] = few ? best[l] : best[(long long)l * p.n];
+    if (!few && depth > 1) deep[i] = best[(long long)l * p.n + depth - 1];
+  }
+
+  // ---- each beam's sum, a lane a part
+#pragma unroll 1
   for (int k = warp; k < p.beams; k += WARPS) {
     const int row = b * p.beams + k;
+    PartSum part = {};
+    part.top = -INF;
+    if (lane < S) part = p.sums[row * S + lane];
     const float score = p.scores[row];
-    PartSum a[MAX_SPLITS / 32];
-#pragma unroll
-    for (int i = 0; i < MAX_SPLITS / 32; ++i) {
-      const int s = lane + 32 * i;
-      a[i].top = -INF;
-      if (s < S) a[i] = p.sums[row * S + s];
-    }
+    const bool done = p.done && p.done[row];
     int st = DEAD;
     if (!(score <= FLT_MAX)) {
       if (lane == 0) flag_nan(p.status);
     } else if (score > -INF) {
-      st = p.done && p.done[row] ? ENDED : RUNS;
+      st = done ? ENDED : RUNS;
     }
-    double r = 0.0;
-    unsigned long long sum = 0;
+    double c = score, r = 0.0;
     if (st == RUNS) {
-      float top = -INF, q = -INF;
-      bool all2 = true;
-#pragma unroll
-      for (int i = 0; i < MAX_SPLITS / 32; ++i) {
-        if (a[i].top == -INF) continue;
-        top = fmaxf(top, a[i].top);
-        if (a[i].base2) q = fmaxf(q, a[i].q);
-        else all2 = false;
-      }
-      for (int d = 16; d; d >>= 1) {
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, d));
-      }
-      all2 = __all_sync(0xffffffffu, all2);
-      if (top == -INF) {
+      const bool some = part.top > -INF;
+      const float q = warp_max(some && part.base2 ? part.q : -INF);
+      if (!__any_sync(0xffffffffu, some)) {
         st = DEAD;
-      } else if (all2) {  // shifts to the largest reference
-        r = q * LN2;
-#pragma unroll
-        for (int i = 0; i < MAX_SPLITS / 32; ++i)
-          if (a[i].top > -INF && q - a[i].q < 63.0f) sum += a[i].sum >> (int)(q - a[i].q);
       } else {
-        r = -DBL_MAX;
+        unsigned long long sum;
+        if (__all_sync(0xffffffffu, !some || part.base2)) {  // shifts to the largest reference
+          r = q * LN2;
+          sum = some && q - part.q < 63.0f ? part.sum >> (int)(q - part.q) : 0;
+        } else {
+          sum = sum_of_any(part, some, r);
+        }
 #pragma unroll
-        for (int i = 0; i < MAX_SPLITS / 32; ++i)
-          if (a[i].top > -INF) r = fmax(r, a[i].base2 ? a[i].q * LN2 : (double)a[i].top);
-        for (int d = 16; d; d >>= 1) r = fmax(r, __shfl_xor_sync(0xffffffffu, r, d));
-#pragma unroll
-        for (int i = 0; i < MAX_SPLITS / 32; ++i)
-          if (a[i].top > -INF)
-            sum += (unsigned long long)((double)a[i].sum * exp((a[i].base2 ? a[i].q * LN2 : (double)a[i].top) - r));
+        for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        const Log l = ln(sum);
+        c = (double)score - (l.e - FIX) * LN2 - (double)l.hi - (double)l.lo;
       }
-      for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
     }
-    if (lane == 0) base[k] = score, ref[k] = r, sum_of[k] = sum, state[k] = (uint8_t)st, floor_of[k] = -INF;
+    if (lane == 0) base[k] = c, ref[k] = r, state[k] = (uint8_t)st, floor_of[k] = -INF;
   }
-  __syncthreads();
-  if (tid < p.beams && state[tid] == RUNS) base[tid] -= ln(sum_of[tid]) - FIX * LN2;
   __syncthreads();
 
-  auto put = [&](const Cand& c) {
-    const int i = atomicAdd(&count_s, 1);
-    score_of[i] = c.score, key_of[i] = c.key, beam_of[i] = (uint8_t)c.beam;
+  auto put = [&](const Cand& c) { kept[atomicAdd(&count_s, 1)] = c; };
+  auto value = [&](int k, unsigned long long key) {  // of a list's key
+    const uint32_t logit = (uint32_t)(key >> 32);
+    return cand(base[k] + ((double)unordered(logit) - ref[k]), k, logit, 0xffffffffu - (uint32_t)key);
   };
-  auto value = [&](int k, unsigned long long key) {
-    const Cand c = {ordered(base[k] + ((double)unordered((uint32_t)(key >> 32)) - ref[k])), key, k};
-    return c;
-  };
-  if (tid < p.beams && state[tid] == ENDED) {  // one candidate, itself
-    const Cand c = {ordered(base[tid]), 0xffffffffu - (uint32_t)p.done_token, tid};
-    put(c);
-  }
-  Cand least = {0, 0, DFLASH_BEAM_MAX};  // what is not below it is wanted
-  auto prune = [&]() {  // the n best, sorted
-    __syncthreads();
-    const int count = count_s;
-    const int width = min(JOIN_THREADS, max(32, (count + 31) & ~31)), parts = JOIN_THREADS / width;  // threads of a candidate
-    for (int i = tid; i < count; i += JOIN_THREADS) ranks[i] = 0;
-    __syncthreads();
-    const int part = tid / width;
-    for (int i = tid - part * width; i < count && part < parts; i += width) {
-      const unsigned long long score = score_of[i], key = key_of[i];
-      const int beam = beam_of[i];
+  if (tid < p.beams && state[tid] == ENDED) put(cand(base[tid], tid, 0, (uint32_t)p.done_token));  // one candidate, itself
+  auto ranked = [&](int count, auto&& f) {  // every candidate with its rank
+    const int lanes = rank_lanes(JOIN_THREADS, count), at = tid & (lanes - 1);
+#pragma unroll 1
+    for (int i0 = 0; i0 < count; i0 += JOIN_THREADS / lanes) {
+      const int i = i0 + tid / lanes;
+      const Cand c = kept[min(i, count - 1)];
       int rank = 0;
 #pragma unroll 4
-      for (int j = part; j < count; j += parts) {
-        const unsigned long long o = score_of[j];
-        rank += o > score;
-        if (o == score && j != i) rank += beam_of[j] < beam || (beam_of[j] == beam && key_of[j] > key);
+      for (int j = at; j < count; j += lanes) {
+        const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(&kept[j]);
+        rank += better({o.x, o.y}, c);
       }
-      if (rank) atomicAdd(&ranks[i], rank);
+      for (int d = lanes >> 1; d; d >>= 1) rank += __shfl_xor_sync(0xffffffffu, rank, d);
+      if (at == 0 && i < count && rank < p.n) f(c, rank);
     }
+  };
+  Cand least = {0, 0};  // what is not below it is wanted
+  auto prune = [&]() {  // to the n best
+    const int count = count_s;
+    ranked(count, [&](const Cand& c, int rank) { sorted[rank] = c; });
     __syncthreads();
-    for (int i = tid; i < count; i += JOIN_THREADS)
-      if (ranks[i] < p.n) sorted[ranks[i]] = {score_of[i], key_of[i], beam_of[i]};
-    __syncthreads();
-    const int kept = min(count, p.n);
-    for (int i = tid; i < kept; i += JOIN_THREADS)
-      score_of[i] = sorted[i].score, key_of[i] = sorted[i].key, beam_of[i] = (uint8_t)sorted[i].beam;
-    if (kept == p.n && better(sorted[p.n - 1], least)) least = sorted[p.n - 1];
-    if (tid == 0) count_s = kept;
+    const int left = min(count, p.n);
+#pragma unroll 1
+    for (int i = tid; i < left; i += JOIN_THREADS) kept[i] = sorted[i];
+    if (left == p.n && better(sorted[p.n - 1], least)) least = sorted[p.n - 1];
+    if (tid == 0) count_s = left;
     __syncthreads();
   };
-
   if (few) {
     const int k = tid / (S * p.n);
-    if (mine_key && state[k] == RUNS) put(value(k, mine_key));
+    if (head[0] && state[k] == RUNS) put(value(k, head[0]));
+    __syncthreads();
   } else {
     // ---- a bound below n candidates: the nth largest of the lists' `depth`-th ones, in groups
-    Cand mine = {0, 0, DFLASH_BEAM_MAX};
+    Cand mine = {0, 0};
 #pragma unroll
-    for (int i = 0; i < MAX_LISTS / JOIN_THREADS; ++i) {
+    for (int i = 0; i < PER; ++i) {
       const int l = tid + i * JOIN_THREADS, k = l / S;
       if (l >= lists) break;
-      Cand c = {0, 0, DFLASH_BEAM_MAX}, d = c;
-      if (state[k] == RUNS && head[i]) c = value(k, head[i]);
-      if (state[k] == RUNS && deep[i]) d = value(k, deep[i]);
+      Cand c = {0, 0};
+      const bool runs = state[k] == RUNS;
+      if (runs && head[i]) c = value(k, head[i]);
       head_score[l] = c.score;
-      if (better(d, mine)) mine = d;
+      if (depth > 1) {
+        c.score = 0;
+        if (runs && deep[i]) c = value(k, deep[i]);
+      }
+      if (better(c, mine)) mine = c;
     }
     group_head[tid] = mine;
     __syncthreads();
-    const int G = groups_for(nth), live = min(G, lists), parts = JOIN_THREADS / G;
-    const int g = tid % G, part = tid / G;
-    if (tid < G) {
-      for (int u = tid + G; u < JOIN_THREADS; u += G)
-        if (better(group_head[u], mine)) mine = group_head[u];
-      group_head[tid] = mine;
+    const int live = min(G, lists), parts = JOIN_THREADS / G, g = tid / parts;  // threads of a group
+    if (G < JOIN_THREADS) {
+      if (tid < G) {
+#pragma unroll 1
+        for (int u = tid + G; u < min(JOIN_THREADS, lists); u += G)
+          if (better(group_head[u], mine)) mine = group_head[u];
+        group_head[tid] = mine;
+      }
+      __syncthreads();
     }
-    __syncthreads();
-    if (g < live) {
+    {
       const Cand c = group_head[g];
       int n = 0;
-      for (int u = part; u < live; u += parts) n += better(group_head[u], c);
-      if (c.score && n) atomicAdd(&above[g], n);
+#pragma unroll 1
+      for (int u = tid % parts; u < live; u += parts) n += better(group_head[u], c);
+      for (int d = parts >> 1; d; d >>= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
+      if (g < live && c.score && n == nth - 1) bound_s = c;  // of one group
     }
-    __syncthreads();
-    if (tid < live && group_head[tid].score && above[tid] == nth - 1) bound_s = group_head[tid];
     __syncthreads();
     least = bound_s;
     if (least.score && tid < p.beams && state[tid] == RUNS) {
@@ -724,23 +748,25 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_beam_join(const BeamParams p) 
       const float f = (float)(score - base[tid] + ref[tid] - lost);  // below what rounds to the bound in 64 bits
       floor_of[tid] = f - fabsf(f) * 1e-6f - 1e-30f;                 // and a few last places
     }
+#pragma unroll 1
     for (int l = tid; l < lists; l += JOIN_THREADS) {
       const unsigned long long h = head_score[l];  // equal ones are looked into
       if (h && h >= least.score) chosen[atomicAdd(&chosen_s, 1)] = (uint16_t)l;
     }
     __syncthreads();
 
-    // ---- the candidates of the lists that reach it
-    // LIST_LANES threads a list: its next entries at once, until one is below
+    // ---- the candidates of the lists that reach it: LIST_LANES threads a list, its next entries at once, until one is below
     const int n_chosen = chosen_s;
     constexpr int ABREAST = JOIN_THREADS / LIST_LANES;
+#pragma unroll 1
     for (int c0 = 0; c0 < n_chosen; c0 += ABREAST) {
       const int at = c0 + tid / LIST_LANES;
       const int l = at < n_chosen ? chosen[at] : 0, k = l / S;
       bool open = at < n_chosen;
+#pragma unroll 1
       for (int e0 = 0; e0 < p.n; e0 += LIST_LANES) {
         const int e = e0 + tid % LIST_LANES;
-        Cand c = {0, 0, DFLASH_BEAM_MAX};
+        Cand c = {0, 0};
         bool push = false;
         if (open && e < p.n) {
           const unsigned long long key = best[(long long)l * p.n + e];
@@ -751,23 +777,23 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_beam_join(const BeamParams p) 
         }
         const unsigned some = __ballot_sync(0xffffffffu, push);
         open = open && (some >> (lane / LIST_LANES * LIST_LANES) & ((1u << LIST_LANES) - 1)) == (1u << LIST_LANES) - 1;
-        const int pushers = __syncthreads_count(push);
-        if (count_s + pushers > KEEP) prune();
+        if (count_s + JOIN_THREADS > KEEP) prune();  // the same for all: it is changed only between the barriers below
         __syncthreads();
         if (push && !better(least, c)) put(c);
         if (!__syncthreads_or(open)) break;
       }
     }
   }
-  prune();
-  const int kept = count_s;
-  for (int i = tid; i < p.n; i += JOIN_THREADS) {
-    const bool some = i < kept;
-    const long long o = (long long)b * p.n + i;
-    p.scores_out[o] = some ? (float)unordered(score_of[i]) : -INF;
-    p.parents[o] = some ? b * p.beams + beam_of[i] : -1;
-    p.tokens[o] = some ? (int)(0xffffffffu - (uint32_t)key_of[i]) : -1;
-  }
+
+  // ---- the n best, sorted
+  const int count = count_s;
+  const long long o = (long long)b * p.n;
+  ranked(count, [&](const Cand& c, int rank) {
+    p.scores_out[o + rank] = (float)unordered(c.score);
+    p.parents[o + rank] = b * p.beams + beam_of(c);
+    p.tokens[o + rank] = token_of(c);
+  });
+  for (int i = count + tid; i < p.n; i += JOIN_THREADS) p.scores_out[o + i] = -INF, p.parents[o + i] = p.tokens[o + i] = -1;
 }
 
 // ------------------------------------------------------------------ host
@@ -793,7 +819,7 @@ Plan plan_of(int batch, int beams, int vocab, int n, int dtype) {
   const int per = dtype == DFLASH_F32 ? 4 : 8, vecs = (vocab + per - 1) / per;
   const long long rows = std::max(1ll, (long long)batch * beams);
   const int least = SCAN_THREADS * AHEAD / 2;
-  long long splits = std::min<long long>(BEAM_SLOTS / rows, (vecs + least - 1) / least);
+  long long splits = std::min<long long>(152 * SCAN_CTAS / rows, (vecs + least - 1) / least);
   splits = std::max(1ll, std::min<long long>(splits, std::min(MAX_SPLITS, MAX_LISTS / beams)));
   Plan r;
   r.part = (int)((vecs + splits - 1) / splits + SCAN_THREADS - 1) / SCAN_THREADS * SCAN_THREADS;
