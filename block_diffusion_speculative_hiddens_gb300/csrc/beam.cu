@@ -30,6 +30,9 @@ namespace {
 #define BEAM_AHEAD 4
 #define BEAM_MINB 4
 #endif
+#ifndef BEAM_FEW
+#define BEAM_FEW 128
+#endif
 #ifndef BEAM_JT
 #define BEAM_JT 512
 #endif
@@ -41,6 +44,7 @@ constexpr int AGAIN = 2;          // vectors of a thread that are looked at agai
 constexpr int MAX_SPLITS = 32;    // parts of a row: a lane each when they are joined
 constexpr int MAX_LISTS = 1024;   // parts of a request's rows
 constexpr int JOIN_THREADS = BEAM_JT;
+constexpr int FEW = BEAM_FEW;         // candidates that are ranked without a bound
 constexpr int LIST_LANES = 8;     // of the join that look through a list together
 constexpr int KEEP = 640;         // keys that a selection holds: a push of one a thread, and what was kept before it
 
@@ -569,26 +573,21 @@ DFL_DEV Cand cand(double score, int beam, uint32_t logit, uint32_t token) {
 DFL_DEV int beam_of(const Cand& c) { return DFLASH_BEAM_MAX - 1 - (int)(c.tie >> 56); }
 DFL_DEV int token_of(const Cand& c) { return 0xffffff - (int)(c.tie & 0xffffffu); }
 
-DFL_DEV float warp_max(float v) {
-#pragma unroll
-  for (int d = 16; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
-  return v;
-}
-
 // A part's sum against the row's largest reference r, where the references are not
-// all powers of two.
-__device__ __noinline__ unsigned long long sum_of_any(const PartSum& part, bool some, double& r) {
+// all powers of two; a row's parts are in W lanes.
+__device__ __noinline__ unsigned long long sum_of_any(const PartSum& part, bool some, int W, double& r) {
   const double mine = !some ? -DBL_MAX : part.base2 ? part.q * LN2 : (double)part.top;
   r = mine;
-  for (int d = 16; d; d >>= 1) r = fmax(r, __shfl_xor_sync(0xffffffffu, r, d));
+  for (int d = W >> 1; d; d >>= 1) r = fmax(r, __shfl_xor_sync(0xffffffffu, r, d));
   return some ? (unsigned long long)((double)part.sum * exp(mine - r)) : 0;
 }
 
 __global__ void __launch_bounds__(JOIN_THREADS) k_beam_join(const BeamParams p) {
-  constexpr int WARPS = JOIN_THREADS / 32, PER = MAX_LISTS / JOIN_THREADS;  // lists of a thread
+  constexpr int PER = MAX_LISTS / JOIN_THREADS;  // lists of a thread
   const float INF = __uint_as_float(0x7f800000u);
   enum { DEAD, RUNS, ENDED };
   __shared__ double base[DFLASH_BEAM_MAX], ref[DFLASH_BEAM_MAX];  // score = base + (logit - ref)
+  __shared__ unsigned long long sum_of[DFLASH_BEAM_MAX];
   __shared__ float floor_of[DFLASH_BEAM_MAX];                    // logits below it do not reach the bound
   __shared__ uint8_t state[DFLASH_BEAM_MAX];
   __shared__ unsigned long long head_score[MAX_LISTS];
@@ -598,13 +597,13 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_beam_join(const BeamParams p) 
   __shared__ Cand kept[KEEP], sorted[DFLASH_BEAM_MAX_N];
   __shared__ int count_s, chosen_s;
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, b = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, b = blockIdx.x;
   const int S = p.splits, lists = p.beams * S;
   const unsigned long long* best = p.best + (long long)b * lists * p.n;
   // Few candidates are all ranked.  Of more, the lists are compared at a depth:
   // with fewer than four lists a candidate asked for, deeper, so that few of the
   // lists are above the bound.
-  const bool few = lists * p.n <= JOIN_THREADS;
+  const bool few = lists * p.n <= FEW;
   int depth = 1;
 #pragma unroll 1
   while (depth < p.n && lists < 4 * ((p.n + depth - 1) / depth)) depth *= 2;
@@ -628,41 +627,47 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_beam_join(const BeamParams p) 
   }
 
   // ---- each beam's sum, a lane a part
+  const int W = S > 1 ? 1 << (32 - __clz(S - 1)) : 1;  // lanes of a beam
 #pragma unroll 1
-  for (int k = warp; k < p.beams; k += WARPS) {
-    const int row = b * p.beams + k;
+  for (int k0 = 0; k0 < p.beams; k0 += JOIN_THREADS / W) {
+    const int k = k0 + tid / W, at = tid & (W - 1), row = b * p.beams + k;
     PartSum part = {};
     part.top = -INF;
-    if (lane < S) part = p.sums[row * S + lane];
-    const float score = p.scores[row];
-    const bool done = p.done && p.done[row];
-    int st = DEAD;
-    if (!(score <= FLT_MAX)) {
-      if (lane == 0) flag_nan(p.status);
-    } else if (score > -INF) {
-      st = done ? ENDED : RUNS;
+    float score = -INF;
+    bool done = false;
+    if (k < p.beams) {
+      if (at < S) part = p.sums[row * S + at];
+      score = p.scores[row];
+      done = p.done && p.done[row];
     }
-    double c = score, r = 0.0;
-    if (st == RUNS) {
-      const bool some = part.top > -INF;
-      const float q = warp_max(some && part.base2 ? part.q : -INF);
-      if (!__any_sync(0xffffffffu, some)) {
-        st = DEAD;
-      } else {
-        unsigned long long sum;
-        if (__all_sync(0xffffffffu, !some || part.base2)) {  // shifts to the largest reference
-          r = q * LN2;
-          sum = some && q - part.q < 63.0f ? part.sum >> (int)(q - part.q) : 0;
-        } else {
-          sum = sum_of_any(part, some, r);
-        }
-#pragma unroll
-        for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        const Log l = ln(sum);
-        c = (double)score - (l.e - FIX) * LN2 - (double)l.hi - (double)l.lo;
-      }
+    if (!(score <= FLT_MAX) && at == 0) flag_nan(p.status);
+    const bool runs = score > -INF && score <= FLT_MAX && !done;
+    const bool some = runs && part.top > -INF;  // a beam's parts hold anything only where it runs
+    const unsigned group = (W == 32 ? 0xffffffffu : (1u << W) - 1) << (lane & ~(W - 1));
+    const bool any = __ballot_sync(0xffffffffu, some) & group;
+    const bool bare = __ballot_sync(0xffffffffu, some && !part.base2) & group;
+    float q = some && part.base2 ? part.q : -INF;
+    for (int d = W >> 1; d; d >>= 1) q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, d));
+    double r = q * LN2;
+    unsigned long long sum = some && q - part.q < 63.0f ? part.sum >> (int)(q - part.q) : 0;  // shifted to the largest reference
+    if (__any_sync(0xffffffffu, bare)) {
+      double r2 = 0.0;
+      const unsigned long long sum2 = sum_of_any(part, some, W, r2);
+      if (bare) r = r2, sum = sum2;
     }
-    if (lane == 0) base[k] = c, ref[k] = r, state[k] = (uint8_t)st, floor_of[k] = -INF;
+    for (int d = W >> 1; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (k < p.beams && at == 0) {
+      base[k] = score;
+      ref[k] = any ? r : 0.0;
+      sum_of[k] = sum;
+      state[k] = (uint8_t)(any ? RUNS : score > -INF && score <= FLT_MAX && done ? ENDED : DEAD);
+      floor_of[k] = -INF;
+    }
+  }
+  __syncthreads();
+  if (tid < p.beams && state[tid] == RUNS) {
+    const Log l = ln(sum_of[tid]);
+    base[tid] += (FIX - l.e) * LN2 - (double)l.hi - (double)l.lo;
   }
   __syncthreads();
 
