@@ -50,7 +50,6 @@ DFL_DEV void give_up(const Pool& p, int id) {
 // that stay as they are (a long shared prefix) cost their reads only.  The
 // lengths, which every CTA reads, are written by the last one.
 constexpr int FORK_THREADS = 1024;
-constexpr int FORK_UNITS = DFLASH_POOL_MAX_BATCH / FORK_THREADS;  // of four entries, a thread
 
 DFL_DEV int4 load_entries(const Pool& p, int row, int col, bool vec) {
   const int* at = p.table + row * p.stride + col;
@@ -63,96 +62,118 @@ DFL_DEV int4 load_entries(const Pool& p, int row, int col, bool vec) {
   return v;
 }
 
-// What row b becomes: its parent's row, or -1 (empty), or b itself (as it is).
-DFL_DEV int parent_of(const Pool& p, const int* parents, int b, int& len, bool& bad) {
-  const int src = parents[b];
-  bad = false;
-  if (src == b) return b;
-  len = 0;
+// What becomes of row b: it keeps its entries (src = b), or goes on as row src.
+struct Step {
+  int src, len;   // -1: empty; its new length
+  int had, has;   // pages before and after
+  bool bad;
+};
+DFL_DEV Step step_of(const Pool& p, const int* parents, int b) {
+  Step s;
+  s.src = parents[b];
   const int mine = p.lens[b];
-  if (src >= 0 && src < p.batch) len = p.lens[src];
-  if (src < -1 || src >= p.batch || !len_fits(p, len) || !len_fits(p, mine)) {
-    bad = true;
-    return b;
-  }
-  return src;
+  const bool any = s.src >= 0 && s.src < p.batch;
+  s.len = any ? p.lens[s.src] : 0;
+  s.bad = s.src != b && ((!any && s.src != -1) || !len_fits(p, s.len) || !len_fits(p, mine));
+  if (s.bad) s.src = b;
+  if (s.src == b) s.len = mine;
+  s.had = pages_of(mine, p.shift);
+  s.has = pages_of(s.len, p.shift);
+  return s;
 }
 
-__global__ void __launch_bounds__(FORK_THREADS) k_fork(const Pool p, const int* parents, int cols, bool vec) {
+// Four entries of a row: the new ones in place of the old ones, and the counts.
+DFL_DEV void change_entries(const Pool& p, int b, int col, const Step& s, const int4& now, const int4& was, bool vec) {
+  const int w[4] = {was.x, was.y, was.z, was.w}, n[4] = {now.x, now.y, now.z, now.w};
+  int out[4];
+  unsigned differ = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const bool held = col + j < s.had, holds = col + j < s.has;
+    out[j] = holds ? n[j] : held ? -1 : w[j];
+    differ |= (held != holds || (held && w[j] != n[j])) << j;
+  }
+  if (!differ) return;
+  int* at = p.table + b * p.stride + col;
+#pragma unroll 1
+  for (unsigned d = differ; d; d &= d - 1) {
+    const int j = __ffs(d) - 1;
+    if (col + j < s.has) hold(p, j == 0 ? n[0] : j == 1 ? n[1] : j == 2 ? n[2] : n[3]);
+    if (col + j < s.had) give_up(p, j == 0 ? w[0] : j == 1 ? w[1] : j == 2 ? w[2] : w[3]);
+  }
+  if (vec && col + 4 <= p.max_pages) {
+    *reinterpret_cast<int4*>(at) = make_int4(out[0], out[1], out[2], out[3]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (col + j < max(s.has, s.had)) at[j] = out[j];
+  }
+}
+
+// Whether this is the grid's last CTA here, which finds what the others have done
+// and read done; the count is back at 0 behind it.
+DFL_DEV bool last_of(uint32_t* ticket) {
+  unsigned old;
+  asm volatile("atom.inc.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(old) : "l"(ticket), "r"(gridDim.x - 1) : "memory");
+  return old == gridDim.x - 1;
+}
+
+// ONE: a unit of four entries a thread, in registers; else in shared memory [units].
+template <bool ONE>
+__global__ void __launch_bounds__(FORK_THREADS, 1) k_fork(const Pool p, const int* parents, int cols, bool vec) {
+  extern __shared__ __align__(16) int4 rows[];
   pdl_launch_dependents();
   pdl_wait();
   const int col0 = blockIdx.x * cols, quads = cols >> 2, units = p.batch * quads;
-  int4 now[FORK_UNITS];
-#pragma unroll
-  for (int i = 0; i < FORK_UNITS; ++i) {
-    const int u = threadIdx.x + i * FORK_THREADS;
-    if (u >= units) break;
-    const int b = u / quads, col = col0 + 4 * (u - b * quads);
-    int len;
-    bool bad;
-    const int src = parent_of(p, parents, b, len, bad);
-    if (bad && blockIdx.x == 0 && col == 0) dev_error(p.status, DFLASH_DEV_ARG);
-    if (src != b && src >= 0 && col < pages_of(len, p.shift)) now[i] = load_entries(p, src, col, vec);
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < FORK_UNITS; ++i) {
-    const int u = threadIdx.x + i * FORK_THREADS;
-    if (u >= units) break;
-    const int b = u / quads, col = col0 + 4 * (u - b * quads);
-    int len;
-    bool bad;
-    const int src = parent_of(p, parents, b, len, bad);
-    if (src == b) continue;
-    const int has = src < 0 ? 0 : pages_of(len, p.shift), had = pages_of(p.lens[b], p.shift);
-    if (col >= max(has, had)) continue;
-    const int4 was = load_entries(p, b, col, vec);
-    const int w[4] = {was.x, was.y, was.z, was.w}, n[4] = {now[i].x, now[i].y, now[i].z, now[i].w};
-    int out[4];
-    bool changed = false;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const bool held = col + j < had, holds = col + j < has;
-      out[j] = holds ? n[j] : held ? -1 : w[j];
-      if (held && holds && w[j] == n[j]) continue;
-      changed |= held || holds;
-      if (holds) hold(p, n[j]);
-      if (held) give_up(p, w[j]);
+  const int tid = threadIdx.x;
+  // the lengths: the first column's threads of each row have them
+  if (ONE) {
+    const int b = tid / quads, col = col0 + 4 * (tid - b * quads);
+    Step s = {};
+    int4 now = make_int4(-1, -1, -1, -1), was = now;
+    if (tid < units) {
+      s = step_of(p, parents, b);
+      if (s.src != b) {
+        if (col < s.has) now = load_entries(p, s.src, col, vec);
+        if (col < max(s.has, s.had)) was = load_entries(p, b, col, vec);
+      }
     }
-    if (!changed) continue;
-    int* at = p.table + b * p.stride + col;
-    if (vec && col + 4 <= p.max_pages) {
-      *reinterpret_cast<int4*>(at) = make_int4(out[0], out[1], out[2], out[3]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (col + j < max(has, had)) at[j] = out[j];
+    __syncthreads();
+    if (tid < units && s.src != b && col < max(s.has, s.had)) change_entries(p, b, col, s, now, was, vec);
+    if (tid < units && s.bad && col == 0) dev_error(p.status, DFLASH_DEV_ARG);
+    __shared__ bool last;
+    if (gridDim.x > 1) {
+      if (tid == 0) last = last_of(p.status + 1);
+      __syncthreads();
+      if (!last) return;
     }
-  }
-  // the lengths, once every CTA has read them
-  __shared__ bool last;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    __threadfence();
-    last = atomicInc(p.status + 1, gridDim.x - 1) == gridDim.x - 1;  // wraps to 0
-    __threadfence();
-  }
-  __syncthreads();
-  if (!last) return;
-  int lens[FORK_UNITS];
-#pragma unroll
-  for (int i = 0; i < FORK_UNITS; ++i) {
-    const int b = threadIdx.x + i * FORK_THREADS;
-    if (b >= p.batch) break;
-    bool bad;
-    if (parent_of(p, parents, b, lens[i], bad) == b) lens[i] = p.lens[b];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < FORK_UNITS; ++i) {
-    const int b = threadIdx.x + i * FORK_THREADS;
-    if (b >= p.batch) break;
-    p.lens[b] = lens[i];
+    if (tid < units && tid == b * quads && s.src != b) p.lens[b] = s.len;
+  } else {
+#pragma unroll 1
+    for (int u = tid; u < units; u += FORK_THREADS) {
+      const int b = u / quads, col = col0 + 4 * (u - b * quads);
+      const Step s = step_of(p, parents, b);
+      if (s.src != b && col < s.has) rows[u] = load_entries(p, s.src, col, vec);
+      if (s.bad && col == 0) dev_error(p.status, DFLASH_DEV_ARG);
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int u = tid; u < units; u += FORK_THREADS) {
+      const int b = u / quads, col = col0 + 4 * (u - b * quads);
+      const Step s = step_of(p, parents, b);
+      if (s.src != b && col < max(s.has, s.had)) change_entries(p, b, col, s, rows[u], load_entries(p, b, col, vec), vec);
+    }
+    __shared__ bool last;
+    __syncthreads();
+    if (tid == 0) last = last_of(p.status + 1);
+    __syncthreads();
+    if (!last) return;
+    int* lens = reinterpret_cast<int*>(rows);
+#pragma unroll 1
+    for (int b = tid; b < p.batch; b += FORK_THREADS) lens[b] = step_of(p, parents, b).len;
+    __syncthreads();
+#pragma unroll 1
+    for (int b = tid; b < p.batch; b += FORK_THREADS) p.lens[b] = lens[b];
   }
 }
 
@@ -261,36 +282,21 @@ DFL_DEV unsigned long long block_before(unsigned long long v, unsigned long long
   return buf[warp] + s - v;
 }
 
-// What a sequence asks for.
-struct Change {
-  bool valid;
-  int had, has;  // pages
-  int inside;    // positions of the last page held, where the sequence grows inside it (else 0)
-};
-DFL_DEV Change change_of(const Pool& p, int len, int now) {
-  Change c = {};
-  c.valid = len_fits(p, len) && len_fits(p, now);
-  if (!c.valid) return c;
-  c.had = pages_of(len, p.shift);
-  c.has = pages_of(now, p.shift);
-  if (now > len) c.inside = len & ((1 << p.shift) - 1);
-  return c;
-}
-
 // Shared last pages of growing sequences: page -> their number and the lowest.
 struct Sharers {
   int* page;        // [slots], -1 empty
   uint32_t* who;    // number << 16 | lowest sequence (both below 2^14)
   int mask;
 };
+DFL_DEV int first_slot(const Sharers& h, int page) { return (int)(((unsigned)page * 2654435769u) >> 7) & h.mask; }
 DFL_DEV int slot_of(const Sharers& h, int page) {
-  int s = (int)(((unsigned)page * 2654435769u) >> 7) & h.mask;
+  int s = first_slot(h, page);
   while (h.page[s] != page) s = (s + 1) & h.mask;  // it was put there
   return s;
 }
 DFL_DEV void add_sharer(const Sharers& h, int page, int b) {
-  int s = (int)(((unsigned)page * 2654435769u) >> 7) & h.mask;
-  for (;;) {  // at most half of the slots are taken
+  int s = first_slot(h, page);
+  for (;;) {  // there are as many slots as sequences, at least
     const int was = atomicCAS(h.page + s, -1, page);
     if (was == -1 || was == page) break;
     s = (s + 1) & h.mask;
@@ -303,93 +309,106 @@ DFL_DEV void add_sharer(const Sharers& h, int page, int b) {
   } while (old != seen);
 }
 
-__global__ void __launch_bounds__(SCAN_THREADS) k_resize(const Pool p, const int* new_lens, int* moves, int capacity,
-                                                         int ctas, int slots, bool vec) {
+// What is known of a sequence in the call, in shared memory.
+struct Change {
+  int had, has;    // pages; -1: the sequence stays as it is
+  int page;        // its last one, where the sequence grows inside one that is shared or pinned (else -1)
+  unsigned off;    // pages taken before it
+};
+// [16 bits: copies before it][1: a copy of `page` is made][9: positions held of the last page]
+DFL_DEV uint32_t pack_copy(int before, bool copy, int inside) { return (uint32_t)before << 16 | (uint32_t)copy << 15 | (uint32_t)inside; }
+
+__global__ void __launch_bounds__(SCAN_THREADS, 1) k_resize(const Pool p, const int* new_lens, int* moves, int capacity,
+                                                         int ctas, int slots, bool vec, bool tvec) {
   extern __shared__ __align__(16) char smem[];
   __shared__ unsigned long long sums[SCAN_WARPS + 1];
   __shared__ int counts[SCAN_WARPS + 1];
-  unsigned* off = reinterpret_cast<unsigned*>(smem);                // [batch + 1] pages taken before a sequence
+  __shared__ int shrinks;
+  Change* seq = reinterpret_cast<Change*>(smem);                      // [batch]
+  uint32_t* copies = reinterpret_cast<uint32_t*>(seq + p.batch);     // [batch]
   Sharers shared;
-  shared.page = reinterpret_cast<int*>(off + p.batch + 1);          // [slots]
-  shared.who = reinterpret_cast<uint32_t*>(shared.page + slots);    // [slots]
+  shared.page = reinterpret_cast<int*>(copies + p.batch);             // [slots]
+  shared.who = reinterpret_cast<uint32_t*>(shared.page + slots);      // [slots]
   shared.mask = slots - 1;
-  uint16_t* copies = reinterpret_cast<uint16_t*>(shared.who + slots);  // [batch] copies up to and with a sequence's
   const int rank = ctas > 1 ? (int)cluster_ctarank() : 0;
+  const int lane = threadIdx.x & 31;
   pdl_launch_dependents();
   for (int i = threadIdx.x; i < slots; i += SCAN_THREADS) {
     shared.page[i] = -1;
     shared.who[i] = 0xffffu;
   }
+  if (threadIdx.x == 0) shrinks = 0;
   pdl_wait();
+  const Part part = scan_part(p.n_pages, ctas, rank);
+  const int4 head = load_refs(p.refs, part.first + 4 * lane, part.end, vec);  // on its way meanwhile
   __syncthreads();
 
   // every CTA goes through the whole batch, a thread a few sequences in a row
   const int per = (p.batch + SCAN_THREADS - 1) / SCAN_THREADS;
   const int b0 = min(p.batch, (int)threadIdx.x * per), b1 = min(p.batch, b0 + per);
   const bool speaks = rank == 0;
+  bool less = false;
+#pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     const int len = p.lens[b], now = new_lens[b];
-    const Change c = change_of(p, len, now);
-    if (!c.valid && speaks)
-      dev_error(p.status, len < 0 || now < 0 || !len_fits(p, len) ? DFLASH_DEV_ARG : DFLASH_DEV_CAPACITY);
-    if (c.inside) {
-      const int page = p.table[b * p.stride + c.had - 1];
-      if ((unsigned)page >= (unsigned)p.n_pages) {
-        if (speaks) dev_error(p.status, DFLASH_DEV_PAGE);
-      } else {
-        const int r = p.refs[page];
-        if (r > 1) add_sharer(shared, page, b);
-        else if (r == 0 && speaks) dev_error(p.status, DFLASH_DEV_PAGE);
-      }
+    Change c = {-1, -1, -1, 0};
+    int inside = 0;
+    if (!len_fits(p, len) || !len_fits(p, now)) {
+      if (speaks) dev_error(p.status, now < 0 || !len_fits(p, len) ? DFLASH_DEV_ARG : DFLASH_DEV_CAPACITY);
+    } else {
+      c.had = pages_of(len, p.shift);
+      c.has = pages_of(now, p.shift);
+      less |= c.has < c.had;
+      if (now > len) inside = len & ((1 << p.shift) - 1);
     }
+    if (inside) {
+      const int page = p.table[b * p.stride + c.had - 1];
+      const int r = (unsigned)page < (unsigned)p.n_pages ? p.refs[page] : 0;
+      if (r > 1) add_sharer(shared, page, b);
+      if (r > 1 || r < 0) c.page = page;
+      if (r == 0 && speaks) dev_error(p.status, DFLASH_DEV_PAGE);  // none, or one that nobody holds
+    }
+    seq[b] = c;
+    copies[b] = (uint32_t)inside;
   }
+  if (less) shrinks = 1;
   __syncthreads();
-  unsigned long long sum = 0;
-  auto takes = [&](int b, unsigned long long& need, bool& copy) {
-    const Change c = change_of(p, p.lens[b], new_lens[b]);
-    copy = false;
-    if (c.inside) {
-      const int page = p.table[b * p.stride + c.had - 1];
-      if ((unsigned)page < (unsigned)p.n_pages) {
-        const int r = p.refs[page];
-        if (r > 1) {
-          const uint32_t w = shared.who[slot_of(shared, page)];
-          copy = (int)(w >> 16) < r || (int)(w & 0xffffu) != b;
-        } else {
-          copy = r < 0;
-        }
+  unsigned long long sum = 0;  // pages taken, copies above 2^48
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) {
+    const Change c = seq[b];
+    bool copy = false;
+    if (c.page >= 0) {
+      const int r = p.refs[c.page];
+      copy = r < 0;
+      if (!copy) {
+        const uint32_t w = shared.who[slot_of(shared, c.page)];
+        copy = (int)(w >> 16) < r || (int)(w & 0xffffu) != b;
       }
     }
-    need = (unsigned long long)max(c.has - c.had, 0) + copy;
-  };
-  for (int b = b0; b < b1; ++b) {
-    unsigned long long need;
-    bool copy;
-    takes(b, need, copy);
-    sum += need | (unsigned long long)copy << 48;
+    copies[b] |= (uint32_t)copy << 15;
+    sum += (unsigned long long)max(c.has - c.had, 0) + copy + ((unsigned long long)copy << 48);
   }
   unsigned long long before = block_before(sum, sums);
   const unsigned long long all = sums[SCAN_WARPS];
   const unsigned long long want = all & ((1ull << 48) - 1);
   const int n_copies = (int)(all >> 48);
-  if (want <= (unsigned long long)p.n_pages) {  // else it does not fit anyway, nor 32 bits
-    for (int b = b0; b < b1; ++b) {
-      unsigned long long need;
-      bool copy;
-      takes(b, need, copy);
-      off[b] = (unsigned)before;
-      before += need | (unsigned long long)copy << 48;
-      copies[b] = (uint16_t)(before >> 48);
-    }
-    if (threadIdx.x == 0) off[p.batch] = (unsigned)want;
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) {
+    const Change c = seq[b];
+    const uint32_t w = copies[b];
+    const bool copy = w >> 15 & 1;
+    seq[b].off = (unsigned)before;  // all of them fit if the call does
+    copies[b] = pack_copy((int)(before >> 48), copy, w & 0x1ff);
+    before += (unsigned long long)max(c.has - c.had, 0) + copy + ((unsigned long long)copy << 48);
   }
 
   // the free pages
-  const int lane = threadIdx.x & 31;
-  const Part part = scan_part(p.n_pages, ctas, rank);
+  auto refs_at = [&](int i) { return i == part.first ? head : load_refs(p.refs, i + 4 * lane, part.end, vec); };
   int mine = 0;
+#pragma unroll 1
   for (int i = part.first; i < part.end; i += 128) {
-    const int4 r = load_refs(p.refs, i + 4 * lane, part.end, vec);
+    const int4 r = refs_at(i);
     mine += (r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0);
   }
   const Before found = cluster_before(warp_total(mine), counts, ctas, rank);
@@ -399,6 +418,7 @@ __global__ void __launch_bounds__(SCAN_THREADS) k_resize(const Pool p, const int
   const int used = fits ? n_copies : 0;
   const int tid = rank * SCAN_THREADS + threadIdx.x;
   if (tid < 3) moves[tid] = tid == 0 ? used : 0;
+#pragma unroll 1
   for (int i = used + 1 + tid; i <= capacity; i += ctas * SCAN_THREADS) {
     moves[3ll * i] = moves[3ll * i + 1] = -1;
     moves[3ll * i + 2] = 0;
@@ -410,63 +430,71 @@ __global__ void __launch_bounds__(SCAN_THREADS) k_resize(const Pool p, const int
     return;
   }
   int next = found.before;
+#pragma unroll 1
   for (int i = part.first; i < part.end && next < (int)want; i += 128) {
-    const int4 r = load_refs(p.refs, i + 4 * lane, part.end, vec);
+    const int4 r = refs_at(i);
     const int f[4] = {r.x == 0, r.y == 0, r.z == 0, r.w == 0};
     const int n = f[0] + f[1] + f[2] + f[3];
     int place = next + warp_before(n);
     next += warp_total(n);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (!f[j]) continue;
-      const int k = place++;
-      if (k >= (int)want) continue;
-      const int page = i + 4 * lane + j;
-      int lo = 0, hi = p.batch;  // the last b with off[b] <= k: one that takes pages
+    unsigned mask = (unsigned)f[0] | (unsigned)f[1] << 1 | (unsigned)f[2] << 2 | (unsigned)f[3] << 3;
+#pragma unroll 1
+    for (; mask; mask &= mask - 1, ++place) {
+      if (place >= (int)want) break;
+      const int page = i + 4 * lane + __ffs(mask) - 1;
+      int lo = 0, hi = p.batch;  // the last sequence with off <= place: one that takes pages
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if ((int)off[mid] <= k) lo = mid;
+        if ((int)seq[mid].off <= place) lo = mid;
         else hi = mid;
       }
-      const int b = lo, len = p.lens[b];
-      const int had = pages_of(len, p.shift);
-      const bool copy = copies[b] != (b > 0 ? copies[b - 1] : 0);
-      int* row = p.table + b * p.stride;
-      const int at = k - (int)off[b];
+      const Change c = seq[lo];
+      const uint32_t w = copies[lo];
+      const int at = place - (int)c.off, copy = w >> 15 & 1;
+      int* row = p.table + lo * p.stride;
       p.refs[page] = 1;
       if (copy && at == 0) {
-        const int from = row[had - 1];
-        int* m = moves + 3ll * copies[b];
-        m[0] = from;
+        int* m = moves + 3ll * (1 + (w >> 16));
+        m[0] = c.page;
         m[1] = page;
-        m[2] = len & ((1 << p.shift) - 1);
-        row[had - 1] = page;
-        give_up(p, from);
+        m[2] = w & 0x1ff;
+        row[c.had - 1] = page;
+        give_up(p, c.page);
       } else {
-        row[had + at - copy] = page;
+        row[c.had + at - copy] = page;
       }
     }
   }
   __syncwarp();
   cluster_sync_all();  // the free pages are found, and no length is read any more
-  // what is given up, a warp a sequence, and the new lengths
-  for (int b = rank * SCAN_WARPS + (threadIdx.x >> 5); b < p.batch; b += ctas * SCAN_WARPS) {
-    const int len = p.lens[b], now = new_lens[b];
-    const Change c = change_of(p, len, now);
-    __syncwarp();
-    if (!c.valid) continue;
-    for (int i = c.has + lane; i < c.had; i += 32) {
-      int* at = p.table + b * p.stride + i;
-      give_up(p, *at);
-      *at = -1;
+  // what is given up, 128 entries a warp at a time, and the new lengths
+  if (shrinks) {
+    const int pieces = (p.max_pages + 127) >> 7;
+    const int warps = ctas * SCAN_WARPS;
+#pragma unroll 1
+    for (int it = rank * SCAN_WARPS + (threadIdx.x >> 5); it < p.batch * pieces; it += warps) {
+      const int b = it / pieces, i = ((it - b * pieces) << 7) + 4 * lane;
+      const Change c = seq[b];
+      if (i + 4 <= c.has || i >= c.had) continue;
+      const int4 v = load_entries(p, b, i, tvec);
+      const int id[4] = {v.x, v.y, v.z, v.w};
+      int* row = p.table + b * p.stride;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (i + j < c.has || i + j >= c.had) continue;
+        give_up(p, id[j]);
+        row[i + j] = -1;
+      }
     }
-    if (lane == 0) p.lens[b] = now;
   }
+#pragma unroll 1
+  for (int b = tid; b < p.batch; b += ctas * SCAN_THREADS)
+    if (seq[b].had >= 0) p.lens[b] = new_lens[b];
 }
 
 // ------------------------------------------------------------------ compact
 
-__global__ void __launch_bounds__(SCAN_THREADS) k_compact(const Pool p, int* moves, int capacity, int* remap, int ctas,
+__global__ void __launch_bounds__(SCAN_THREADS, 1) k_compact(const Pool p, int* moves, int capacity, int* remap, int ctas,
                                                           bool vec) {
   __shared__ int free_counts[SCAN_WARPS + 1], held_counts[SCAN_WARPS + 1], low[SCAN_WARPS + 1];
   const int rank = ctas > 1 ? (int)cluster_ctarank() : 0;
@@ -474,9 +502,12 @@ __global__ void __launch_bounds__(SCAN_THREADS) k_compact(const Pool p, int* mov
   pdl_launch_dependents();
   pdl_wait();
   const Part part = scan_part(p.n_pages, ctas, rank);
+  const int4 head = load_refs(p.refs, part.first + 4 * lane, part.end, vec);
+  auto refs_at = [&](int i) { return i == part.first ? head : load_refs(p.refs, i + 4 * lane, part.end, vec); };
   int f = 0, h = 0;
+#pragma unroll 1
   for (int i = part.first; i < part.end; i += 128) {
-    const int4 r = load_refs(p.refs, i + 4 * lane, part.end, vec);
+    const int4 r = refs_at(i);
     f += (r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0);
     h += (r.x > 0) + (r.y > 0) + (r.z > 0) + (r.w > 0);
   }
@@ -485,17 +516,19 @@ __global__ void __launch_bounds__(SCAN_THREADS) k_compact(const Pool p, int* mov
   const Before held = cluster_before(warp_total(h), held_counts, ctas, rank);
   // held pages below `used` stay
   int stay = 0;
+#pragma unroll 1
   for (int i = part.first; i < min(part.end, used); i += 128) {
     const int q = i + 4 * lane;
-    const int4 r = load_refs(p.refs, q, part.end, vec);
+    const int4 r = refs_at(i);
     stay += (r.x > 0 && q < used) + (r.y > 0 && q + 1 < used) + (r.z > 0 && q + 2 < used) + (r.w > 0 && q + 3 < used);
   }
   const int staying = cluster_before(warp_total(stay), low, ctas, rank).total;
   const int n = held.total - staying;  // that move; at least as many free pages lie below `used`
   int hole = holes.before, mover = held.before - staying;
+#pragma unroll 1
   for (int i = part.first; i < part.end; i += 128) {
     const int q = i + 4 * lane;
-    const int4 v = load_refs(p.refs, q, part.end, vec);
+    const int4 v = refs_at(i);
     const int r[4] = {v.x, v.y, v.z, v.w};
     int nf = 0, nh = 0;
 #pragma unroll
@@ -600,12 +633,18 @@ template <typename V>
 __global__ void __launch_bounds__(COPY_THREADS) k_copy_pages(const __grid_constant__ CopyParams p) {
   pdl_launch_dependents();
   pdl_wait();
-  const int n = min(max(p.moves[0], 0), p.capacity);
-  const long long items = (long long)n * p.n_pools * p.chunks;
-  for (long long it = blockIdx.x; it < items; it += gridDim.x) {
-    const long long mp = it / p.chunks;
-    const int c = (int)(it - mp * p.chunks);
-    const int m = (int)(mp / p.n_pools), which = (int)(mp - (long long)m * p.n_pools);
+  const int n = min(max(p.moves[0], 0), min(p.capacity, p.n_pages));  // no page is copied to twice
+  // the first chunk of every page, then the second: pages of which little is
+  // copied then cost every CTA alike
+  const unsigned pages = (unsigned)n * (unsigned)p.n_pools;  // of all pools: below 2^31
+  if (pages == 0) return;
+  const unsigned step = gridDim.x % pages;
+  const int step_c = (int)(gridDim.x / pages);
+  int c = (int)(blockIdx.x / pages);
+  for (unsigned at = blockIdx.x % pages; c < p.chunks; at += step, c += step_c) {
+    if (at >= pages) at -= pages, ++c;
+    if (c >= p.chunks) break;
+    const int m = (int)(at / (unsigned)p.n_pools), which = (int)(at - (unsigned)m * p.n_pools);
     const int* mv = p.moves + 3ll * (m + 1);
     const int src = mv[0], dst = mv[1], count = min(mv[2], p.page_size);
     const int p0 = c * p.chunk;
@@ -702,7 +741,13 @@ int scan_ctas(int n_pages) {
   return c;
 }
 
-size_t resize_smem(int batch, int slots) { return 4ull * (batch + 1) + 8ull * slots + 2ull * batch; }
+// Slots of the shared pages: twice the sequences, or as many as there are at least where that does not fit.
+int resize_slots(int batch) {
+  int slots = 64;
+  while (slots < (batch > 4096 ? batch : 2 * batch)) slots *= 2;
+  return slots;
+}
+size_t resize_smem(int batch) { return (sizeof(Change) + 4ull) * batch + 8ull * resize_slots(batch); }
 
 }  // namespace
 
@@ -720,13 +765,19 @@ int dflash_pages_fork(const dflash_page_pool* c, const int32_t* parents, void* s
   const PoolParts w = pool_parts(c);
   if (!apart({w.refs, w.table, w.lens, w.status}, {strided_ints(parents, c->batch)})) return DFLASH_ERR_INVALID_ARG;
   // Columns of a CTA: as many as give every thread one unit of four entries, but
-  // no fewer than four: then up to eight units a thread.
+  // no fewer than four: larger batches take several units a thread.
   int cols = 4;
   while (cols * 2 * c->batch <= 4 * FORK_THREADS && cols < c->max_pages) cols *= 2;
   DeviceGuard guard(c->device);
   if (!guard.ok) return DFLASH_ERR_CUDA;
-  return launch(k_fork, dim3((unsigned)((c->max_pages + cols - 1) / cols)), FORK_THREADS, 0, 1, stream, pool_of(c), parents,
-                cols, table_vec(c));
+  const dim3 grid((unsigned)((c->max_pages + cols - 1) / cols));
+  const int units = c->batch * (cols / 4);
+  if (units <= FORK_THREADS)
+    return launch(k_fork<true>, grid, (units + 31) / 32 * 32, 0, 1, stream, pool_of(c), parents, cols, table_vec(c));
+  if (int e = cuda_status(cudaFuncSetAttribute(k_fork<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               DFLASH_POOL_MAX_BATCH * (int)sizeof(int4))))
+    return e;
+  return launch(k_fork<false>, grid, FORK_THREADS, units * sizeof(int4), 1, stream, pool_of(c), parents, cols, table_vec(c));
 }
 
 int dflash_pages_resize(const dflash_page_pool* c, const int32_t* new_lens, int32_t* moves, int32_t capacity,
@@ -738,18 +789,17 @@ int dflash_pages_resize(const dflash_page_pool* c, const int32_t* new_lens, int3
   if (!apart({w.refs, w.table, w.lens, w.status, strided_ints(moves, 3 + 3ll * capacity)},
              {strided_ints(new_lens, c->batch)}))
     return DFLASH_ERR_INVALID_ARG;
-  int slots = 64;
-  while (slots < 2 * c->batch) slots *= 2;
-  const size_t smem = resize_smem(c->batch, slots);
+  if ((long long)c->batch * ((c->max_pages + 127ll) / 128) > 0x7fffffffll) return DFLASH_ERR_CAPACITY;
+  const size_t smem = resize_smem(c->batch);
   DeviceGuard guard(c->device);
   if (!guard.ok) return DFLASH_ERR_CUDA;
   if (smem > 48 * 1024)
     if (int e = cuda_status(cudaFuncSetAttribute(k_resize, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 (int)resize_smem(DFLASH_POOL_MAX_BATCH, 2 * DFLASH_POOL_MAX_BATCH))))
+                                                 (int)resize_smem(DFLASH_POOL_MAX_BATCH))))
       return e;
   const int ctas = scan_ctas(c->n_pages);
   return launch(k_resize, dim3((unsigned)ctas), SCAN_THREADS, smem, ctas, stream, pool_of(c), new_lens, moves, capacity,
-                ctas, slots, (reinterpret_cast<uintptr_t>(c->refs) & 15) == 0);
+                ctas, resize_slots(c->batch), (reinterpret_cast<uintptr_t>(c->refs) & 15) == 0, table_vec(c));
 }
 
 int dflash_pages_compact(const dflash_page_pool* c, int32_t* moves, int32_t capacity, int32_t* remap, void* stream) {
@@ -809,17 +859,20 @@ int dflash_pages_copy(const dflash_paged_cache* caches, int32_t n_caches, const 
   p.chunks = (c0.page_size + p.chunk - 1) / p.chunk;
   p.flat = flat;
   p.status = c0.status;
+  const long long most = std::min(capacity, c0.n_pages);
+  const int per = (int)std::min<long long>(COPY_CACHES, 0x3fffffffll / most);  // page copies of a launch fit 31 bits
+  if (per < 1) return DFLASH_ERR_CAPACITY;
   DeviceGuard guard(c0.device);
   if (!guard.ok) return DFLASH_ERR_CUDA;
-  for (int at = 0; at < n_caches; at += COPY_CACHES) {
-    const int n = std::min(COPY_CACHES, n_caches - at);
+  for (int at = 0; at < n_caches; at += per) {
+    const int n = std::min(per, n_caches - at);
     p.n_pools = 2 * n;
     for (int i = 0; i < n; ++i) {
       const dflash_paged_cache& c = caches[at + i];
       p.pool[2 * i] = {static_cast<char*>(c.k), 2 * c.k_page_stride, 2 * c.k_pos_stride, 2 * c.k_head_stride};
       p.pool[2 * i + 1] = {static_cast<char*>(c.v), 2 * c.v_page_stride, 2 * c.v_pos_stride, 2 * c.v_head_stride};
     }
-    const unsigned grid = (unsigned)std::min<long long>(152 * 8, (long long)capacity * p.n_pools * p.chunks);
+    const unsigned grid = (unsigned)std::min<long long>(152 * 8, most * p.n_pools * p.chunks);
     const int e = vec ? launch(k_copy_pages<uint4>, dim3(grid), COPY_THREADS, 0, 1, stream, p)
                       : launch(k_copy_pages<uint16_t>, dim3(grid), COPY_THREADS, 0, 1, stream, p);
     if (e) return e;
