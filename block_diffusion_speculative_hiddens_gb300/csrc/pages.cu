@@ -6,6 +6,7 @@
 // out of step with the counts, the pages handed out do not depend on the order of
 // atomics (the lowest free ones, by rank), and compact needs no other view.
 #include <algorithm>
+#include <climits>
 #include <type_traits>
 
 #include "common.cuh"
@@ -26,20 +27,30 @@ struct Pool {
 DFL_DEV int pages_of(int len, int shift) { return (int)(((unsigned)len + (1u << shift) - 1) >> shift); }
 DFL_DEV bool len_fits(const Pool& p, int len) { return len >= 0 && pages_of(len, p.shift) <= p.max_pages; }
 
-// One holder more or less of a page.  Whether a page is pinned does not change
-// during a call, and a page given up has a holder until then.
-DFL_DEV void hold(const Pool& p, int id) {
-  if ((unsigned)id >= (unsigned)p.n_pages) dev_error(p.status, DFLASH_DEV_PAGE);
-  else if (__ldcg(p.refs + id) >= 0) atomicAdd(p.refs + id, 1);
-}
+// One holder less of a page.  Whether a page is pinned does not change during a
+// call, and a page given up has a holder until then.
 DFL_DEV void give_up(const Pool& p, int id) {
-  if ((unsigned)id >= (unsigned)p.n_pages) {
-    dev_error(p.status, DFLASH_DEV_PAGE);
-    return;
-  }
   const int r = __ldcg(p.refs + id);
   if (r > 0) atomicSub(p.refs + id, 1);
-  else if (r == 0) dev_error(p.status, DFLASH_DEV_PAGE);
+}
+
+// One holder more and less of each of four entries' pages, those with their bit set.
+DFL_DEV void count_entries(const Pool& p, const int (&more)[4], unsigned m, const int (&less)[4], unsigned l) {
+  int rm[4], rl[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {  // all of them on their way at once; outside the pool: as if nobody held it
+    rm[j] = m >> j & 1 && (unsigned)more[j] < (unsigned)p.n_pages ? __ldcg(p.refs + more[j]) : INT_MIN;
+    rl[j] = l >> j & 1 ? (unsigned)less[j] < (unsigned)p.n_pages ? __ldcg(p.refs + less[j]) : 0 : INT_MIN;
+  }
+  bool bad = false;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (rm[j] >= 0) atomicAdd(p.refs + more[j], 1);
+    bad |= m >> j & 1 && (unsigned)more[j] >= (unsigned)p.n_pages;
+    if (rl[j] > 0) atomicSub(p.refs + less[j], 1);
+    bad |= rl[j] == 0;
+  }
+  if (bad) dev_error(p.status, DFLASH_DEV_PAGE);
 }
 
 // ------------------------------------------------------------------ fork
@@ -61,6 +72,8 @@ DFL_DEV int4 load_entries(const Pool& p, int row, int col, bool vec) {
   if (col + 3 < p.max_pages) v.w = at[3];
   return v;
 }
+
+DFL_DEV unsigned entries_below(int n) { return n <= 0 ? 0 : n >= 4 ? 15u : (1u << n) - 1; }  // of four
 
 // What becomes of row b: it keeps its entries (src = b), or goes on as row src.
 struct Step {
@@ -95,12 +108,7 @@ DFL_DEV void change_entries(const Pool& p, int b, int col, const Step& s, const 
   }
   if (!differ) return;
   int* at = p.table + b * p.stride + col;
-#pragma unroll 1
-  for (unsigned d = differ; d; d &= d - 1) {
-    const int j = __ffs(d) - 1;
-    if (col + j < s.has) hold(p, j == 0 ? n[0] : j == 1 ? n[1] : j == 2 ? n[2] : n[3]);
-    if (col + j < s.had) give_up(p, j == 0 ? w[0] : j == 1 ? w[1] : j == 2 ? w[2] : w[3]);
-  }
+  count_entries(p, n, differ & entries_below(s.has - col), w, differ & entries_below(s.had - col));
   if (vec && col + 4 <= p.max_pages) {
     *reinterpret_cast<int4*>(at) = make_int4(out[0], out[1], out[2], out[3]);
   } else {
@@ -478,12 +486,15 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) k_resize(const Pool p, const 
       if (i + 4 <= c.has || i >= c.had) continue;
       const int4 v = load_entries(p, b, i, tvec);
       const int id[4] = {v.x, v.y, v.z, v.w};
-      int* row = p.table + b * p.stride;
+      const unsigned lost = entries_below(c.had - i) & ~entries_below(c.has - i);
+      count_entries(p, id, 0, id, lost);
+      int* row = p.table + b * p.stride + i;
+      if (tvec && lost == 15) {
+        *reinterpret_cast<int4*>(row) = make_int4(-1, -1, -1, -1);
+      } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (i + j < c.has || i + j >= c.had) continue;
-        give_up(p, id[j]);
-        row[i + j] = -1;
+        for (int j = 0; j < 4; ++j)
+          if (lost >> j & 1) row[j] = -1;
       }
     }
   }
