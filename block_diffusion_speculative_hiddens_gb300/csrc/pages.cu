@@ -27,14 +27,9 @@ struct Pool {
 DFL_DEV int pages_of(int len, int shift) { return (int)(((unsigned)len + (1u << shift) - 1) >> shift); }
 DFL_DEV bool len_fits(const Pool& p, int len) { return len >= 0 && pages_of(len, p.shift) <= p.max_pages; }
 
-// One holder less of a page.  Whether a page is pinned does not change during a
-// call, and a page given up has a holder until then.
-DFL_DEV void give_up(const Pool& p, int id) {
-  const int r = __ldcg(p.refs + id);
-  if (r > 0) atomicSub(p.refs + id, 1);
-}
-
-// One holder more and less of each of four entries' pages, those with their bit set.
+// One holder more and less of each of four entries' pages, those with their bit
+// set.  Whether a page is pinned does not change during a call, and a page given up
+// has a holder until then.
 DFL_DEV void count_entries(const Pool& p, const int (&more)[4], unsigned m, const int (&less)[4], unsigned l) {
   int rm[4], rl[4];
 #pragma unroll
@@ -321,10 +316,11 @@ DFL_DEV void add_sharer(const Sharers& h, int page, int b) {
 struct Change {
   int had, has;    // pages; -1: the sequence stays as it is
   int page;        // its last one, where the sequence grows inside one that is shared or pinned (else -1)
-  unsigned off;    // pages taken before it
+  unsigned off;    // pages taken before it; until that is known, the count of `page`
 };
-// [16 bits: copies before it][1: a copy of `page` is made][9: positions held of the last page]
-DFL_DEV uint32_t pack_copy(int before, bool copy, int inside) { return (uint32_t)before << 16 | (uint32_t)copy << 15 | (uint32_t)inside; }
+// In a word beside it: copies before it, whether `page` is copied and whether it
+// is counted (not pinned), positions held of it.
+constexpr uint32_t COPIED = 1u << 15, COUNTED = 1u << 14, INSIDE = 0x1ff;
 
 __global__ void __launch_bounds__(SCAN_THREADS, 1) k_resize(const Pool p, const int* new_lens, int* moves, int capacity,
                                                          int ctas, int slots, bool vec, bool tvec) {
@@ -373,7 +369,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) k_resize(const Pool p, const 
       const int page = p.table[b * p.stride + c.had - 1];
       const int r = (unsigned)page < (unsigned)p.n_pages ? p.refs[page] : 0;
       if (r > 1) add_sharer(shared, page, b);
-      if (r > 1 || r < 0) c.page = page;
+      if (r > 1 || r < 0) c.page = page, c.off = (unsigned)r;
       if (r == 0 && speaks) dev_error(p.status, DFLASH_DEV_PAGE);  // none, or one that nobody holds
     }
     seq[b] = c;
@@ -387,14 +383,14 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) k_resize(const Pool p, const 
     const Change c = seq[b];
     bool copy = false;
     if (c.page >= 0) {
-      const int r = p.refs[c.page];
+      const int r = (int)c.off;
       copy = r < 0;
       if (!copy) {
         const uint32_t w = shared.who[slot_of(shared, c.page)];
         copy = (int)(w >> 16) < r || (int)(w & 0xffffu) != b;
       }
+      if (copy) copies[b] |= COPIED | (r > 0 ? COUNTED : 0);
     }
-    copies[b] |= (uint32_t)copy << 15;
     sum += (unsigned long long)max(c.has - c.had, 0) + copy + ((unsigned long long)copy << 48);
   }
   unsigned long long before = block_before(sum, sums);
@@ -405,9 +401,9 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) k_resize(const Pool p, const 
   for (int b = b0; b < b1; ++b) {
     const Change c = seq[b];
     const uint32_t w = copies[b];
-    const bool copy = w >> 15 & 1;
+    const bool copy = w & COPIED;
     seq[b].off = (unsigned)before;  // all of them fit if the call does
-    copies[b] = pack_copy((int)(before >> 48), copy, w & 0x1ff);
+    copies[b] = (uint32_t)(before >> 48) << 16 | (w & 0xffffu);
     before += (unsigned long long)max(c.has - c.had, 0) + copy + ((unsigned long long)copy << 48);
   }
 
@@ -443,13 +439,18 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) k_resize(const Pool p, const 
     const int4 r = refs_at(i);
     const int f[4] = {r.x == 0, r.y == 0, r.z == 0, r.w == 0};
     const int n = f[0] + f[1] + f[2] + f[3];
-    int place = next + warp_before(n);
-    next += warp_total(n);
-    unsigned mask = (unsigned)f[0] | (unsigned)f[1] << 1 | (unsigned)f[2] << 2 | (unsigned)f[3] << 3;
+    // the step's free pages in order, then a lane each
+    int* list = shared.page + (threadIdx.x >> 5) * 128;  // the sharers are done with
+    int at = warp_before(n);
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (f[j]) list[at++] = i + 4 * lane + j;
+    __syncwarp();
+    const int total = min(warp_total(n), (int)want - next);
 #pragma unroll 1
-    for (; mask; mask &= mask - 1, ++place) {
-      if (place >= (int)want) break;
-      const int page = i + 4 * lane + __ffs(mask) - 1;
+    for (int k = lane; k < total; k += 32) {
+      const int page = list[k], place = next + k;
       int lo = 0, hi = p.batch;  // the last sequence with off <= place: one that takes pages
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -458,49 +459,62 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) k_resize(const Pool p, const 
       }
       const Change c = seq[lo];
       const uint32_t w = copies[lo];
-      const int at = place - (int)c.off, copy = w >> 15 & 1;
+      const int nth = place - (int)c.off, copy = (w & COPIED) != 0;
       int* row = p.table + lo * p.stride;
       p.refs[page] = 1;
-      if (copy && at == 0) {
+      if (copy && nth == 0) {
         int* m = moves + 3ll * (1 + (w >> 16));
         m[0] = c.page;
         m[1] = page;
-        m[2] = w & 0x1ff;
+        m[2] = w & INSIDE;
         row[c.had - 1] = page;
-        give_up(p, c.page);
       } else {
-        row[c.had + at - copy] = page;
+        row[c.had + nth - copy] = page;
       }
     }
+    next += total;
   }
   __syncwarp();
   cluster_sync_all();  // the free pages are found, and no length is read any more
-  // what is given up, 128 entries a warp at a time, and the new lengths
+  // what is given up, 128 entries a warp at a time, the pages that were copied, and the new lengths
   if (shrinks) {
-    const int pieces = (p.max_pages + 127) >> 7;
+    const int pieces = (p.max_pages + 127) >> 7, items = p.batch * pieces;
     const int warps = ctas * SCAN_WARPS;
+    constexpr int ABREAST = 2;  // pieces of a warp with their loads on their way
 #pragma unroll 1
-    for (int it = rank * SCAN_WARPS + (threadIdx.x >> 5); it < p.batch * pieces; it += warps) {
-      const int b = it / pieces, i = ((it - b * pieces) << 7) + 4 * lane;
-      const Change c = seq[b];
-      if (i + 4 <= c.has || i >= c.had) continue;
-      const int4 v = load_entries(p, b, i, tvec);
-      const int id[4] = {v.x, v.y, v.z, v.w};
-      const unsigned lost = entries_below(c.had - i) & ~entries_below(c.has - i);
-      count_entries(p, id, 0, id, lost);
-      int* row = p.table + b * p.stride + i;
-      if (tvec && lost == 15) {
-        *reinterpret_cast<int4*>(row) = make_int4(-1, -1, -1, -1);
-      } else {
+    for (int it = rank * SCAN_WARPS + (threadIdx.x >> 5); it < items; it += ABREAST * warps) {
+      int4 v[ABREAST];
+      unsigned lost[ABREAST];
+      int* row[ABREAST];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (lost >> j & 1) row[j] = -1;
+      for (int u = 0; u < ABREAST; ++u) {
+        const int t = it + u * warps, b = t / pieces, i = ((t - b * pieces) << 7) + 4 * lane;
+        lost[u] = 0;
+        if (t >= items) continue;
+        lost[u] = entries_below(seq[b].had - i) & ~entries_below(seq[b].has - i);
+        row[u] = p.table + b * p.stride + i;
+        if (lost[u]) v[u] = load_entries(p, b, i, tvec);
+      }
+#pragma unroll
+      for (int u = 0; u < ABREAST; ++u) {
+        if (!lost[u]) continue;
+        const int id[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+        count_entries(p, id, 0, id, lost[u]);
+        if (tvec && lost[u] == 15) {
+          *reinterpret_cast<int4*>(row[u]) = make_int4(-1, -1, -1, -1);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (lost[u] >> j & 1) row[u][j] = -1;
+        }
       }
     }
   }
 #pragma unroll 1
-  for (int b = tid; b < p.batch; b += ctas * SCAN_THREADS)
+  for (int b = tid; b < p.batch; b += ctas * SCAN_THREADS) {
+    if ((copies[b] & COPIED) && (copies[b] & COUNTED)) atomicSub(p.refs + seq[b].page, 1);
     if (seq[b].had >= 0) p.lens[b] = new_lens[b];
+  }
 }
 
 // ------------------------------------------------------------------ compact
@@ -754,7 +768,7 @@ int scan_ctas(int n_pages) {
 
 // Slots of the shared pages: twice the sequences, or as many as there are at least where that does not fit.
 int resize_slots(int batch) {
-  int slots = 64;
+  int slots = SCAN_WARPS * 128 / 2;  // their memory serves the lists of free pages afterwards
   while (slots < (batch > 4096 ? batch : 2 * batch)) slots *= 2;
   return slots;
 }
