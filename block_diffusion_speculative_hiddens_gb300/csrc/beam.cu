@@ -30,6 +30,9 @@ namespace {
 #define BEAM_AHEAD 4
 #define BEAM_MINB 4
 #endif
+#ifndef BEAM_SLOTS
+#define BEAM_SLOTS 608
+#endif
 #ifndef BEAM_FEW
 #define BEAM_FEW 128
 #endif
@@ -262,15 +265,16 @@ __global__ void __launch_bounds__(SCAN_THREADS, SCAN_CTAS) k_beam_scan(const Bea
   pdl_wait();
 
   // ---- the sum and the largest logit
-  // The loads of a batch are on their way while the one before is summed.  What
-  // does not lie wholly inside the row is left to end_vector.
-  uint4 next[AHEAD];
+  // Two batches are on their way at a time.  What does not lie wholly inside the
+  // row is left to its ends.
+  uint4 even[AHEAD], odds[AHEAD];
   int k = v0 + tid;  // of the next batch
-  auto fetch = [&]() {
+  auto fetch = [&](uint4 (&v)[AHEAD]) {
 #pragma unroll
-    for (int j = 0; j < AHEAD; ++j, k += SCAN_THREADS) next[j] = k > 0 && k < end ? in.load(k) : none;
+    for (int j = 0; j < AHEAD; ++j, k += SCAN_THREADS) v[j] = k > 0 && k < end ? in.load(k) : none;
   };
-  fetch();
+  fetch(even);
+  if (batches > 1) fetch(odds);
   const float score = p.scores[row];
   const bool done = p.done && p.done[row];
   if (!(score > -INF) || score == INF || done) return;  // no logits are asked for
@@ -292,24 +296,29 @@ __global__ void __launch_bounds__(SCAN_THREADS, SCAN_CTAS) k_beam_scan(const Bea
     unpair(fma2(x2, lo2, fma2(x2, hi2, ref)), a, b);
     sum2 = add2(sum2, pair(ex2(a), ex2(b)));
   };
-  for (int b = 0, seg = 0; seg < SEGMENTS; ++seg) {
-    for (const int last = min(batches, b + seg_len); b < last; ++b) {
-      uint4 now[AHEAD];
+  int seg = 0, left = seg_len;  // batches to the segment's end
+  auto batch = [&](uint4 (&v)[AHEAD], int b) {
+    see(Vec<T>::top(v));
 #pragma unroll
-      for (int j = 0; j < AHEAD; ++j) now[j] = next[j];
-      if (b + 1 < batches) fetch();
-      see(Vec<T>::top(now));
+    for (int j = 0; j < AHEAD; ++j) {
+      float x[N];
+      Vec<T>::floats(v[j], x);
 #pragma unroll
-      for (int j = 0; j < AHEAD; ++j) {
-        float x[N];
-        Vec<T>::floats(now[j], x);
-#pragma unroll
-        for (int e = 0; e < N; e += 2) add(x[e], x[e + 1]);
-      }
+      for (int e = 0; e < N; e += 2) add(x[e], x[e + 1]);
     }
-    top_of[seg * SCAN_THREADS + tid] = top;
-    top = -INF;
+    if (b + 2 < batches) fetch(v);
+    if (--left == 0) {
+      top_of[seg++ * SCAN_THREADS + tid] = top;
+      top = -INF;
+      left = seg_len;
+    }
+  };
+#pragma unroll 1
+  for (int b = 0; b < batches; b += 2) {
+    batch(even, b);
+    if (b + 1 < batches) batch(odds, b + 1);
   }
+  for (; seg < SEGMENTS; ++seg, top = -INF) top_of[seg * SCAN_THREADS + tid] = top;
   // the row's ends, after the rest whatever its alignment
 #pragma unroll 1
   for (int i = v0 == 0 ? 0 : max(inner, v0); i < v1; i = max(inner, i + 1)) {  // three vectors at most
@@ -824,7 +833,7 @@ Plan plan_of(int batch, int beams, int vocab, int n, int dtype) {
   const int per = dtype == DFLASH_F32 ? 4 : 8, vecs = (vocab + per - 1) / per;
   const long long rows = std::max(1ll, (long long)batch * beams);
   const int least = SCAN_THREADS * AHEAD / 2;
-  long long splits = std::min<long long>(152 * SCAN_CTAS / rows, (vecs + least - 1) / least);
+  long long splits = std::min<long long>((BEAM_SLOTS) / rows, (vecs + least - 1) / least);
   splits = std::max(1ll, std::min<long long>(splits, std::min(MAX_SPLITS, MAX_LISTS / beams)));
   Plan r;
   r.part = (int)((vecs + splits - 1) / splits + SCAN_THREADS - 1) / SCAN_THREADS * SCAN_THREADS;
