@@ -13,9 +13,9 @@
 // rows with equal logits get equal sums, whatever their alignment: which thread
 // takes a logit goes by its index alone.
 //
-// Sums: exponents are taken to base 2 against an integer reference, so that the
-// parts' sums join by exact shifts; a thread's sum is a float (600 terms at most
-// between two parts' ends), its join a 64-bit fixed-point sum.
+// Sums: exponents are taken to base 2 against an integer reference, so that sums
+// join by exact shifts.  A thread's sum is two floats (of some hundred terms each),
+// a warp's and a row's a 64-bit fixed-point number.
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -26,30 +26,19 @@
 
 namespace {
 
-#ifndef BEAM_AHEAD
-#define BEAM_AHEAD 4
-#define BEAM_MINB 4
-#endif
-#ifndef BEAM_SLOTS
-#define BEAM_SLOTS 608
-#endif
-#ifndef BEAM_FEW
-#define BEAM_FEW 128
-#endif
-#ifndef BEAM_JT
-#define BEAM_JT 512
-#endif
 constexpr int SCAN_THREADS = 256;
-constexpr int SCAN_CTAS = BEAM_MINB;      // of an SM
-constexpr int AHEAD = BEAM_AHEAD;          // vectors of a thread in flight
+constexpr int SCAN_CTAS = 4;      // of an SM
+constexpr int SMS = 152;
+constexpr int AHEAD = 4;          // vectors of a thread's batch
 constexpr int SEGMENTS = 8;       // of a part, with a maximum each
 constexpr int AGAIN = 2;          // vectors of a thread that are looked at again at once
 constexpr int MAX_SPLITS = 32;    // parts of a row: a lane each when they are joined
 constexpr int MAX_LISTS = 1024;   // parts of a request's rows
-constexpr int JOIN_THREADS = BEAM_JT;
-constexpr int FEW = BEAM_FEW;         // candidates that are ranked without a bound
+constexpr int JOIN_THREADS = 512;
+constexpr int FEW = 128;          // candidates that are ranked without a bound
 constexpr int LIST_LANES = 8;     // of the join that look through a list together
-constexpr int KEEP = 640;         // keys that a selection holds: a push of one a thread, and what was kept before it
+constexpr int KEEP = 640;         // keys that a part's selection holds: a push of one a thread, and what was kept before it
+constexpr int JOIN_KEEP = 1024;   // and the join's
 
 // log2(e) in two floats: their sum is off by 2^-50.
 constexpr float LOG2E_HI = 1.44269502162933349609f;
@@ -456,6 +445,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, SCAN_CTAS) k_beam_scan(const Bea
 #pragma unroll 1
     for (int i0 = 0; i0 < count; i0 += SCAN_THREADS / lanes) {
       const int i = i0 + tid / lanes;
+      if (i0 + (tid & ~31) / lanes >= count) break;  // a warp without any
       const unsigned long long key = keys[min(i, count - 1)];
       int rank = 0;
 #pragma unroll 4
@@ -603,7 +593,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_beam_join(const BeamParams p) 
   __shared__ Cand group_head[JOIN_THREADS];
   __shared__ Cand bound_s;
   __shared__ uint16_t chosen[MAX_LISTS];
-  __shared__ Cand kept[KEEP], sorted[DFLASH_BEAM_MAX_N];
+  __shared__ Cand kept[JOIN_KEEP], sorted[DFLASH_BEAM_MAX_N];
   __shared__ int count_s, chosen_s;
 
   const int tid = threadIdx.x, lane = tid & 31, b = blockIdx.x;
@@ -691,6 +681,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_beam_join(const BeamParams p) 
 #pragma unroll 1
     for (int i0 = 0; i0 < count; i0 += JOIN_THREADS / lanes) {
       const int i = i0 + tid / lanes;
+      if (i0 + (tid & ~31) / lanes >= count) break;  // a warp without any
       const Cand c = kept[min(i, count - 1)];
       int rank = 0;
 #pragma unroll 4
@@ -791,7 +782,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_beam_join(const BeamParams p) 
         }
         const unsigned some = __ballot_sync(0xffffffffu, push);
         open = open && (some >> (lane / LIST_LANES * LIST_LANES) & ((1u << LIST_LANES) - 1)) == (1u << LIST_LANES) - 1;
-        if (count_s + JOIN_THREADS > KEEP) prune();  // the same for all: it is changed only between the barriers below
+        if (count_s + JOIN_THREADS > JOIN_KEEP) prune();  // the same for all: it is changed only between the barriers below
         __syncthreads();
         if (push && !better(least, c)) put(c);
         if (!__syncthreads_or(open)) break;
@@ -833,7 +824,7 @@ Plan plan_of(int batch, int beams, int vocab, int n, int dtype) {
   const int per = dtype == DFLASH_F32 ? 4 : 8, vecs = (vocab + per - 1) / per;
   const long long rows = std::max(1ll, (long long)batch * beams);
   const int least = SCAN_THREADS * AHEAD / 2;
-  long long splits = std::min<long long>((BEAM_SLOTS) / rows, (vecs + least - 1) / least);
+  long long splits = std::min<long long>(SMS * SCAN_CTAS / rows, (vecs + least - 1) / least);
   splits = std::max(1ll, std::min<long long>(splits, std::min(MAX_SPLITS, MAX_LISTS / beams)));
   Plan r;
   r.part = (int)((vecs + splits - 1) / splits + SCAN_THREADS - 1) / SCAN_THREADS * SCAN_THREADS;

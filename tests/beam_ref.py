@@ -185,5 +185,5 @@ def select_tolerance(score, terms):
     """A score is start + (logit - lse), and the sum of exponentials behind lse is off, relative to itself, by at most:
     the exponents' two roundings, 2 ln 2 * 2^-24 |t| with |t| <= 32 for terms that matter (what lies below adds less
     than 2^-31 a term); the exponential's 2^-22; `terms` additions of a thread in two accumulators, 2^-24 each; the
-    joins' 2^-27.  Then one rounding of the score to 32 bits."""
-    return 2 * 0.6932 * 32 * 2.0 ** -24 + 2.0 ** -22 + (terms / 2 + 1) * 2.0 ** -24 + 2.0 ** -27 + 2.0 ** -24 * abs(score)
+    joins' 2^-27 and the logarithm's 2^-27.  Then one rounding of the score to 32 bits."""
+    return 2 * 0.6932 * 32 * 2.0 ** -24 + 2.0 ** -22 + (terms / 2 + 1) * 2.0 ** -24 + 2.0 ** -26 + 2.0 ** -24 * abs(score)
