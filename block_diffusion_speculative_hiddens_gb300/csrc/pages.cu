@@ -519,8 +519,44 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) k_resize(const Pool p, const 
 
 // ------------------------------------------------------------------ compact
 
+// REMAP_EACH entries of a row, `width` apart, to their pages' new places.
+constexpr int REMAP_THREADS = 256;
+constexpr int REMAP_EACH = 4;
+constexpr int REMAP_PIECES = 2;  // of a warp of the scanning cluster, at most
+
+DFL_DEV void remap_entries(const Pool& p, const int* remap, int b, int i0, int width) {
+  const int len = p.lens[b];
+  if (!len_fits(p, len)) {
+    if (i0 == 0) dev_error(p.status, DFLASH_DEV_ARG);
+    return;
+  }
+  const int held = pages_of(len, p.shift);
+  int* row = p.table + b * p.stride;
+  int id[REMAP_EACH], to[REMAP_EACH];
+#pragma unroll
+  for (int j = 0; j < REMAP_EACH; ++j) id[j] = i0 + j * width < held ? row[i0 + j * width] : 0;
+#pragma unroll
+  for (int j = 0; j < REMAP_EACH; ++j) {
+    to[j] = id[j];  // what lies past the held ones stays
+    if (i0 + j * width < held) to[j] = (unsigned)id[j] < (unsigned)p.n_pages ? __ldcg(remap + id[j]) : -1;
+  }
+#pragma unroll
+  for (int j = 0; j < REMAP_EACH; ++j) {
+    if (to[j] < 0) dev_error(p.status, DFLASH_DEV_PAGE);  // outside the pool, or held and yet free: left as it is
+    else if (to[j] != id[j]) row[i0 + j * width] = to[j];
+  }
+}
+
+__global__ void __launch_bounds__(REMAP_THREADS) k_remap(const Pool p, const int* remap, int blocks_per_row) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int b = blockIdx.x / blocks_per_row, part = blockIdx.x - b * blocks_per_row;
+  remap_entries(p, remap, b, part * REMAP_THREADS * REMAP_EACH + threadIdx.x, REMAP_THREADS);
+}
+
+// with_table: the table is small enough for the cluster to go through it too.
 __global__ void __launch_bounds__(SCAN_THREADS, 1) k_compact(const Pool p, int* moves, int capacity, int* remap, int ctas,
-                                                          bool vec) {
+                                                          bool vec, bool with_table) {
   __shared__ int free_counts[SCAN_WARPS + 1], held_counts[SCAN_WARPS + 1], low[SCAN_WARPS + 1];
   const int rank = ctas > 1 ? (int)cluster_ctarank() : 0;
   const int lane = threadIdx.x & 31;
@@ -595,39 +631,14 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) k_compact(const Pool p, int* 
       m[2] = 0;
     }
   }
-}
-
-constexpr int REMAP_THREADS = 256;
-constexpr int REMAP_EACH = 4;  // entries of a thread, a block's width apart
-
-__global__ void __launch_bounds__(REMAP_THREADS) k_remap(const Pool p, const int* remap, int blocks_per_row) {
-  pdl_launch_dependents();
-  pdl_wait();
-  const int b = blockIdx.x / blocks_per_row, part = blockIdx.x - b * blocks_per_row;
-  const int len = p.lens[b];
-  if (!len_fits(p, len)) {
-    if (part == 0 && threadIdx.x == 0) dev_error(p.status, DFLASH_DEV_ARG);
-    return;
-  }
-  const int held = pages_of(len, p.shift);
-  int* row = p.table + b * p.stride;
-  const int i0 = part * REMAP_THREADS * REMAP_EACH + threadIdx.x;
-  int id[REMAP_EACH];
-#pragma unroll
-  for (int j = 0; j < REMAP_EACH; ++j) {
-    const int i = i0 + j * REMAP_THREADS;
-    id[j] = i < held ? row[i] : -2;
-  }
-#pragma unroll
-  for (int j = 0; j < REMAP_EACH; ++j) {
-    if (id[j] == -2 && i0 + j * REMAP_THREADS >= held) continue;
-    if ((unsigned)id[j] >= (unsigned)p.n_pages) {
-      dev_error(p.status, DFLASH_DEV_PAGE);
-      continue;
-    }
-    const int to = remap[id[j]];
-    if (to < 0) dev_error(p.status, DFLASH_DEV_PAGE);  // held, and yet free: left as it is
-    else if (to != id[j]) row[i0 + j * REMAP_THREADS] = to;
+  if (!with_table) return;
+  __syncwarp();
+  cluster_sync_all();  // remap is whole
+  const int per_row = (p.max_pages + 32 * REMAP_EACH - 1) / (32 * REMAP_EACH);  // pieces, a warp each
+#pragma unroll 1
+  for (int it = tid >> 5; it < per_row * p.batch; it += threads >> 5) {
+    const int b = it / per_row;
+    remap_entries(p, remap, b, (it - b * per_row) * 32 * REMAP_EACH + lane, 32);
   }
 }
 
@@ -834,15 +845,20 @@ int dflash_pages_compact(const dflash_page_pool* c, int32_t* moves, int32_t capa
   const PoolParts w = pool_parts(c);
   if (!apart({w.refs, w.table, w.status, strided_ints(moves, 3 + 3ll * capacity), strided_ints(remap, c->n_pages)}, {w.lens}))
     return DFLASH_ERR_INVALID_ARG;
-  DeviceGuard guard(c->device);
-  if (!guard.ok) return DFLASH_ERR_CUDA;
-  const int ctas = scan_ctas(c->n_pages);
-  if (int e = launch(k_compact, dim3((unsigned)ctas), SCAN_THREADS, 0, ctas, stream, pool_of(c), moves, capacity, remap, ctas,
-                     (reinterpret_cast<uintptr_t>(c->refs) & 15) == 0))
-    return e;
   const int per_row = (c->max_pages + REMAP_THREADS * REMAP_EACH - 1) / (REMAP_THREADS * REMAP_EACH);
   const long long blocks = (long long)per_row * c->batch;
   if (blocks > 0x7fffffffll) return DFLASH_ERR_CAPACITY;
+  DeviceGuard guard(c->device);
+  if (!guard.ok) return DFLASH_ERR_CUDA;
+  // A table of some pieces a warp is gone through by the same cluster; a larger one
+  // by a grid of its own, which takes a launch more and has all SMs.
+  const long long pieces = (long long)((c->max_pages + 32 * REMAP_EACH - 1) / (32 * REMAP_EACH)) * c->batch;
+  const int ctas = scan_ctas((int)std::min<long long>(DFLASH_POOL_MAX_PAGES, std::max<long long>(c->n_pages, pieces * 128)));
+  const bool with_table = pieces <= REMAP_PIECES * SCAN_WARPS * ctas;
+  if (int e = launch(k_compact, dim3((unsigned)ctas), SCAN_THREADS, 0, ctas, stream, pool_of(c), moves, capacity, remap, ctas,
+                     (reinterpret_cast<uintptr_t>(c->refs) & 15) == 0, with_table))
+    return e;
+  if (with_table) return DFLASH_OK;
   return launch(k_remap, dim3((unsigned)blocks), REMAP_THREADS, 0, 1, stream, pool_of(c), remap, per_row);
 }
 

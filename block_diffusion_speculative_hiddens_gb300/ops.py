@@ -24,7 +24,7 @@ Which sequence holds which page, around a step of the whole model:
 and of a beam search, whose sequences go on from one another:
 
     scores, parents, tokens = beam_select(logits, scores)
-    fork(pool, parents)
+    fork(pool, parents.view(-1))
 
 The C entry points, their argument structs, limits and device-side checks are
 in include/dflash.h; this module checks the tensors (ValueError) and passes
@@ -558,43 +558,49 @@ def beam_select(logits, scores, n: int = None, *, done=None, done_token: int = 0
     three, contiguous; scores itself may be the first if n is the number of beams.
     status: an int32 word for DEV_NAN, such as a cache's or pool's `status`.
     workspace: uint8, beam_workspace() bytes; by default allocated for the call."""
-    device = logits.get_device()
-    if logits.dtype not in _LOGITS or device < 0 or len(logits.shape) != 2 or logits.stride(1) != 1:
+    device, kind, shape = logits.get_device(), _LOGITS.get(logits.dtype), scores.shape
+    if kind is None or device < 0 or logits.dim() != 2 or logits.stride(1) != 1:
         raise ValueError(f"logits: expected float16, bfloat16 or float32 [batch * beams, vocab] with contiguous rows on a "
                          f"CUDA device, got {list(logits.shape)} {logits.dtype} on {logits.device}")
+    rows, vocab = logits.shape
+    if scores.dtype is not torch.float32 or scores.get_device() != device or len(shape) != 2 or \
+            shape[0] * shape[1] != rows or not scores.is_contiguous():
+        raise ValueError(f"scores: expected contiguous float32 [batch, beams], {rows} values, on cuda:{device}, got "
+                         f"{list(shape)} {scores.dtype} on {scores.device}")
     if _graded(logits) or _graded(scores):
         _no_gradient("logits" if _graded(logits) else "scores")
     raw = _raw_stream(stream, device)
-    rows, vocab = logits.shape
-    if scores.dtype is not torch.float32 or scores.get_device() != device or len(scores.shape) != 2 or \
-            scores.shape[0] * scores.shape[1] != rows or not scores.is_contiguous():
-        raise ValueError(f"scores: expected contiguous float32 [batch, beams], {rows} values, on cuda:{device}, got "
-                         f"{list(scores.shape)} {scores.dtype} on {scores.device}")
-    batch, beams = scores.shape
+    batch, beams = shape
     n = beams if n is None else _int32(n, "n")
-    if done is not None and (done.dtype not in (torch.bool, torch.uint8) or done.get_device() != device or
-                             done.shape != scores.shape or not done.is_contiguous()):
-        raise ValueError(f"done: expected contiguous bool {[batch, beams]} on cuda:{device}, got {list(done.shape)} "
-                         f"{done.dtype} on {done.device}")
-    if status is not None and (status.dtype is not torch.int32 or status.get_device() != device or status.numel() < 1):
-        raise ValueError(f"status: expected an int32 word on cuda:{device}, got {status.dtype} on {status.device}")
+    ended = 0
+    if done is not None:
+        if done.dtype not in (torch.bool, torch.uint8) or done.get_device() != device or done.shape != shape or \
+                not done.is_contiguous():
+            raise ValueError(f"done: expected contiguous bool {[batch, beams]} on cuda:{device}, got {list(done.shape)} "
+                             f"{done.dtype} on {done.device}")
+        ended = done.data_ptr()
+    word = 0
+    if status is not None:
+        if status.dtype is not torch.int32 or status.get_device() != device or status.numel() < 1:
+            raise ValueError(f"status: expected an int32 word on cuda:{device}, got {status.dtype} on {status.device}")
+        word = status.data_ptr()
     if out is None:
         if n < 1:
             raise ValueError(f"n: expected at least 1, got {n}")
-        shape = batch, n
-        out = (_empty(shape, torch.float32, logits, stream), _empty(shape, torch.int32, logits, stream),
-               _empty(shape, torch.int32, logits, stream))
+        out = (_empty((batch, n), torch.float32, logits, stream), _empty((batch, n), torch.int32, logits, stream),
+               _empty((batch, n), torch.int32, logits, stream))
     else:
+        out = tuple(out)
         for what, t, dtype in zip(("scores", "parents", "tokens"), out, (torch.float32, torch.int32, torch.int32)):
             if t.dtype is not dtype or t.get_device() != device or tuple(t.shape) != (batch, n) or not t.is_contiguous():
                 raise ValueError(f"out: expected contiguous {dtype} {[batch, n]} on cuda:{device} for {what}, got "
                                  f"{list(t.shape)} {t.dtype} on {t.device}")
             if _graded(t):
                 _no_gradient("out")
-        out = tuple(out)
+    best, parents, tokens = out
     lib = load()
     if workspace is None:
-        nbytes = lib.dflash_beam_select_workspace(batch, beams, vocab, n, _LOGITS[logits.dtype])
+        nbytes = lib.dflash_beam_select_workspace(batch, beams, vocab, n, kind)
         if nbytes:
             workspace = _empty(nbytes, torch.uint8, logits, stream)
     elif workspace.dtype is not torch.uint8 or workspace.get_device() != device or not workspace.is_contiguous():
@@ -602,10 +608,9 @@ def beam_select(logits, scores, n: int = None, *, done=None, done_token: int = 0
                          f"{workspace.device}")
     else:
         nbytes = workspace.numel()
-    args = _BEAM.pack(logits.data_ptr(), logits.stride(0), scores.data_ptr(), 0 if done is None else done.data_ptr(),
-                      out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(),
-                      0 if status is None else status.data_ptr(), 0 if workspace is None else workspace.data_ptr(), nbytes,
-                      batch, beams, vocab, n, _int32(done_token, "done_token"), _LOGITS[logits.dtype], device, 0)
+    args = _BEAM.pack(logits.data_ptr(), logits.stride(0), scores.data_ptr(), ended, best.data_ptr(), parents.data_ptr(),
+                      tokens.data_ptr(), word, 0 if workspace is None else workspace.data_ptr(), nbytes, batch, beams, vocab, n,
+                      _int32(done_token, "done_token"), kind, device, 0)
     code = lib.dflash_beam_select(args, raw)
     if code:
         raise DflashError("dflash_beam_select", code)

@@ -657,7 +657,9 @@ DFLASH_API int dflash_pages_fork(const dflash_page_pool* pool, const int32_t* pa
  * follow; moves gets the copies (all positions), remap (DEVICE int32 [n_pages])
  * each old page's new place, its own where it stayed, -1 where it was free: for
  * page numbers that the caller keeps elsewhere.  Run dflash_pages_copy before the
- * cache is used again.  capacity >= n_pages / 2, else DFLASH_ERR_CAPACITY. */
+ * cache is used again.  A sequence whose length does not fit its table row keeps its
+ * entries and sets DFLASH_DEV_ARG; so does, with DFLASH_DEV_PAGE, a held entry that is
+ * outside the pool or whose page is free.  capacity >= n_pages / 2, else DFLASH_ERR_CAPACITY. */
 DFLASH_API int dflash_pages_compact(const dflash_page_pool* pool, int32_t* moves, int32_t capacity, int32_t* remap,
                                     void* stream);
 
