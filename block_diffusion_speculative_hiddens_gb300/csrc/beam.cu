@@ -1,12 +1,12 @@
 // The next beams of a search: the n best of beams * vocab continuations a
 // request, scored by the running score and the logarithm of the softmax.
 //
-// One pass over the logits, a part of a row a CTA: each thread sums
-// exp(logit - reference) and keeps its maximum.  The n-th largest of the CTA's
-// thread maxima bounds its n-th largest logit from below, and only the n threads
-// whose maximum reaches it can hold one of the n: their logits are read again
-// (from L2) and the n best kept, sorted.  A second kernel, a CTA a request, joins
-// the parts' sums and chooses among their lists in the same way, by score.
+// One pass over the logits, a part of a row a CTA: the sum of exp(logit -
+// reference), and the largest logit of each cell, some tens of vectors that a
+// thread or four neighbours take.  A second kernel, a CTA a request, joins the
+// parts' sums to each beam's logarithm.  The n-th largest of some groups' cells, by
+// score, bounds the n-th best continuation from below; only cells that reach the
+// bound can hold one, hardly more than n, and their logits alone are read again.
 //
 // The order within a row is the logits' own, so equal logits tie exactly.  Between
 // rows the scores are compared in 64 bits; the sums behind them are kept so that
@@ -26,19 +26,20 @@
 
 namespace {
 
+#ifndef BEAM_SLOTS
+#define BEAM_SLOTS 608
+#endif
 constexpr int SCAN_THREADS = 256;
 constexpr int SCAN_CTAS = 4;      // of an SM
-constexpr int SMS = 152;
 constexpr int AHEAD = 4;          // vectors of a thread's batch
-constexpr int SEGMENTS = 8;       // of a part, with a maximum each
-constexpr int AGAIN = 2;          // vectors of a thread that are looked at again at once
+constexpr int MAX_SEGMENTS = 8;   // of a part, with cells of their own
 constexpr int MAX_SPLITS = 32;    // parts of a row: a lane each when they are joined
-constexpr int MAX_LISTS = 1024;   // parts of a request's rows
 constexpr int JOIN_THREADS = 512;
-constexpr int FEW = 128;          // candidates that are ranked without a bound
-constexpr int LIST_LANES = 8;     // of the join that look through a list together
-constexpr int KEEP = 640;         // keys that a part's selection holds: a push of one a thread, and what was kept before it
-constexpr int JOIN_KEEP = 1024;   // and the join's
+constexpr int AGAIN = 2;          // vectors of a thread that are looked at again at once
+constexpr int CELL_LOADS = 6;     // of a thread of the join: four cells each, held in registers
+constexpr int CELLS = 4 * CELL_LOADS * JOIN_THREADS;  // of a request
+constexpr int CHOSEN = 4 * JOIN_THREADS;  // cells that are looked into at a time: a load of every thread, at least
+constexpr int KEEP = 1024;        // candidates that are kept at a time
 
 // log2(e) in two floats: their sum is off by 2^-50.
 constexpr float LOG2E_HI = 1.44269502162933349609f;
@@ -67,9 +68,11 @@ struct BeamParams {
   int* tokens;
   uint32_t* status;
   PartSum* sums;             // [rows][splits]
-  unsigned long long* best;  // [rows][splits][n] keys
-  int batch, beams, vocab, n, splits, part;  // part: vectors of a split
-  int done_token;
+  float* cells;              // [rows][splits][segments][SCAN_THREADS / quad] largest logits
+  int batch, beams, vocab, n, done_token;
+  int splits, part;          // parts of a row, vectors of one
+  int segments, seg_len;     // of a part; batches of one
+  int quad, quad_log;        // threads of a cell: a power of two up to 32
 };
 
 DFL_DEV void flag_nan(uint32_t* status) {
@@ -213,19 +216,8 @@ struct Row {
   DFL_DEV float at(int token) const { return Vec<T>::one(data + (long long)token * Vec<T>::SIZE); }
 };
 
-// Groups whose maxima bound the n-th largest: enough for about n to 1.4 n values
-// to reach the bound (G ln(G / (G - n)) of independent ones), no more, since each
-// group is compared with all.
-DFL_DEV int groups_for(int n) { return n <= 24 ? 64 : n <= 64 ? 128 : 256; }
-
 DFL_DEV float pow2_or_0(float e) {  // 2^e for whole e <= 0, 0 where it is too small to matter
   return e < -120.0f ? 0.0f : __uint_as_float((uint32_t)(127 + (int)e) << 23);
-}
-
-// Lanes that rank one of `count` values together: a power of two, up to a warp.
-DFL_DEV int rank_lanes(int threads, int count) {
-  const int per = threads / max(count, 1);
-  return per < 2 ? 1 : min(32, 1 << (31 - __clz(per)));
 }
 
 template <int T, bool ALIGNED>
@@ -234,26 +226,22 @@ __global__ void __launch_bounds__(SCAN_THREADS, SCAN_CTAS) k_beam_scan(const Bea
   constexpr int WARPS = SCAN_THREADS / 32;
   constexpr int BATCH = AHEAD * SCAN_THREADS;  // vectors of AHEAD rounds; a round is a vector a thread
   const float INF = __uint_as_float(0x7f800000u);
-  __shared__ float top_of[SEGMENTS * SCAN_THREADS];  // threads' largest logits in a part's segments
-  __shared__ float group_top[SCAN_THREADS];
+  __shared__ uint32_t cell[MAX_SEGMENTS * SCAN_THREADS];  // the part's, in order
   __shared__ float warp_top[WARPS], warp_q[WARPS];
   __shared__ unsigned long long warp_sum[WARPS];
-  __shared__ float bound_s;
-  __shared__ uint16_t chosen[SEGMENTS * SCAN_THREADS];  // those that hold candidates
-  __shared__ unsigned long long keys[KEEP], sorted[DFLASH_BEAM_MAX_N];
-  __shared__ int count_s, chosen_s;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int row = blockIdx.x / p.splits, part = blockIdx.x - row * p.splits;
   const Row<T, ALIGNED> in = {p.logits + row * p.row_bytes, p.vocab};
   const int vecs = (p.vocab + N - 1) / N, inner = in.inner();
   const int v0 = part * p.part, v1 = min(vecs, v0 + p.part), end = min(v1, inner);
-  const int batches = (v1 - v0 + BATCH - 1) / BATCH, seg_len = (batches + SEGMENTS - 1) / SEGMENTS;
+  const int batches = (v1 - v0 + BATCH - 1) / BATCH;
+  const int wide = SCAN_THREADS >> p.quad_log;  // cells of a segment
   const uint4 none = make_uint4(Vec<T>::NONE, Vec<T>::NONE, Vec<T>::NONE, Vec<T>::NONE);
   pdl_launch_dependents();
   pdl_wait();
 
-  // ---- the sum and the largest logit
+  // ---- the sum and the largest logits
   // Two batches are on their way at a time.  What does not lie wholly inside the
   // row is left to its ends.
   uint4 even[AHEAD], odds[AHEAD];
@@ -267,7 +255,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, SCAN_CTAS) k_beam_scan(const Bea
   const float score = p.scores[row];
   const bool done = p.done && p.done[row];
   if (!(score > -INF) || score == INF || done) return;  // no logits are asked for
-  float top = -INF, q = -1e30f;
+  float top = -INF, whole = -INF, q = -1e30f;  // of the segment, of all
   Pair sum2 = pair(0.0f, 0.0f);
   const Pair hi2 = pair(LOG2E_HI, LOG2E_HI), lo2 = pair(LOG2E_LO, LOG2E_LO);
   auto see = [&](float m) {  // a maximum, before its terms
@@ -285,7 +273,14 @@ __global__ void __launch_bounds__(SCAN_THREADS, SCAN_CTAS) k_beam_scan(const Bea
     unpair(fma2(x2, lo2, fma2(x2, hi2, ref)), a, b);
     sum2 = add2(sum2, pair(ex2(a), ex2(b)));
   };
-  int seg = 0, left = seg_len;  // batches to the segment's end
+  auto close = [&](int seg) {  // the segment's cells
+    whole = fmaxf(whole, top);
+    float m = top;
+    for (int d = 1; d < p.quad; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if ((tid & (p.quad - 1)) == 0) cell[seg * wide + (tid >> p.quad_log)] = ordered(m);
+    top = -INF;
+  };
+  int seg = 0, left = p.seg_len;  // batches to the segment's end
   auto batch = [&](uint4 (&v)[AHEAD], int b) {
     see(Vec<T>::top(v));
 #pragma unroll
@@ -296,70 +291,55 @@ __global__ void __launch_bounds__(SCAN_THREADS, SCAN_CTAS) k_beam_scan(const Bea
       for (int e = 0; e < N; e += 2) add(x[e], x[e + 1]);
     }
     if (b + 2 < batches) fetch(v);
-    if (--left == 0) {
-      top_of[seg++ * SCAN_THREADS + tid] = top;
-      top = -INF;
-      left = seg_len;
-    }
   };
 #pragma unroll 1
   for (int b = 0; b < batches; b += 2) {
     batch(even, b);
-    if (b + 1 < batches) batch(odds, b + 1);
+    if (--left == 0) close(seg++), left = p.seg_len;
+    if (b + 1 >= batches) break;
+    batch(odds, b + 1);
+    if (--left == 0) close(seg++), left = p.seg_len;
   }
-  for (; seg < SEGMENTS; ++seg, top = -INF) top_of[seg * SCAN_THREADS + tid] = top;
+#pragma unroll 1
+  for (; seg < p.segments; ++seg) close(seg);
+  __syncwarp();  // a cell is a warp's
   // the row's ends, after the rest whatever its alignment
 #pragma unroll 1
   for (int i = v0 == 0 ? 0 : max(inner, v0); i < v1; i = max(inner, i + 1)) {  // three vectors at most
     if ((i - v0) % SCAN_THREADS != tid) continue;
-    float x[N], m0 = -INF;
+    float x[N], m = -INF;
 #pragma unroll
     for (int e = 0; e < N; ++e) x[e] = i * N + e < p.vocab ? in.at(i * N + e) : -INF;
 #pragma unroll
-    for (int e = 0; e < N; ++e) m0 = fmaxf(m0, x[e]);
-    top = -INF;
-    see(m0);
+    for (int e = 0; e < N; ++e) m = fmaxf(m, x[e]);
+    see(m);
 #pragma unroll
     for (int e = 0; e < N; e += 2) add(x[e], x[e + 1]);
-    float& m = top_of[(i - v0) / (seg_len * BATCH) * SCAN_THREADS + tid];
-    m = fmaxf(m, top);
+    whole = fmaxf(whole, m);
+    atomicMax(&cell[(i - v0) / (p.seg_len * BATCH) * wide + (tid >> p.quad_log)], ordered(m));
   }
 
-  // ---- joined over the block: the sum, and the group maxima
-  const int G = groups_for(p.n), per = SCAN_THREADS / G;  // threads of a group: 4, 2, 1
-  const int g = tid / per;
-  auto tops = [&]() {  // a thread's, then its group's and warp's
-    top = top_of[tid];
+  // ---- joined over the block
+  auto warp_max = [&](float m) {
 #pragma unroll
-    for (int i = 1; i < SEGMENTS; ++i) top = fmaxf(top, top_of[i * SCAN_THREADS + tid]);
-    float m = top;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      if (d == per && tid % per == 0) group_top[g] = m;
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    }
-    if (lane == 0) warp_top[warp] = m;
+    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    return m;
   };
-  tops();
-  float s;
-  {
-    float s1;
-    unpair(sum2, s, s1);
-    s += s1;
-  }
-  float most = s > 0.0f ? q : -1e30f;
-#pragma unroll
-  for (int d = 16; d; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
   auto fixed_sum = [&](float v) {
     unsigned long long f = __float2ull_rn(v * (float)(1ull << FIX));
 #pragma unroll
     for (int d = 16; d; d >>= 1) f += __shfl_xor_sync(0xffffffffu, f, d);
-    if (lane == 0) warp_sum[warp] = f;
+    return f;
   };
+  float s, s1;
+  unpair(sum2, s, s1);
+  s += s1;
   const bool odd = !(s < 1e37f);
-  fixed_sum(odd ? 0.0f : s * pow2_or_0(q - most));
-  if (lane == 0) warp_q[warp] = most;
-  if (tid == 0) count_s = chosen_s = 0;
+  {
+    const float most = warp_max(s > 0.0f ? q : -1e30f), m = warp_max(whole);
+    const unsigned long long f = fixed_sum(odd ? 0.0f : s * pow2_or_0(q - most));
+    if (lane == 0) warp_top[warp] = m, warp_q[warp] = most, warp_sum[warp] = f;
+  }
   const bool any_odd = __syncthreads_or(odd);
   float part_top = warp_top[0], part_q = warp_q[0];
 #pragma unroll
@@ -385,147 +365,45 @@ __global__ void __launch_bounds__(SCAN_THREADS, SCAN_CTAS) k_beam_scan(const Bea
       }
     };
     bool bad = false;
+    whole = -INF;
+    __syncthreads();  // the maxima are read
 #pragma unroll 1
-    for (int i = 0; i < SEGMENTS; ++i) {
-      float m = -INF;
-      each(i * seg_len * AHEAD, (i + 1) * seg_len * AHEAD, [&](float x) {
+    for (int i = 0; i < p.segments; ++i) {
+      top = -INF;
+      each(i * p.seg_len * AHEAD, (i + 1) * p.seg_len * AHEAD, [&](float x) {
         bad |= !(x <= FLT_MAX);
-        m = fmaxf(m, clean(x));
+        top = fmaxf(top, clean(x));
       });
-      top_of[i * SCAN_THREADS + tid] = m;
+      __syncwarp();
+      close(i);
     }
     if (bad) flag_nan(p.status);
-    __syncthreads();
-    tops();
+    whole = warp_max(whole);
+    if (lane == 0) warp_top[warp] = whole, warp_q[warp] = 0.0f;
     __syncthreads();
     part_top = warp_top[0];
 #pragma unroll
     for (int w = 1; w < WARPS; ++w) part_top = fmaxf(part_top, warp_top[w]);
+    part_q = 0.0f;
     s = 0.0f;
     if (part_top > -INF) each(0, batches * AHEAD, [&](float x) { s += expf(clean(x) - part_top); });
-    if (lane == 0) warp_q[warp] = 0.0f;
-    part_q = 0.0f;
-    fixed_sum(s);
+    __syncwarp();
+    const unsigned long long f = fixed_sum(s);
+    if (lane == 0) warp_sum[warp] = f;
     __syncthreads();
   }
-
-  // ---- a bound below n of the part's logits: the n-th largest group maximum
-  {
-    const float mine = group_top[g];
-    int above = 0;
-#pragma unroll 8
-    for (int u = tid % per; u < G; u += per) {
-      const float o = group_top[u];
-      above += (o > mine) | ((o == mine) & (u < g));
-    }
-    if (per >= 2) above += __shfl_xor_sync(0xffffffffu, above, 1);
-    if (per >= 4) above += __shfl_xor_sync(0xffffffffu, above, 2);
-    if (above == p.n - 1) bound_s = mine;  // of one group
-  }
+  const long long at = row * p.splits + part;
   if (tid == 0) {
     unsigned long long sum = 0;
 #pragma unroll
     for (int w = 0; w < WARPS; ++w)
       if (part_q - warp_q[w] < 63.0f) sum += warp_sum[w] >> (int)(part_q - warp_q[w]);
     const PartSum r = {sum, part_q, part_top, plain, 0};
-    p.sums[row * p.splits + part] = r;
+    p.sums[at] = r;
   }
-  __syncthreads();
-  const float bound = fmaxf(bound_s, -FLT_MAX);  // -inf: no token
-
-  // ---- the threads' segments that can hold one of the n, and their logits again
-  if (top >= bound)
-    for (int i = 0; i < SEGMENTS; ++i)
-      if (top_of[i * SCAN_THREADS + tid] >= bound) chosen[atomicAdd(&chosen_s, 1)] = (uint16_t)(i * SCAN_THREADS + tid);
-  __syncthreads();
-  const int n_chosen = chosen_s;
-  unsigned long long least = (unsigned long long)ordered(bound) << 32;  // keys at or below are not wanted
-  auto ranked = [&](int count, auto&& f) {  // every key with its rank
-    const int lanes = rank_lanes(SCAN_THREADS, count), at = tid & (lanes - 1);
+  float* cells = p.cells + at * (p.segments * wide);
 #pragma unroll 1
-    for (int i0 = 0; i0 < count; i0 += SCAN_THREADS / lanes) {
-      const int i = i0 + tid / lanes;
-      if (i0 + (tid & ~31) / lanes >= count) break;  // a warp without any
-      const unsigned long long key = keys[min(i, count - 1)];
-      int rank = 0;
-#pragma unroll 4
-      for (int j = at; j < count; j += lanes) rank += keys[j] > key;
-      for (int d = lanes >> 1; d; d >>= 1) rank += __shfl_xor_sync(0xffffffffu, rank, d);
-      if (at == 0 && i < count && rank < p.n) f(key, rank);
-    }
-  };
-  auto prune = [&]() {  // to the n largest keys
-    const int count = count_s;
-    ranked(count, [&](unsigned long long key, int rank) { sorted[rank] = key; });
-    __syncthreads();
-    const int kept = min(count, p.n);
-    for (int i = tid; i < kept; i += SCAN_THREADS) keys[i] = sorted[i];
-    if (kept == p.n) least = max(least, sorted[p.n - 1]);
-    if (tid == 0) count_s = kept;
-    __syncthreads();
-  };
-  const int rounds = seg_len * AHEAD, items = rounds * n_chosen;  // rounds of a segment
-#pragma unroll 1
-  for (int i0 = 0; i0 < items; i0 += AGAIN * SCAN_THREADS) {
-    int token[AGAIN];
-    unsigned wanted = 0;  // of their tokens
-    uint4 v[AGAIN];
-    bool whole[AGAIN];
-#pragma unroll
-    for (int j = 0; j < AGAIN; ++j) {
-      const int it = i0 + j * SCAN_THREADS + tid, r = it / n_chosen;
-      token[j] = 0;
-      whole[j] = false;
-      if (it >= items) continue;
-      const int c = chosen[it - r * n_chosen];
-      const int i = v0 + (c / SCAN_THREADS * rounds + r) * SCAN_THREADS + c % SCAN_THREADS;
-      token[j] = i * N;
-      whole[j] = i > 0 && i < end;
-      if (whole[j]) v[j] = in.load(i);
-      else if (i < v1) wanted |= ((1u << min(N, p.vocab - token[j])) - 1) << j * N;
-    }
-#pragma unroll
-    for (int j = 0; j < AGAIN; ++j) {
-      if (!whole[j]) continue;
-      float x[N];
-      Vec<T>::floats(v[j], x);
-#pragma unroll
-      for (int e = 0; e < N; ++e) wanted |= (x[e] >= bound) << (j * N + e);
-    }
-    auto visit = [&](unsigned w, auto&& push) {
-#pragma unroll 1
-      for (; w; w &= w - 1) {
-        const int bit = __ffs(w) - 1, t = (AGAIN > 1 && bit >= N ? token[AGAIN - 1] : token[0]) + bit % N;
-        const float x = in.at(t);
-        const unsigned long long key = (unsigned long long)ordered(x) << 32 | (0xffffffffu - (uint32_t)t);
-        if (x >= bound && x <= FLT_MAX && key > least) push(key);
-      }
-    };
-    const int before = count_s;
-    __syncthreads();
-    bool full = false;
-    visit(wanted, [&](unsigned long long key) {
-      const int o = atomicAdd(&count_s, 1);
-      if (o < KEEP) keys[o] = key;
-      else full = true;
-    });
-    if (__syncthreads_or(full)) {  // too many at once: again from `before`, in turns of one a thread
-      if (tid == 0) count_s = before;
-      __syncthreads();
-#pragma unroll 1
-      for (int e = 0; e < AGAIN * N; ++e) {
-        if (count_s + SCAN_THREADS > KEEP) prune();  // leaves at most DFLASH_BEAM_MAX_N
-        __syncthreads();
-        visit(wanted & 1u << e, [&](unsigned long long key) { keys[atomicAdd(&count_s, 1)] = key; });
-        __syncthreads();
-      }
-    }
-  }
-  // the n best, sorted
-  unsigned long long* best = p.best + (long long)(row * p.splits + part) * p.n;
-  const int count = count_s;
-  ranked(count, [&](unsigned long long key, int rank) { best[rank] = key; });
-  for (int i = count + tid; i < p.n; i += SCAN_THREADS) best[i] = 0;
+  for (int i = tid; i < p.segments * wide; i += SCAN_THREADS) cells[i] = unordered(cell[i]);
 }
 
 // ------------------------------------------------------------------ the join
@@ -581,48 +459,47 @@ __device__ __noinline__ unsigned long long sum_of_any(const PartSum& part, bool 
   return some ? (unsigned long long)((double)part.sum * exp(mine - r)) : 0;
 }
 
+// Groups whose best bound the n-th best: enough for about n to 1.4 n values to
+// reach the bound (G ln(G / (G - n)) of independent ones), no more, since each
+// group is compared with all.
+DFL_DEV int groups_for(int n) { return n <= 24 ? 64 : n <= 64 ? 128 : 256; }
+
+// Lanes that rank one of `count` values together: a power of two, up to a warp.
+DFL_DEV int rank_lanes(int count) {
+  const int per = JOIN_THREADS / max(count, 1);
+  return per < 2 ? 1 : min(32, 1 << (31 - __clz(per)));
+}
+
+template <int T, bool ALIGNED>
 __global__ void __launch_bounds__(JOIN_THREADS) k_beam_join(const BeamParams p) {
-  constexpr int PER = MAX_LISTS / JOIN_THREADS;  // lists of a thread
+  constexpr int N = Vec<T>::N;
   const float INF = __uint_as_float(0x7f800000u);
   enum { DEAD, RUNS, ENDED };
   __shared__ double base[DFLASH_BEAM_MAX], ref[DFLASH_BEAM_MAX];  // score = base + (logit - ref)
-  __shared__ unsigned long long sum_of[DFLASH_BEAM_MAX];
   __shared__ float floor_of[DFLASH_BEAM_MAX];                    // logits below it do not reach the bound
+  __shared__ float2 near_of[DFLASH_BEAM_MAX];                    // base and ref, rounded
   __shared__ uint8_t state[DFLASH_BEAM_MAX];
-  __shared__ unsigned long long head_score[MAX_LISTS];
-  __shared__ Cand group_head[JOIN_THREADS];
-  __shared__ Cand bound_s;
-  __shared__ uint16_t chosen[MAX_LISTS];
-  __shared__ Cand kept[JOIN_KEEP], sorted[DFLASH_BEAM_MAX_N];
+  __shared__ float bound_s;
+  __shared__ int2 chosen[CHOSEN];                                // first vector; beam, above the part's end
+  __shared__ Cand kept[KEEP], sorted[DFLASH_BEAM_MAX_N];
   __shared__ int count_s, chosen_s;
 
   const int tid = threadIdx.x, lane = tid & 31, b = blockIdx.x;
-  const int S = p.splits, lists = p.beams * S;
-  const unsigned long long* best = p.best + (long long)b * lists * p.n;
-  // Few candidates are all ranked.  Of more, the lists are compared at a depth:
-  // with fewer than four lists a candidate asked for, deeper, so that few of the
-  // lists are above the bound.
-  const bool few = lists * p.n <= FEW;
-  int depth = 1;
-#pragma unroll 1
-  while (depth < p.n && lists < 4 * ((p.n + depth - 1) / depth)) depth *= 2;
-  depth = min(depth, p.n);
-  const int nth = (p.n + depth - 1) / depth, G = groups_for(nth);
+  const int S = p.splits, wide = SCAN_THREADS >> p.quad_log;
+  const int row_cells = S * p.segments * wide, all_cells = p.beams * row_cells;  // multiples of 8, at most CELLS
+  const float4* cells = reinterpret_cast<const float4*>(p.cells + (long long)b * all_cells);
   if (tid == 0) {
     count_s = chosen_s = 0;
-    bound_s = {0, 0};
   }
   pdl_launch_dependents();
   pdl_wait();
-  // the first candidates are on their way while the sums are joined; those of a beam that does not run are not looked at
-  unsigned long long head[PER], deep[PER];
+  // the cells are on their way while the sums are joined; those of a beam that does not run are not looked at
+  float4 cell[CELL_LOADS];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int l = tid + i * JOIN_THREADS;
-    head[i] = deep[i] = 0;
-    if (l >= (few ? lists * p.n : lists)) continue;
-    head[i] = few ? best[l] : best[(long long)l * p.n];
-    if (!few && depth > 1) deep[i] = best[(long long)l * p.n + depth - 1];
+  for (int i = 0; i < CELL_LOADS; ++i) {
+    const int c = tid + i * JOIN_THREADS;
+    cell[i] = make_float4(-INF, -INF, -INF, -INF);
+    if (4 * c < all_cells) cell[i] = __ldcg(cells + c);
   }
 
   // ---- each beam's sum, a lane a part
@@ -656,28 +533,73 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_beam_join(const BeamParams p) 
     }
     for (int d = W >> 1; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
     if (k < p.beams && at == 0) {
-      base[k] = score;
-      ref[k] = any ? r : 0.0;
-      sum_of[k] = sum;
+      double c = score;
+      if (any) {
+        const Log l = ln(sum);
+        c += (FIX - l.e) * LN2 - (double)l.hi - (double)l.lo;
+      } else {
+        r = 0.0;
+      }
+      base[k] = c;
+      ref[k] = r;
+      near_of[k] = make_float2((float)c, (float)r);
       state[k] = (uint8_t)(any ? RUNS : score > -INF && score <= FLT_MAX && done ? ENDED : DEAD);
       floor_of[k] = -INF;
     }
   }
   __syncthreads();
-  if (tid < p.beams && state[tid] == RUNS) {
-    const Log l = ln(sum_of[tid]);
-    base[tid] += (FIX - l.e) * LN2 - (double)l.hi - (double)l.lo;
-  }
-  __syncthreads();
 
   auto put = [&](const Cand& c) { kept[atomicAdd(&count_s, 1)] = c; };
-  auto value = [&](int k, unsigned long long key) {  // of a list's key
-    const uint32_t logit = (uint32_t)(key >> 32);
-    return cand(base[k] + ((double)unordered(logit) - ref[k]), k, logit, 0xffffffffu - (uint32_t)key);
+  auto value = [&](int k, float x, int token) {
+    return cand(base[k] + ((double)x - ref[k]), k, ordered(x), (uint32_t)token);
   };
   if (tid < p.beams && state[tid] == ENDED) put(cand(base[tid], tid, 0, (uint32_t)p.done_token));  // one candidate, itself
+
+  // ---- a bound below n candidates: the n-th best of some groups' best cells, in 32
+  // bits with what those may be off by taken away
+  {
+    float best = -INF;
+#pragma unroll
+    for (int i = 0; i < CELL_LOADS; ++i) {
+      const int c = 4 * (tid + i * JOIN_THREADS), k = c / row_cells;
+      if (c >= all_cells || state[k] != RUNS) continue;
+      const float x = fmaxf(fmaxf(cell[i].x, cell[i].y), fmaxf(cell[i].z, cell[i].w));
+      const float2 near = near_of[k];
+      const float score = near.x + (x - near.y);
+      const float off = (fabsf(score) + fabsf(near.x) + fabsf(near.y) + fabsf(x)) * 0x1p-21f;  // eight roundings of the largest
+      if (x > -INF) best = fmaxf(best, score - off);
+    }
+    float* group_best = reinterpret_cast<float*>(chosen);  // not used yet
+    group_best[tid] = best;
+    __syncthreads();
+    const int G = groups_for(p.n), lanes = JOIN_THREADS / G, g = tid / lanes;
+    float m = -INF;
+#pragma unroll 1
+    for (int u = g + (tid % lanes) * G; u < JOIN_THREADS; u += lanes * G) m = fmaxf(m, group_best[u]);  // its members
+    for (int d = lanes >> 1; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    __syncthreads();
+    if (tid % lanes == 0) group_best[g] = m;
+    __syncthreads();
+    int above = 0;
+#pragma unroll 8
+    for (int u = tid % lanes; u < G; u += lanes) {
+      const float o = group_best[u];
+      above += (o > m) | ((o == m) & (u < g));
+    }
+    for (int d = lanes >> 1; d; d >>= 1) above += __shfl_xor_sync(0xffffffffu, above, d);
+    if (above == p.n - 1 && tid % lanes == 0) bound_s = m;  // of one group; -inf: there are not as many
+    __syncthreads();
+  }
+  if (tid < p.beams && state[tid] == RUNS) {
+    const float2 near = near_of[tid];
+    const float f = bound_s - near.x + near.y;  // below it no logit reaches the bound
+    floor_of[tid] = bound_s > -INF && fabsf(near.x) <= FLT_MAX ? f - (fabsf(f) + fabsf(bound_s) + fabsf(near.x) + fabsf(near.y)) * 0x1p-21f : -INF;
+  }
+  Cand least = {0, 0};  // what is not below it is wanted
+  __syncthreads();
+
   auto ranked = [&](int count, auto&& f) {  // every candidate with its rank
-    const int lanes = rank_lanes(JOIN_THREADS, count), at = tid & (lanes - 1);
+    const int lanes = rank_lanes(count), at = tid & (lanes - 1);
 #pragma unroll 1
     for (int i0 = 0; i0 < count; i0 += JOIN_THREADS / lanes) {
       const int i = i0 + tid / lanes;
@@ -693,7 +615,6 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_beam_join(const BeamParams p) 
       if (at == 0 && i < count && rank < p.n) f(c, rank);
     }
   };
-  Cand least = {0, 0};  // what is not below it is wanted
   auto prune = [&]() {  // to the n best
     const int count = count_s;
     ranked(count, [&](const Cand& c, int rank) { sorted[rank] = c; });
@@ -705,88 +626,106 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_beam_join(const BeamParams p) 
     if (tid == 0) count_s = left;
     __syncthreads();
   };
-  if (few) {
-    const int k = tid / (S * p.n);
-    if (head[0] && state[k] == RUNS) put(value(k, head[0]));
-    __syncthreads();
-  } else {
-    // ---- a bound below n candidates: the nth largest of the lists' `depth`-th ones, in groups
-    Cand mine = {0, 0};
+
+  // ---- the cells that reach it, and their logits
+  const int rounds = p.seg_len * AHEAD, cell_vecs = rounds << p.quad_log;
+  const int vecs = (p.vocab + N - 1) / N;
+  unsigned hits = 0;  // of this thread's cells
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int l = tid + i * JOIN_THREADS, k = l / S;
-      if (l >= lists) break;
-      Cand c = {0, 0};
-      const bool runs = state[k] == RUNS;
-      if (runs && head[i]) c = value(k, head[i]);
-      head_score[l] = c.score;
-      if (depth > 1) {
-        c.score = 0;
-        if (runs && deep[i]) c = value(k, deep[i]);
-      }
-      if (better(c, mine)) mine = c;
-    }
-    group_head[tid] = mine;
-    __syncthreads();
-    const int live = min(G, lists), parts = JOIN_THREADS / G, g = tid / parts;  // threads of a group
-    if (G < JOIN_THREADS) {
-      if (tid < G) {
+  for (int i = 0; i < CELL_LOADS; ++i) {
+    const int c = 4 * (tid + i * JOIN_THREADS), k = c / row_cells;
+    if (c >= all_cells || state[k] != RUNS) continue;
+    const float least_x = fmaxf(floor_of[k], -FLT_MAX);
+    hits |= ((cell[i].x >= least_x) | (cell[i].y >= least_x) << 1 | (cell[i].z >= least_x) << 2 | (cell[i].w >= least_x) << 3) << 4 * i;
+  }
+  auto choose = [&](unsigned h) {  // false: there was no room
+    if (h == 0) return true;
+    int o = atomicAdd(&chosen_s, __popc(h));
+    if (o + __popc(h) > CHOSEN) return false;
 #pragma unroll 1
-        for (int u = tid + G; u < min(JOIN_THREADS, lists); u += G)
-          if (better(group_head[u], mine)) mine = group_head[u];
-        group_head[tid] = mine;
+    for (; h; h &= h - 1) {
+      const int bit = __ffs(h) - 1, c = 4 * (tid + (bit >> 2) * JOIN_THREADS) + (bit & 3);
+      const int k = c / row_cells, at = c - k * row_cells;  // beam, cell of its row
+      const int seg = at / wide, part = seg / p.segments;   // segment of the row, part
+      const int first = part * p.part + (seg - part * p.segments) * rounds * SCAN_THREADS + ((at - seg * wide) << p.quad_log);
+      chosen[o++] = make_int2(first, k << 25 | min(vecs, (part + 1) * p.part));
+    }
+    return true;
+  };
+  auto look = [&](bool turns) {  // into the chosen ones; false: more was wanted than is kept
+    const int items = chosen_s * cell_vecs;
+    bool full = false;
+#pragma unroll 1
+    for (int i0 = 0; i0 < items; i0 += AGAIN * JOIN_THREADS) {
+      int token[AGAIN], beam[AGAIN];
+      unsigned wanted = 0;  // of their tokens
+      uint4 v[AGAIN];
+      bool inside[AGAIN];
+#pragma unroll
+      for (int j = 0; j < AGAIN; ++j) {
+        const int it = i0 + j * JOIN_THREADS + tid;
+        token[j] = beam[j] = 0;
+        inside[j] = false;
+        if (it >= items) continue;
+        const int o = it / cell_vecs, nth = it - o * cell_vecs;
+        const int2 c = chosen[o];
+        const int i = c.x + (nth >> p.quad_log) * SCAN_THREADS + (nth & (p.quad - 1));  // vector
+        const int k = c.y >> 25, v1 = c.y & 0x1ffffff;
+        const Row<T, ALIGNED> in = {p.logits + (b * p.beams + k) * p.row_bytes, p.vocab};
+        beam[j] = k;
+        token[j] = i * N;
+        inside[j] = i > 0 && i < min(v1, in.inner());
+        if (inside[j]) v[j] = in.load(i);
+        else if (i < v1) wanted |= ((1u << min(N, p.vocab - token[j])) - 1) << j * N;
+      }
+#pragma unroll
+      for (int j = 0; j < AGAIN; ++j) {
+        if (!inside[j]) continue;
+        float x[N];
+        Vec<T>::floats(v[j], x);
+        const float least_x = floor_of[beam[j]];
+#pragma unroll
+        for (int e = 0; e < N; ++e) wanted |= (x[e] >= least_x) << (j * N + e);
+      }
+#pragma unroll 1
+      for (int e = 0; turns ? e < AGAIN * N : wanted != 0; ++e) {  // in turns: one token a thread
+        if (turns) {
+          __syncthreads();
+          if (count_s + JOIN_THREADS > KEEP) prune();  // leaves at most DFLASH_BEAM_MAX_N
+          __syncthreads();
+          if (!(wanted >> e & 1)) continue;
+        }
+        const int bit = turns ? e : __ffs(wanted) - 1;
+        wanted &= ~(1u << bit);
+        const int t = (bit >= N ? token[AGAIN - 1] : token[0]) + bit % N, k = bit >= N ? beam[AGAIN - 1] : beam[0];
+        const Row<T, ALIGNED> in = {p.logits + (b * p.beams + k) * p.row_bytes, p.vocab};
+        const float x = in.at(t);
+        if (!(x >= floor_of[k] && x >= -FLT_MAX && x <= FLT_MAX)) continue;
+        const Cand c = value(k, x, t);
+        if (better(least, c)) continue;
+        const int o = atomicAdd(&count_s, 1);
+        if (o < KEEP) kept[o] = c;
+        else full = true;
+      }
+    }
+    return !__syncthreads_or(full);
+  };
+  // All of them at once; or, where there is no room for the cells or for what they
+  // hold, a load of every thread at a time, in turns.
+  const int before = count_s;
+  const bool room = choose(hits);
+  if (__syncthreads_or(!room) || !look(false)) {
+#pragma unroll 1
+    for (int i = 0; i < CELL_LOADS; ++i) {
+      __syncthreads();
+      if (tid == 0) {
+        chosen_s = 0;
+        if (i == 0) count_s = before;
       }
       __syncthreads();
-    }
-    {
-      const Cand c = group_head[g];
-      int n = 0;
-#pragma unroll 1
-      for (int u = tid % parts; u < live; u += parts) n += better(group_head[u], c);
-      for (int d = parts >> 1; d; d >>= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
-      if (g < live && c.score && n == nth - 1) bound_s = c;  // of one group
-    }
-    __syncthreads();
-    least = bound_s;
-    if (least.score && tid < p.beams && state[tid] == RUNS) {
-      const double score = unordered(least.score), lost = (fabs(score) + fabs(base[tid]) + fabs(ref[tid])) * 0x1p-50;
-      const float f = (float)(score - base[tid] + ref[tid] - lost);  // below what rounds to the bound in 64 bits
-      floor_of[tid] = f - fabsf(f) * 1e-6f - 1e-30f;                 // and a few last places
-    }
-#pragma unroll 1
-    for (int l = tid; l < lists; l += JOIN_THREADS) {
-      const unsigned long long h = head_score[l];  // equal ones are looked into
-      if (h && h >= least.score) chosen[atomicAdd(&chosen_s, 1)] = (uint16_t)l;
-    }
-    __syncthreads();
-
-    // ---- the candidates of the lists that reach it: LIST_LANES threads a list, its next entries at once, until one is below
-    const int n_chosen = chosen_s;
-    constexpr int ABREAST = JOIN_THREADS / LIST_LANES;
-#pragma unroll 1
-    for (int c0 = 0; c0 < n_chosen; c0 += ABREAST) {
-      const int at = c0 + tid / LIST_LANES;
-      const int l = at < n_chosen ? chosen[at] : 0, k = l / S;
-      bool open = at < n_chosen;
-#pragma unroll 1
-      for (int e0 = 0; e0 < p.n; e0 += LIST_LANES) {
-        const int e = e0 + tid % LIST_LANES;
-        Cand c = {0, 0};
-        bool push = false;
-        if (open && e < p.n) {
-          const unsigned long long key = best[(long long)l * p.n + e];
-          if (key && unordered((uint32_t)(key >> 32)) >= floor_of[k]) {
-            c = value(k, key);
-            push = !better(least, c);
-          }
-        }
-        const unsigned some = __ballot_sync(0xffffffffu, push);
-        open = open && (some >> (lane / LIST_LANES * LIST_LANES) & ((1u << LIST_LANES) - 1)) == (1u << LIST_LANES) - 1;
-        if (count_s + JOIN_THREADS > JOIN_KEEP) prune();  // the same for all: it is changed only between the barriers below
-        __syncthreads();
-        if (push && !better(least, c)) put(c);
-        if (!__syncthreads_or(open)) break;
-      }
+      choose(hits & 15u << 4 * i);
+      __syncthreads();
+      look(true);
     }
   }
 
@@ -804,8 +743,8 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_beam_join(const BeamParams p) 
 // ------------------------------------------------------------------ host
 
 struct Plan {
-  int splits, part;
-  size_t sums, best, bytes;  // offsets
+  int splits, part, segments, seg_len, quad, quad_log;
+  size_t cells, bytes;  // offset of the cells; of the sums: 0
 };
 constexpr int MAX_VOCAB = 1 << 24;  // of a row: the fixed-point sums' range
 
@@ -818,20 +757,29 @@ int beam_check(int batch, int beams, int vocab, int n, int dtype) {
   return (long long)batch * beams * MAX_SPLITS > 0x7fffffffll ? DFLASH_ERR_CAPACITY : DFLASH_OK;
 }
 
-// Parts of a row: as many CTAs as run at once, none with less than half a step
-// of loads.
-Plan plan_of(int batch, int beams, int vocab, int n, int dtype) {
+// Parts of a row: as many CTAs as run at once, none with less than half a batch.
+// Cells: a thread's in up to MAX_SEGMENTS segments, but no more of a request than
+// the join holds: fewer segments, then more threads a cell.  That fits: 608 parts of
+// 256 / 32 cells, or 64 of one part each.
+Plan plan_of(int batch, int beams, int vocab, int dtype) {
   const int per = dtype == DFLASH_F32 ? 4 : 8, vecs = (vocab + per - 1) / per;
   const long long rows = std::max(1ll, (long long)batch * beams);
   const int least = SCAN_THREADS * AHEAD / 2;
-  long long splits = std::min<long long>(SMS * SCAN_CTAS / rows, (vecs + least - 1) / least);
-  splits = std::max(1ll, std::min<long long>(splits, std::min(MAX_SPLITS, MAX_LISTS / beams)));
+  long long splits = std::min<long long>((BEAM_SLOTS) / rows, (vecs + least - 1) / least);
+  splits = std::max(1ll, std::min<long long>(splits, MAX_SPLITS));
   Plan r;
   r.part = (int)((vecs + splits - 1) / splits + SCAN_THREADS - 1) / SCAN_THREADS * SCAN_THREADS;
   r.splits = (vecs + r.part - 1) / r.part;
-  r.sums = 0;
-  r.best = (rows * r.splits * sizeof(PartSum) + 255) / 256 * 256;
-  r.bytes = r.best + rows * r.splits * n * sizeof(unsigned long long);
+  const int batches = (r.part + SCAN_THREADS * AHEAD - 1) / (SCAN_THREADS * AHEAD);
+  r.segments = std::min(MAX_SEGMENTS, batches);
+  r.quad = 1, r.quad_log = 0;
+  auto cells = [&]() { return (long long)beams * r.splits * r.segments * (SCAN_THREADS / r.quad); };
+  while (r.segments > 1 && cells() > CELLS) r.segments = (r.segments + 1) / 2;
+  while (r.quad < 32 && cells() > CELLS) r.quad *= 2, ++r.quad_log;
+  r.seg_len = (batches + r.segments - 1) / r.segments;
+  r.segments = (batches + r.seg_len - 1) / r.seg_len;
+  r.cells = (rows * r.splits * sizeof(PartSum) + 255) / 256 * 256;
+  r.bytes = r.cells + rows * r.splits * r.segments * (SCAN_THREADS / r.quad) * sizeof(float);
   return r;
 }
 
@@ -851,7 +799,8 @@ int launch_beam(const BeamParams& p, bool aligned, cudaStream_t s) {
     return e;
   cfg.gridDim = dim3((unsigned)p.batch);
   cfg.blockDim = dim3(JOIN_THREADS);
-  return cuda_status(cudaLaunchKernelEx(&cfg, k_beam_join, p));
+  return cuda_status(aligned ? cudaLaunchKernelEx(&cfg, k_beam_join<T, true>, p)
+                             : cudaLaunchKernelEx(&cfg, k_beam_join<T, false>, p));
 }
 
 }  // namespace
@@ -860,7 +809,7 @@ extern "C" {
 
 size_t dflash_beam_select_workspace(int32_t batch, int32_t beams, int32_t vocab, int32_t n, int32_t dtype) {
   if (beam_check(batch, beams, vocab, n, dtype) || batch == 0) return 0;
-  return plan_of(batch, beams, vocab, n, dtype).bytes;
+  return plan_of(batch, beams, vocab, dtype).bytes;
 }
 
 int dflash_beam_select(const dflash_beam_args* a, void* stream) {
@@ -870,7 +819,7 @@ int dflash_beam_select(const dflash_beam_args* a, void* stream) {
   if (!a->logits || !a->scores || !a->scores_out || !a->parents || !a->tokens || a->device < 0 ||
       (a->done && (a->done_token < 0 || a->done_token >= a->vocab)))
     return DFLASH_ERR_INVALID_ARG;
-  const Plan plan = plan_of(a->batch, a->beams, a->vocab, a->n, a->dtype);
+  const Plan plan = plan_of(a->batch, a->beams, a->vocab, a->dtype);
   if (!a->workspace || (reinterpret_cast<uintptr_t>(a->workspace) & 255) || a->workspace_bytes < (int64_t)plan.bytes)
     return DFLASH_ERR_WORKSPACE;
   const long long size = a->dtype == DFLASH_F32 ? 4 : 2, rows = (long long)a->batch * a->beams, outs = (long long)a->batch * a->n;
@@ -896,14 +845,18 @@ int dflash_beam_select(const dflash_beam_args* a, void* stream) {
   p.parents = a->parents;
   p.tokens = a->tokens;
   p.status = a->status;
-  p.sums = reinterpret_cast<PartSum*>(static_cast<char*>(a->workspace) + plan.sums);
-  p.best = reinterpret_cast<unsigned long long*>(static_cast<char*>(a->workspace) + plan.best);
+  p.sums = static_cast<PartSum*>(a->workspace);
+  p.cells = reinterpret_cast<float*>(static_cast<char*>(a->workspace) + plan.cells);
   p.batch = a->batch;
   p.beams = a->beams;
   p.vocab = a->vocab;
   p.n = a->n;
   p.splits = plan.splits;
   p.part = plan.part;
+  p.segments = plan.segments;
+  p.seg_len = plan.seg_len;
+  p.quad = plan.quad;
+  p.quad_log = plan.quad_log;
   p.done_token = a->done_token;
   const bool aligned = (reinterpret_cast<uintptr_t>(a->logits) & 15) == 0 && (rows == 1 || p.row_bytes % 16 == 0);
   DeviceGuard guard(a->device);
