@@ -35,7 +35,6 @@ constexpr int AHEAD = 4;          // vectors of a thread's batch
 constexpr int MAX_SEGMENTS = 8;   // of a part, with cells of their own
 constexpr int MAX_SPLITS = 32;    // parts of a row: a lane each when they are joined
 constexpr int JOIN_THREADS = 512;
-constexpr int AGAIN = 2;          // vectors of a thread that are looked at again at once
 constexpr int CELL_LOADS = 6;     // of a thread of the join: four cells each, held in registers
 constexpr int CELLS = 4 * CELL_LOADS * JOIN_THREADS;  // of a request
 constexpr int CHOSEN = 4 * JOIN_THREADS;  // cells that are looked into at a time: a load of every thread, at least
@@ -486,6 +485,8 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_beam_join(const BeamParams p) 
 
   const int tid = threadIdx.x, lane = tid & 31, b = blockIdx.x;
   const int S = p.splits, wide = SCAN_THREADS >> p.quad_log;
+  const float per_row_cell = 1.0f / (float)(S * p.segments * wide);
+  auto row_of = [&](int c) { return (int)(((float)c + 0.5f) * per_row_cell); };  // of a cell: below 2^14, half a cell from the next
   const int row_cells = S * p.segments * wide, all_cells = p.beams * row_cells;  // multiples of 8, at most CELLS
   const float4* cells = reinterpret_cast<const float4*>(p.cells + (long long)b * all_cells);
   if (tid == 0) {
@@ -561,7 +562,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_beam_join(const BeamParams p) 
     float best = -INF;
 #pragma unroll
     for (int i = 0; i < CELL_LOADS; ++i) {
-      const int c = 4 * (tid + i * JOIN_THREADS), k = c / row_cells;
+      const int c = 4 * (tid + i * JOIN_THREADS), k = row_of(c);
       if (c >= all_cells || state[k] != RUNS) continue;
       const float x = fmaxf(fmaxf(cell[i].x, cell[i].y), fmaxf(cell[i].z, cell[i].w));
       const float2 near = near_of[k];
@@ -633,7 +634,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_beam_join(const BeamParams p) 
   unsigned hits = 0;  // of this thread's cells
 #pragma unroll
   for (int i = 0; i < CELL_LOADS; ++i) {
-    const int c = 4 * (tid + i * JOIN_THREADS), k = c / row_cells;
+    const int c = 4 * (tid + i * JOIN_THREADS), k = row_of(c);
     if (c >= all_cells || state[k] != RUNS) continue;
     const float least_x = fmaxf(floor_of[k], -FLT_MAX);
     hits |= ((cell[i].x >= least_x) | (cell[i].y >= least_x) << 1 | (cell[i].z >= least_x) << 2 | (cell[i].w >= least_x) << 3) << 4 * i;
@@ -645,50 +646,52 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_beam_join(const BeamParams p) 
 #pragma unroll 1
     for (; h; h &= h - 1) {
       const int bit = __ffs(h) - 1, c = 4 * (tid + (bit >> 2) * JOIN_THREADS) + (bit & 3);
-      const int k = c / row_cells, at = c - k * row_cells;  // beam, cell of its row
+      const int k = row_of(c), at = c - k * row_cells;  // beam, cell of its row
       const int seg = at / wide, part = seg / p.segments;   // segment of the row, part
       const int first = part * p.part + (seg - part * p.segments) * rounds * SCAN_THREADS + ((at - seg * wide) << p.quad_log);
       chosen[o++] = make_int2(first, k << 25 | min(vecs, (part + 1) * p.part));
     }
     return true;
   };
+  struct Item {  // a vector of a chosen cell
+    uint4 v;
+    int token, beam;
+    int count;  // of its tokens, -1: all of them, in v
+  };
+  auto fetch = [&](int it, int items) {
+    Item r = {};
+    if (it >= items) return r;
+    const int o = it / cell_vecs, nth = it - o * cell_vecs;
+    const int2 c = chosen[o];
+    const int i = c.x + (nth >> p.quad_log) * SCAN_THREADS + (nth & (p.quad - 1)), v1 = c.y & 0x1ffffff;
+    r.beam = c.y >> 25;
+    r.token = i * N;
+    const Row<T, ALIGNED> in = {p.logits + (b * p.beams + r.beam) * p.row_bytes, p.vocab};
+    if (i > 0 && i < min(v1, in.inner())) r.v = in.load(i), r.count = -1;
+    else if (i < v1) r.count = min(N, p.vocab - r.token);
+    return r;
+  };
   auto look = [&](bool turns) {  // into the chosen ones; false: more was wanted than is kept
     const int items = chosen_s * cell_vecs;
     bool full = false;
+    Item next = fetch(tid, items);
 #pragma unroll 1
-    for (int i0 = 0; i0 < items; i0 += AGAIN * JOIN_THREADS) {
-      int token[AGAIN], beam[AGAIN];
-      unsigned wanted = 0;  // of their tokens
-      uint4 v[AGAIN];
-      bool inside[AGAIN];
-#pragma unroll
-      for (int j = 0; j < AGAIN; ++j) {
-        const int it = i0 + j * JOIN_THREADS + tid;
-        token[j] = beam[j] = 0;
-        inside[j] = false;
-        if (it >= items) continue;
-        const int o = it / cell_vecs, nth = it - o * cell_vecs;
-        const int2 c = chosen[o];
-        const int i = c.x + (nth >> p.quad_log) * SCAN_THREADS + (nth & (p.quad - 1));  // vector
-        const int k = c.y >> 25, v1 = c.y & 0x1ffffff;
-        const Row<T, ALIGNED> in = {p.logits + (b * p.beams + k) * p.row_bytes, p.vocab};
-        beam[j] = k;
-        token[j] = i * N;
-        inside[j] = i > 0 && i < min(v1, in.inner());
-        if (inside[j]) v[j] = in.load(i);
-        else if (i < v1) wanted |= ((1u << min(N, p.vocab - token[j])) - 1) << j * N;
-      }
-#pragma unroll
-      for (int j = 0; j < AGAIN; ++j) {
-        if (!inside[j]) continue;
+    for (int i0 = 0; i0 < items; i0 += JOIN_THREADS) {
+      const Item now = next;
+      if (i0 + JOIN_THREADS < items) next = fetch(i0 + JOIN_THREADS + tid, items);
+      const float least_x = floor_of[now.beam];
+      unsigned wanted = 0;  // of its tokens
+      if (now.count < 0) {
         float x[N];
-        Vec<T>::floats(v[j], x);
-        const float least_x = floor_of[beam[j]];
+        Vec<T>::floats(now.v, x);
 #pragma unroll
-        for (int e = 0; e < N; ++e) wanted |= (x[e] >= least_x) << (j * N + e);
+        for (int e = 0; e < N; ++e) wanted |= (x[e] >= least_x) << e;
+      } else {
+        wanted = (1u << now.count) - 1;
       }
+      const Row<T, ALIGNED> in = {p.logits + (b * p.beams + now.beam) * p.row_bytes, p.vocab};
 #pragma unroll 1
-      for (int e = 0; turns ? e < AGAIN * N : wanted != 0; ++e) {  // in turns: one token a thread
+      for (int e = 0; turns ? e < N : wanted != 0; ++e) {  // in turns: one token a thread
         if (turns) {
           __syncthreads();
           if (count_s + JOIN_THREADS > KEEP) prune();  // leaves at most DFLASH_BEAM_MAX_N
@@ -697,11 +700,9 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_beam_join(const BeamParams p) 
         }
         const int bit = turns ? e : __ffs(wanted) - 1;
         wanted &= ~(1u << bit);
-        const int t = (bit >= N ? token[AGAIN - 1] : token[0]) + bit % N, k = bit >= N ? beam[AGAIN - 1] : beam[0];
-        const Row<T, ALIGNED> in = {p.logits + (b * p.beams + k) * p.row_bytes, p.vocab};
-        const float x = in.at(t);
-        if (!(x >= floor_of[k] && x >= -FLT_MAX && x <= FLT_MAX)) continue;
-        const Cand c = value(k, x, t);
+        const float x = in.at(now.token + bit);
+        if (!(x >= least_x && x >= -FLT_MAX && x <= FLT_MAX)) continue;
+        const Cand c = value(now.beam, x, now.token + bit);
         if (better(least, c)) continue;
         const int o = atomicAdd(&count_s, 1);
         if (o < KEEP) kept[o] = c;
