@@ -26,11 +26,9 @@
 
 namespace {
 
-#ifndef BEAM_SLOTS
-#define BEAM_SLOTS 608
-#endif
 constexpr int SCAN_THREADS = 256;
 constexpr int SCAN_CTAS = 4;      // of an SM
+constexpr int SLOTS = 152 * SCAN_CTAS;  // CTAs that run at once
 constexpr int AHEAD = 4;          // vectors of a thread's batch
 constexpr int MAX_SEGMENTS = 8;   // of a part, with cells of their own
 constexpr int MAX_SPLITS = 32;    // parts of a row: a lane each when they are joined
@@ -766,7 +764,7 @@ Plan plan_of(int batch, int beams, int vocab, int dtype) {
   const int per = dtype == DFLASH_F32 ? 4 : 8, vecs = (vocab + per - 1) / per;
   const long long rows = std::max(1ll, (long long)batch * beams);
   const int least = SCAN_THREADS * AHEAD / 2;
-  long long splits = std::min<long long>((BEAM_SLOTS) / rows, (vecs + least - 1) / least);
+  long long splits = std::min<long long>(SLOTS / rows, (vecs + least - 1) / least);
   splits = std::max(1ll, std::min<long long>(splits, MAX_SPLITS));
   Plan r;
   r.part = (int)((vecs + splits - 1) / splits + SCAN_THREADS - 1) / SCAN_THREADS * SCAN_THREADS;

@@ -275,6 +275,69 @@ def test_the_largest_pool(ops):
         ops.resize(make_pool(ops, 1, 1, 16), i32([1]), moves=torch.zeros(1, 3, dtype=I32, device="cuda"))
 
 
+def test_tables_past_32_bits(ops):
+    """Rows so far apart that the last ones begin past 2^31 entries; odd strides, which take entries one by one."""
+    batch, width, page = 8192, 5, 16
+    for stride in (270000, 270001):
+        table = torch.empty(batch * stride, dtype=I32, device="cuda").as_strided((batch, width), (stride, 1))
+        table.fill_(-7)
+        pool = ops.PagePool(table, 5 * batch, page)
+        lens = torch.arange(batch, device="cuda") * 7 % 81
+        ops.resize(pool, lens.to(I32))
+        need = (lens + 15) // 16
+        col = torch.arange(width, device="cuda")
+        want = torch.where(col < need[:, None], (torch.cumsum(need, 0) - need)[:, None] + col, -7)
+        assert torch.equal(table.long(), want)
+        parents = torch.arange(batch - 1, -1, -1, device="cuda")
+        ops.fork(pool, parents.to(I32))
+        has = col < need[parents][:, None]
+        assert torch.equal(table[has].long(), want[parents][has]) and (table[~has] < 0).all()
+        moves, remap = ops.compact(pool)
+        assert moves[0, 0].item() == 0 and pool.read_status() == 0
+        ops.resize(pool, torch.zeros_like(pool.lens))
+        assert not pool.refs.any() and (table < 0).all() and pool.read_status() == 0
+        del table, pool
+
+
+def test_wide_tables_of_few_and_of_many_sequences(ops):
+    """Columns shared out to several blocks, a grid of its own for the compaction's table, whole rows given up."""
+    for batch, width in ((1, 3000), (9, 2600), (700, 130)):
+        n_pages = batch * width + 9
+        pool = make_pool(ops, batch, width, n_pages)
+        ref = beam_ref.Pool.of(pool)
+        rng = random.Random(width)
+        step(ops, pool, ref, "resize", [rng.randint(0, width * 16) for _ in range(batch)])
+        step(ops, pool, ref, "fork", [rng.randrange(-1, batch) for _ in range(batch)])
+        ref.check()
+        step(ops, pool, ref, "resize", [n // rng.choice([1, 2, 5, 10 ** 9]) for n in ref.lens])
+        moves, remap = ops.compact(pool)
+        want, want_remap = ref.compact()
+        assert moves_of(moves) == want and remap.tolist() == want_remap
+        same(pool, ref)
+        ref.check()
+
+
+def test_entries_behind_a_sequences_end_do_not_matter(ops):
+    """Whatever they hold, the pages that come to lie there among it."""
+    pool = make_pool(ops, 3, 6, 30)
+    ref = beam_ref.Pool.of(pool)
+    for fill in (-1, 0, 5, 2 ** 31 - 1, -2 ** 31):
+        for b, n in enumerate(ref.lens):
+            for i in range(ref.pages(n), 6):
+                ref.table[b][i] = fill
+        pool.page_table.copy_(i32(ref.table))
+        step(ops, pool, ref, "resize", [33, 0, 90])
+        for b, n in enumerate(ref.lens):  # the very pages that a fork brings
+            for i in range(ref.pages(n), 6):
+                ref.table[b][i] = ref.table[(b + 1) % 3][i]
+        pool.page_table.copy_(i32(ref.table))
+        step(ops, pool, ref, "fork", [1, 2, 0])
+        ref.check()
+        step(ops, pool, ref, "fork", [0, 0, 0])
+        step(ops, pool, ref, "resize", [17, 0, 96])
+        ref.check()
+
+
 # ------------------------------------------------------------------ copies
 
 ORDERS = {"psh": (0, 1, 2, 3), "phs": (0, 2, 1, 3), "hps": (1, 2, 0, 3), "sph": (1, 0, 2, 3)}
@@ -434,6 +497,39 @@ def test_ties_go_to_the_lowest_beam_and_token(ops, dtype):
     up = torch.arange(vocab, device="cuda", dtype=F32).div(vocab).to(dtype).expand(4, vocab)  # ascending
     check_select(ops, up.contiguous(), torch.zeros(4, 1, device="cuda"), 128, exact=True)
     check_select(ops, up.flip(1).contiguous(), torch.zeros(4, 1, device="cuda"), 128, exact=True)
+
+
+@pytest.mark.parametrize("batch,beams,vocab,n", [(1, 1, 300000, 128), (2, 16, 151936, 128), (1, 64, 40001, 5), (3, 2, 70000, 64)])
+def test_ties_in_every_part_of_many_rows(ops, batch, beams, vocab, n):
+    """Every cell reaches the bound, thousands of candidates are equal: taken in turns, the lowest of them kept."""
+    g = gen(n)
+    flat = torch.zeros(batch * beams, vocab, dtype=BF16, device="cuda")
+    check_select(ops, flat, torch.zeros(batch, beams, device="cuda"), n, exact=True)
+    few = torch.randint(0, 3, (batch * beams, vocab), generator=g, device="cuda").to(BF16)
+    check_select(ops, few, -torch.arange(float(beams), device="cuda").repeat(batch, 1) / 8, n)
+    few[:, : vocab // 2] = -math.inf
+    few[beams - 1] = -math.inf
+    check_select(ops, few, -torch.rand(batch, beams, generator=g, device="cuda"), n)
+
+
+def test_selection_past_32_bits(ops):
+    """More than 2^32 bytes and 2^31 values of logits: the last rows as by themselves."""
+    rows, vocab = 14400, 151936
+    logits = torch.empty(rows, vocab, dtype=BF16, device="cuda")
+    for i in range(0, rows, 1600):
+        logits[i:i + 1600].normal_(generator=gen(i))
+    scores = -torch.rand(rows // 4, 4, generator=gen(1), device="cuda")
+    got = ops.beam_select(logits, scores, 6)
+    for b in (0, rows // 8, rows // 4 - 2):
+        want = ops.beam_select(logits[4 * b:4 * b + 8], scores[b:b + 2], 6)
+        for i in range(2):  # other parts of the rows: sums equal to rounding
+            assert torch.equal(got[1][b + i], want[1][i] + 4 * b) and torch.equal(got[2][b + i], want[2][i])
+            assert ((got[0][b + i] - want[0][i]).abs() <= 2 * beam_ref.select_tolerance(16.0, 600)).all()
+    assert torch.equal(got[2][5], beam_selected(logits[20:24], scores[5:6], 6))
+
+
+def beam_selected(logits, scores, n):
+    return i32([t for _, _, t in beam_ref.select(logits, scores, n)[0]])
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f16", "f32"])
@@ -597,6 +693,45 @@ def test_two_pools_and_two_selections_at_once(ops):
         for o in got[j]:
             assert all(torch.equal(x, y) for x, y in zip(o, want[j]))
         same(pools[j], refs[j])
+
+
+FIRST_STEP = """
+import torch
+from block_diffusion_speculative_hiddens_gb300 import ops
+i32 = dict(dtype=torch.int32, device="cuda")
+B = %d
+logits = torch.arange(B * 300., device="cuda").view(B, 300).bfloat16()
+scores = torch.zeros(B // 4, 4, device="cuda")
+table = torch.full((B, 9), -1, **i32)
+refs, lens, status = torch.zeros(20 * B, **i32), torch.zeros(B, **i32), torch.zeros(1, **i32)
+pool = ops.PagePool(table, 20 * B, 16, refs=refs, lens=lens)
+k, v = (torch.zeros(20 * B, 16, 2, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+cache = ops.PagedCache(k, v, table)
+new = torch.full((B,), 40, **i32)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    m0 = ops.resize(pool, new)
+    ops.copy_pages(cache, m0)
+    s, p, t = ops.beam_select(logits, scores, status=status)
+    ops.fork(pool, p.view(-1))
+    m1, remap = ops.compact(pool)
+    ops.copy_pages(cache, m1)
+g.replay()
+torch.cuda.synchronize()
+assert pool.read_status() == 0 and cache.read_status() == 0 and (lens == 40).all()
+assert int(refs.sum()) == 3 * B and m0[0, 0].item() == 0
+assert (p >= 0).all() and (t >= 0).all() and torch.isfinite(s).all()
+"""
+
+
+@pytest.mark.parametrize("batch", [4, 2048])
+def test_first_step_of_a_process_may_be_captured(batch):
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_STEP % batch], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 # ------------------------------------------------------------------ together
