@@ -18,6 +18,7 @@
 // a warp's and a row's a 64-bit fixed-point number.
 #include <algorithm>
 #include <cfloat>
+#include <climits>
 #include <cmath>
 
 #include "common.cuh"
@@ -473,8 +474,11 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_beam_join(const BeamParams p) 
   const float INF = __uint_as_float(0x7f800000u);
   enum { DEAD, RUNS, ENDED };
   __shared__ double base[DFLASH_BEAM_MAX], ref[DFLASH_BEAM_MAX];  // score = base + (logit - ref)
-  __shared__ float floor_of[DFLASH_BEAM_MAX];                    // logits below it do not reach the bound
   __shared__ float2 near_of[DFLASH_BEAM_MAX];                    // base and ref, rounded
+  __shared__ float off_of[DFLASH_BEAM_MAX];                      // what the rounding of ref may be
+  __shared__ float floor_of[DFLASH_BEAM_MAX];                    // logits less ref below it do not reach the bound
+  __shared__ float cut_of[DFLASH_BEAM_MAX];                      // logits below it are worse than the n kept ones,
+  __shared__ int limit_of[DFLASH_BEAM_MAX];                      // those at it from this token on
   __shared__ uint8_t state[DFLASH_BEAM_MAX];
   __shared__ float bound_s;
   __shared__ int2 chosen[CHOSEN];                                // first vector; beam, above the part's end
@@ -487,9 +491,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_beam_join(const BeamParams p) 
   auto row_of = [&](int c) { return (int)(((float)c + 0.5f) * per_row_cell); };  // of a cell: below 2^14, half a cell from the next
   const int row_cells = S * p.segments * wide, all_cells = p.beams * row_cells;  // multiples of 8, at most CELLS
   const float4* cells = reinterpret_cast<const float4*>(p.cells + (long long)b * all_cells);
-  if (tid == 0) {
-    count_s = chosen_s = 0;
-  }
+  if (tid == 0) count_s = chosen_s = 0;
   pdl_launch_dependents();
   pdl_wait();
   // the cells are on their way while the sums are joined; those of a beam that does not run are not looked at
@@ -525,7 +527,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_beam_join(const BeamParams p) 
     for (int d = W >> 1; d; d >>= 1) q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, d));
     double r = q * LN2;
     unsigned long long sum = some && q - part.q < 63.0f ? part.sum >> (int)(q - part.q) : 0;  // shifted to the largest reference
-    if (__any_sync(0xffffffffu, bare)) {
+    if (__any_sync(0xffffffffu, bare)) {  // ref is then a logit, or one of the powers of two
       double r2 = 0.0;
       const unsigned long long sum2 = sum_of_any(part, some, W, r2);
       if (bare) r = r2, sum = sum2;
@@ -542,6 +544,9 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_beam_join(const BeamParams p) 
       base[k] = c;
       ref[k] = r;
       near_of[k] = make_float2((float)c, (float)r);
+      off_of[k] = (float)fabs(r - (double)(float)r);
+      cut_of[k] = -INF;
+      limit_of[k] = INT_MAX;
       state[k] = (uint8_t)(any ? RUNS : score > -INF && score <= FLT_MAX && done ? ENDED : DEAD);
       floor_of[k] = -INF;
     }
@@ -557,24 +562,37 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_beam_join(const BeamParams p) 
   // ---- a bound below n candidates: the n-th best of some groups' best cells, in 32
   // bits with what those may be off by taken away
   {
-    float best = -INF;
-#pragma unroll
-    for (int i = 0; i < CELL_LOADS; ++i) {
-      const int c = 4 * (tid + i * JOIN_THREADS), k = row_of(c);
-      if (c >= all_cells || state[k] != RUNS) continue;
-      const float x = fmaxf(fmaxf(cell[i].x, cell[i].y), fmaxf(cell[i].z, cell[i].w));
+    auto lower = [&](int k, float x) {
       const float2 near = near_of[k];
-      const float score = near.x + (x - near.y);
-      const float off = (fabsf(score) + fabsf(near.x) + fabsf(near.y) + fabsf(x)) * 0x1p-21f;  // eight roundings of the largest
-      if (x > -INF) best = fmaxf(best, score - off);
-    }
+      const float d = x - near.y, score = near.x + d;
+      const float off = (fabsf(score) + fabsf(near.x) + fabsf(d)) * 0x1p-21f + 2.0f * off_of[k];  // eight roundings, and ref's
+      return x > -INF ? score - off : -INF;
+    };
     float* group_best = reinterpret_cast<float*>(chosen);  // not used yet
-    group_best[tid] = best;
+    if (all_cells <= JOIN_THREADS) {  // few: a cell each, not the best of a thread's
+      if (4 * tid < all_cells) {
+        const int k = row_of(4 * tid);
+        const bool runs = state[k] == RUNS;
+        const float x[4] = {cell[0].x, cell[0].y, cell[0].z, cell[0].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) group_best[4 * tid + j] = runs ? lower(k, x[j]) : -INF;
+      }
+      if (tid >= all_cells) group_best[tid] = -INF;
+    } else {
+      float best = -INF;
+#pragma unroll
+      for (int i = 0; i < CELL_LOADS; ++i) {
+        const int c = 4 * (tid + i * JOIN_THREADS), k = row_of(c);
+        if (c >= all_cells || state[k] != RUNS) continue;
+        best = fmaxf(best, lower(k, fmaxf(fmaxf(cell[i].x, cell[i].y), fmaxf(cell[i].z, cell[i].w))));
+      }
+      group_best[tid] = best;
+    }
     __syncthreads();
-    const int G = groups_for(p.n), lanes = JOIN_THREADS / G, g = tid / lanes;
-    float m = -INF;
-#pragma unroll 1
-    for (int u = g + (tid % lanes) * G; u < JOIN_THREADS; u += lanes * G) m = fmaxf(m, group_best[u]);  // its members
+    // a group's members: threads G apart, a little more from one to the next, so
+    // that short rows, which begin alike, fall into different groups
+    const int G = groups_for(p.n), lanes = JOIN_THREADS / G, g = tid / lanes, nth = tid % lanes;
+    float m = group_best[nth * G + ((g + 11 * nth) & (G - 1))];
     for (int d = lanes >> 1; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
     __syncthreads();
     if (tid % lanes == 0) group_best[g] = m;
@@ -591,8 +609,9 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_beam_join(const BeamParams p) 
   }
   if (tid < p.beams && state[tid] == RUNS) {
     const float2 near = near_of[tid];
-    const float f = bound_s - near.x + near.y;  // below it no logit reaches the bound
-    floor_of[tid] = bound_s > -INF && fabsf(near.x) <= FLT_MAX ? f - (fabsf(f) + fabsf(bound_s) + fabsf(near.x) + fabsf(near.y)) * 0x1p-21f : -INF;
+    const float d = bound_s - near.x;
+    floor_of[tid] = bound_s > -INF && fabsf(near.x) <= FLT_MAX
+                        ? d - (fabsf(bound_s) + fabsf(near.x) + fabsf(d)) * 0x1p-21f - 2.0f * off_of[tid] : -INF;
   }
   Cand least = {0, 0};  // what is not below it is wanted
   __syncthreads();
@@ -626,6 +645,36 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_beam_join(const BeamParams p) 
     __syncthreads();
   };
 
+  // Whether a logit, or a cell's largest, may be one of the n.
+  auto may_be = [&](int k, float x) { return x - near_of[k].y >= floor_of[k] && x >= -FLT_MAX && x <= FLT_MAX; };
+  // Behind a prune: each beam's lowest logit that goes before the last of the kept
+  // ones (in the last one's own beam the logit itself, up to its token), so that
+  // thousands of equal ones are passed over by a comparison.
+  auto cut = [&]() {
+    if (least.score && tid < p.beams && state[tid] == RUNS) {
+      const int of = beam_of(least);
+      auto before = [&](float x) {
+        const unsigned long long s = ordered(base[tid] + ((double)x - ref[tid]));
+        return s > least.score || (s == least.score && tid < of);
+      };
+      float x = (float)(unordered(least.score) - base[tid] + ref[tid]);
+      int left = 64;  // steps; it is a place or two away
+      limit_of[tid] = INT_MAX;
+      if (tid == of) {
+        cut_of[tid] = unordered((uint32_t)(least.tie >> 24));
+        limit_of[tid] = token_of(least);
+      } else if (before(x)) {
+        float below = nextafterf(x, -INF);
+        while (left-- && before(below)) x = below, below = nextafterf(x, -INF);
+        cut_of[tid] = left < 0 ? -INF : x;
+      } else {
+        while (left-- && !before(x)) x = nextafterf(x, INF);
+        cut_of[tid] = x;  // what is below is known to be worse
+      }
+    }
+    __syncthreads();
+  };
+
   // ---- the cells that reach it, and their logits
   const int rounds = p.seg_len * AHEAD, cell_vecs = rounds << p.quad_log;
   const int vecs = (p.vocab + N - 1) / N;
@@ -634,8 +683,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_beam_join(const BeamParams p) 
   for (int i = 0; i < CELL_LOADS; ++i) {
     const int c = 4 * (tid + i * JOIN_THREADS), k = row_of(c);
     if (c >= all_cells || state[k] != RUNS) continue;
-    const float least_x = fmaxf(floor_of[k], -FLT_MAX);
-    hits |= ((cell[i].x >= least_x) | (cell[i].y >= least_x) << 1 | (cell[i].z >= least_x) << 2 | (cell[i].w >= least_x) << 3) << 4 * i;
+    hits |= (may_be(k, cell[i].x) | may_be(k, cell[i].y) << 1 | may_be(k, cell[i].z) << 2 | may_be(k, cell[i].w) << 3) << 4 * i;
   }
   auto choose = [&](unsigned h) {  // false: there was no room
     if (h == 0) return true;
@@ -669,51 +717,73 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_beam_join(const BeamParams p) 
     else if (i < v1) r.count = min(N, p.vocab - r.token);
     return r;
   };
-  auto look = [&](bool turns) {  // into the chosen ones; false: more was wanted than is kept
+  auto push = [&](int k, float x, int token) {  // false: there is no room
+    const Cand c = value(k, x, token);
+    if (better(least, c)) return true;
+    const int o = atomicAdd(&count_s, 1);
+    if (o < KEEP) kept[o] = c;
+    return o < KEEP;
+  };
+  auto look = [&]() {  // into the chosen ones; false: more was wanted than is kept
     const int items = chosen_s * cell_vecs;
     bool full = false;
     Item next = fetch(tid, items);
 #pragma unroll 1
-    for (int i0 = 0; i0 < items; i0 += JOIN_THREADS) {
+    for (int i0 = 0; i0 < items && !full; i0 += JOIN_THREADS) {
       const Item now = next;
       if (i0 + JOIN_THREADS < items) next = fetch(i0 + JOIN_THREADS + tid, items);
-      const float least_x = floor_of[now.beam];
+      const float ref_x = near_of[now.beam].y, least_d = floor_of[now.beam];
       unsigned wanted = 0;  // of its tokens
       if (now.count < 0) {
         float x[N];
         Vec<T>::floats(now.v, x);
 #pragma unroll
-        for (int e = 0; e < N; ++e) wanted |= (x[e] >= least_x) << e;
+        for (int e = 0; e < N; ++e) wanted |= (x[e] - ref_x >= least_d) << e;
       } else {
         wanted = (1u << now.count) - 1;
       }
       const Row<T, ALIGNED> in = {p.logits + (b * p.beams + now.beam) * p.row_bytes, p.vocab};
 #pragma unroll 1
-      for (int e = 0; turns ? e < N : wanted != 0; ++e) {  // in turns: one token a thread
-        if (turns) {
-          __syncthreads();
-          if (count_s + JOIN_THREADS > KEEP) prune();  // leaves at most DFLASH_BEAM_MAX_N
-          __syncthreads();
-          if (!(wanted >> e & 1)) continue;
-        }
-        const int bit = turns ? e : __ffs(wanted) - 1;
-        wanted &= ~(1u << bit);
-        const float x = in.at(now.token + bit);
-        if (!(x >= least_x && x >= -FLT_MAX && x <= FLT_MAX)) continue;
-        const Cand c = value(now.beam, x, now.token + bit);
-        if (better(least, c)) continue;
-        const int o = atomicAdd(&count_s, 1);
-        if (o < KEEP) kept[o] = c;
-        else full = true;
+      for (; wanted; wanted &= wanted - 1) {
+        const int token = now.token + __ffs(wanted) - 1;
+        const float x = in.at(token);
+        if (may_be(now.beam, x)) full |= !push(now.beam, x, token);
       }
     }
     return !__syncthreads_or(full);
+  };
+  // The same, however many are wanted: a token of each thread in turns, pruned
+  // between them.
+  auto look_in_turns = [&]() {
+    const int items = chosen_s * cell_vecs;
+#pragma unroll 1
+    for (int i0 = 0; i0 < items; i0 += JOIN_THREADS) {
+      const Item now = fetch(i0 + tid, items);
+      const int count = now.count < 0 ? N : now.count;
+      const Row<T, ALIGNED> in = {p.logits + (b * p.beams + now.beam) * p.row_bytes, p.vocab};
+#pragma unroll 1
+      for (int e = 0; e < N; ++e) {
+        const int token = now.token + e;
+        const float x = e < count ? in.at(token) : -INF;
+        const bool wanted = may_be(now.beam, x) &&
+                            (x > cut_of[now.beam] || (x == cut_of[now.beam] && token < limit_of[now.beam]));
+        const int pushers = __syncthreads_count(wanted);
+        if (pushers == 0) continue;
+        if (count_s + pushers > KEEP / 2) {  // leaves at most DFLASH_BEAM_MAX_N; looked at by all before it is changed
+          prune();
+          cut();
+        }
+        __syncthreads();
+        if (wanted) push(now.beam, x, token);
+        __syncthreads();
+      }
+    }
   };
   // All of them at once; or, where there is no room for the cells or for what they
   // hold, a load of every thread at a time, in turns.
   const int before = count_s;
   const bool room = choose(hits);
-  if (__syncthreads_or(!room) || !look(false)) {
+  if (__syncthreads_or(!room) || !look()) {
 #pragma unroll 1
     for (int i = 0; i < CELL_LOADS; ++i) {
       __syncthreads();
@@ -724,7 +794,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_beam_join(const BeamParams p) 
       __syncthreads();
       choose(hits & 15u << 4 * i);
       __syncthreads();
-      look(true);
+      look_in_turns();
     }
   }
 
