@@ -647,8 +647,9 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) k_compact(const Pool p, int* 
 // Bound by memory: every byte is read and written once.  A work item is some
 // 16 KB of one page in one pool, four 16-byte vectors a thread in flight; items
 // go round the CTAs.  The number of copies is known on the device only.
-constexpr int COPY_THREADS = 256;
+constexpr int COPY_THREADS = 128;
 constexpr int COPY_AHEAD = 4;
+constexpr int COPY_CTAS = 16;    // of an SM
 constexpr int COPY_CACHES = 64;  // of a launch
 
 struct PoolAt {
@@ -913,7 +914,7 @@ int dflash_pages_copy(const dflash_paged_cache* caches, int32_t n_caches, const 
       p.pool[2 * i] = {static_cast<char*>(c.k), 2 * c.k_page_stride, 2 * c.k_pos_stride, 2 * c.k_head_stride};
       p.pool[2 * i + 1] = {static_cast<char*>(c.v), 2 * c.v_page_stride, 2 * c.v_pos_stride, 2 * c.v_head_stride};
     }
-    const unsigned grid = (unsigned)std::min<long long>(152 * 8, most * p.n_pools * p.chunks);
+    const unsigned grid = (unsigned)std::min<long long>(152 * COPY_CTAS, most * p.n_pools * p.chunks);
     const int e = vec ? launch(k_copy_pages<uint4>, dim3(grid), COPY_THREADS, 0, 1, stream, p)
                       : launch(k_copy_pages<uint16_t>, dim3(grid), COPY_THREADS, 0, 1, stream, p);
     if (e) return e;
