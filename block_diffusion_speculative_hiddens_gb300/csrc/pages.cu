@@ -796,6 +796,8 @@ int launch(void (*k)(P...), dim3 grid, int threads, size_t smem, int cluster, vo
   return cuda_status(cudaLaunchKernelEx(&cfg, k, static_cast<P>(args)...));
 }
 
+constexpr int MAX_MOVES = 1 << 30;  // of a list that a call fills
+
 // CTAs that scan refs: a step of 128 pages a warp each, at most eight.
 int scan_ctas(int n_pages) {
   int c = 1;
@@ -846,7 +848,7 @@ int dflash_pages_resize(const dflash_page_pool* c, const int32_t* new_lens, int3
                         void* stream) {
   if (int e = pool_check(c)) return e;
   if (!new_lens || !moves || capacity < 0 || !words(new_lens) || !words(moves)) return DFLASH_ERR_INVALID_ARG;
-  if (capacity < c->batch) return DFLASH_ERR_CAPACITY;
+  if (capacity < c->batch || capacity > MAX_MOVES) return DFLASH_ERR_CAPACITY;
   const PoolParts w = pool_parts(c);
   if (!apart({w.refs, w.table, w.lens, w.status, strided_ints(moves, 3 + 3ll * capacity)},
              {strided_ints(new_lens, c->batch)}))
@@ -867,7 +869,7 @@ int dflash_pages_resize(const dflash_page_pool* c, const int32_t* new_lens, int3
 int dflash_pages_compact(const dflash_page_pool* c, int32_t* moves, int32_t capacity, int32_t* remap, void* stream) {
   if (int e = pool_check(c)) return e;
   if (!moves || !remap || capacity < 0 || !words(moves) || !words(remap)) return DFLASH_ERR_INVALID_ARG;
-  if (capacity < c->n_pages / 2) return DFLASH_ERR_CAPACITY;
+  if (capacity < c->n_pages / 2 || capacity > MAX_MOVES) return DFLASH_ERR_CAPACITY;
   const PoolParts w = pool_parts(c);
   if (!apart({w.refs, w.table, w.status, strided_ints(moves, 3 + 3ll * capacity), strided_ints(remap, c->n_pages)}, {w.lens}))
     return DFLASH_ERR_INVALID_ARG;

@@ -639,7 +639,7 @@ DFLASH_API int dflash_pool_read_status(const dflash_page_pool* pool, uint32_t* o
  * its table row (DFLASH_DEV_CAPACITY) or whose old or new length is negative or,
  * the old one, past the row (DFLASH_DEV_ARG) stays as it is, alone.  A held entry
  * outside the pool, or given up where nobody holds it, is left out of the count
- * and sets DFLASH_DEV_PAGE.  capacity >= batch, else DFLASH_ERR_CAPACITY. */
+ * and sets DFLASH_DEV_PAGE.  batch <= capacity <= 2^30, else DFLASH_ERR_CAPACITY. */
 DFLASH_API int dflash_pages_resize(const dflash_page_pool* pool, const int32_t* new_lens, int32_t* moves, int32_t capacity,
                                    void* stream);
 
@@ -659,7 +659,7 @@ DFLASH_API int dflash_pages_fork(const dflash_page_pool* pool, const int32_t* pa
  * page numbers that the caller keeps elsewhere.  Run dflash_pages_copy before the
  * cache is used again.  A sequence whose length does not fit its table row keeps its
  * entries and sets DFLASH_DEV_ARG; so does, with DFLASH_DEV_PAGE, a held entry that is
- * outside the pool or whose page is free.  capacity >= n_pages / 2, else DFLASH_ERR_CAPACITY. */
+ * outside the pool or whose page is free.  n_pages / 2 <= capacity <= 2^30, else DFLASH_ERR_CAPACITY. */
 DFLASH_API int dflash_pages_compact(const dflash_page_pool* pool, int32_t* moves, int32_t capacity, int32_t* remap,
                                     void* stream);
 

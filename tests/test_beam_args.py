@@ -73,6 +73,8 @@ def test_pool_calls_refuse_before_any_cuda_call(lib):
         assert calls["compact"](p, moves=odd) == 1 and calls["compact"](p, remap=odd) == 1
     assert calls["resize"](p, room=3) == 4 and calls["resize"](p, room=2) == 3 and calls["resize"](p, room=-1) == 1
     assert calls["compact"](p, room=4) == 4 and calls["compact"](p, room=3) == 3 and calls["compact"](p, room=-1) == 1
+    for call in (calls["resize"], calls["compact"]):  # more room than indexes reach
+        assert call(p, moves=1 << 40, room=1 << 30) == 4 and call(p, moves=1 << 40, room=(1 << 30) + 1) == 3
     assert calls["compact"](_pool(pages=9), room=4) == 4 and calls["compact"](_pool(pages=1), room=0) == 4
     for at in ((1 << 20) + 28, (1 << 21) + 4, (1 << 22) + 8, 1 << 23, (1 << 23) + 4, (1 << 20) - 8):  # the pool's own
         assert calls["fork"](p, at) == 1 and calls["resize"](p, at) == 1 and calls["resize"](p, moves=at) == 1

@@ -528,6 +528,26 @@ def test_selection_past_32_bits(ops):
     assert torch.equal(got[2][5], beam_selected(logits[20:24], scores[5:6], 6))
 
 
+@pytest.mark.parametrize("dtype,beams", [(F32, 1), (BF16, 3), (F16, 40)], ids=["f32", "bf16", "f16"])
+def test_the_largest_vocabulary(ops, dtype, beams):
+    """Rows of 2^24 tokens, their best ones where cells are widest: at the ends, across parts, next to one another."""
+    vocab = 1 << 24
+    logits = torch.randn(beams, vocab, generator=gen(beams), device="cuda", dtype=dtype)
+    for k in range(beams):
+        for i, at in enumerate((0, 1, vocab // 3, vocab // 2 - 1, vocab // 2, vocab - 2, vocab - 1)):
+            logits[k, at] = 12 + (i + k) % 7
+    scores = -torch.arange(float(beams), device="cuda").view(1, beams) / 64
+    s, p, t = ops.beam_select(logits, scores, 9)
+    x = logits.double()
+    flat = (x - torch.logsumexp(x, -1, keepdim=True) + scores.double().view(-1, 1)).flatten()
+    at = p[0].long() * vocab + t[0].long()
+    best = torch.topk(flat, 9).values
+    assert len(set(at.tolist())) == 9
+    # the sums' terms are 2^24 in number: what a thread adds up, 2^24 / (32 * 256), is the longest run of them
+    assert ((flat[at] - best).abs() <= 2 * beam_ref.select_tolerance(16.0, 2 ** 24 / 8192)).all()
+    assert ((s[0].double() - best).abs() <= beam_ref.select_tolerance(16.0, 2 ** 24 / 8192)).all()
+
+
 def beam_selected(logits, scores, n):
     return i32([t for _, _, t in beam_ref.select(logits, scores, n)[0]])
 
