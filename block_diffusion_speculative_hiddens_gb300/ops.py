@@ -41,6 +41,7 @@ recorded.
 from __future__ import annotations
 
 import ctypes
+import functools
 import struct
 
 import torch
@@ -546,6 +547,11 @@ def copy_pages(caches, moves, *, stream=None):
 
 # ---- beam search
 
+@functools.lru_cache(maxsize=256)
+def _beam_bytes(batch, beams, vocab, n, kind):
+    return load().dflash_beam_select_workspace(batch, beams, vocab, n, kind)
+
+
 def beam_select(logits, scores, n: int = None, *, done=None, done_token: int = 0, out=None, status=None, workspace=None,
                 stream=None):
     """The n best (default: as many as beams) continuations of each request among
@@ -598,9 +604,8 @@ def beam_select(logits, scores, n: int = None, *, done=None, done_token: int = 0
             if _graded(t):
                 _no_gradient("out")
     best, parents, tokens = out
-    lib = load()
     if workspace is None:
-        nbytes = lib.dflash_beam_select_workspace(batch, beams, vocab, n, kind)
+        nbytes = _beam_bytes(batch, beams, vocab, n, kind)
         if nbytes:
             workspace = _empty(nbytes, torch.uint8, logits, stream)
     elif workspace.dtype is not torch.uint8 or workspace.get_device() != device or not workspace.is_contiguous():
@@ -611,7 +616,7 @@ def beam_select(logits, scores, n: int = None, *, done=None, done_token: int = 0
     args = _BEAM.pack(logits.data_ptr(), logits.stride(0), scores.data_ptr(), ended, best.data_ptr(), parents.data_ptr(),
                       tokens.data_ptr(), word, 0 if workspace is None else workspace.data_ptr(), nbytes, batch, beams, vocab, n,
                       _int32(done_token, "done_token"), kind, device, 0)
-    code = lib.dflash_beam_select(args, raw)
+    code = load().dflash_beam_select(args, raw)
     if code:
         raise DflashError("dflash_beam_select", code)
     return out
@@ -621,4 +626,4 @@ def beam_workspace(batch: int, beams: int, vocab: int, n: int, dtype) -> int:
     """Bytes of workspace that beam_select() of this shape needs."""
     if dtype not in _LOGITS:
         raise ValueError(f"dtype: expected float16, bfloat16 or float32, got {dtype}")
-    return load().dflash_beam_select_workspace(batch, beams, vocab, n, _LOGITS[dtype])
+    return _beam_bytes(batch, beams, vocab, n, _LOGITS[dtype])
