@@ -29,7 +29,10 @@
 // chose again (the scan's ends took 7,000 cycles a part: 37 and 9.5 us, but 26.5 for
 // the masked rows); vectors looked into two or four at a time (27 us for the masked
 // rows, 36.9 and 8.6 for the others); one batch of loads on its way (38.3 us); 128
-// bits compared as one integer (no faster); log() (1.1 us of a join).
+// bits compared as one integer (no faster); log() (1.1 us of a join); twice the cells
+// in a join's registers (27.1 us for the masked rows, but 41 for the batch and 10.7 for
+// one request) or two thirds of them (36 for the masked rows); the cells in shared
+// memory, by asynchronous copies (38.0, 9.0 and 13.5 for the odd rows, which take 12.1).
 #include <algorithm>
 #include <cfloat>
 #include <climits>
