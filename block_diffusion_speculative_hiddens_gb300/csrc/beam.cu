@@ -18,21 +18,23 @@
 // a warp's and a row's a 64-bit fixed-point number.
 //
 // Measured in graphs of six calls (bf16, 151,936 tokens).  64 requests of 8 beams,
-// 156 MB: 37.3 us, 23 of them the logits' at the copy rate; the scan alone 29 to 31,
+// 156 MB: 37.1 us, 23 of them the logits' at the copy rate; the scan alone 29 to 31,
 // 512 CTAs of a row each on 608 places (two or three parts a row: 39 to 42 us in all,
 // an odd number of CTAs an SM costs less than the parts' ends), then 4 to 5 of join
 // behind it.  One request of 4 beams 8.7 us: 3.5 of scan, 5 of join, a chain of some
 // twenty dependent steps of 100 to 1,000 cycles each.  Rows at odd addresses (f16,
-// 100,003 tokens, 11 x 5) 12.1 us; f32, 3 x 32 beams, n 64, 98 % masked 29 us, 9 of
-// scan: three CTAs look into 80 cells of 96 vectors each.
+// 100,003 tokens, 11 x 5) 12.0 us; f32, 3 x 32 beams, n 64, 98 % masked 22.7 us, 9 of
+// scan: three CTAs look into 80 cells of 96 vectors each (28.9 with a vector a thread
+// in turns and scores at once, 24.3 with four vectors on their way, 23.8 with eight,
+// which spill).
 // Tried and left: the n best of every part chosen in the scan, from which the join
 // chose again (the scan's ends took 7,000 cycles a part: 37 and 9.5 us, but 26.5 for
-// the masked rows); vectors looked into two or four at a time (27 us for the masked
-// rows, 36.9 and 8.6 for the others); one batch of loads on its way (38.3 us); 128
-// bits compared as one integer (no faster); log() (1.1 us of a join); twice the cells
-// in a join's registers (27.1 us for the masked rows, but 41 for the batch and 10.7 for
-// one request) or two thirds of them (36 for the masked rows); the cells in shared
-// memory, by asynchronous copies (38.0, 9.0 and 13.5 for the odd rows, which take 12.1).
+// the masked rows); one batch of loads on its way (38.3 us); 128 bits compared as one
+// integer (no faster); log() (1.1 us of a join); more registers a join (80: 35.8 us for
+// the batch, but 35.4 instead of 29.8 for 220 requests of 2, one CTA an SM); twice the
+// cells in a join's registers (41 for the batch, 10.7 for one request) or two thirds of
+// them (7 us more for the masked rows); the cells in shared memory, by asynchronous
+// copies (38.0, 9.0, and 13.5 for the odd rows).
 #include <algorithm>
 #include <cfloat>
 #include <climits>
@@ -50,7 +52,7 @@ constexpr int SLOTS = 152 * SCAN_CTAS;  // CTAs that run at once
 constexpr int AHEAD = 4;          // vectors of a thread's batch
 constexpr int MAX_SEGMENTS = 8;   // of a part, with cells of their own
 constexpr int MAX_SPLITS = 32;    // parts of a row: a lane each when they are joined
-constexpr int JOIN_THREADS = 512;
+constexpr int JOIN_LOG = 9, JOIN_THREADS = 1 << JOIN_LOG;
 constexpr int CELL_LOADS = 6;     // of a thread of the join: four cells each, held in registers
 constexpr int CELLS = 4 * CELL_LOADS * JOIN_THREADS;  // of a request
 constexpr int CHOSEN = 4 * JOIN_THREADS;  // cells that are looked into at a time: a load of every thread, at least
@@ -486,7 +488,7 @@ DFL_DEV int rank_lanes(int count) {
 }
 
 template <int T, bool ALIGNED>
-__global__ void __launch_bounds__(JOIN_THREADS) k_beam_join(const BeamParams p) {
+__global__ void __launch_bounds__(JOIN_THREADS, 2) k_beam_join(const BeamParams p) {
   constexpr int N = Vec<T>::N;
   const float INF = __uint_as_float(0x7f800000u);
   enum { DEAD, RUNS, ENDED };
@@ -716,58 +718,104 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_beam_join(const BeamParams p) 
     }
     return true;
   };
-  struct Item {  // a vector of a chosen cell
-    uint4 v;
-    int token, beam;
-    int count;  // of its tokens, -1: all of them, in v
+  auto vector_of = [&](int first, int nth) {  // of a cell: its nth
+    return first + (nth >> p.quad_log) * SCAN_THREADS + (nth & (p.quad - 1));
   };
-  auto fetch = [&](int it, int items) {
-    Item r = {};
-    if (it >= items) return r;
-    const int o = it / cell_vecs, nth = it - o * cell_vecs;
-    const int2 c = chosen[o];
-    const int i = c.x + (nth >> p.quad_log) * SCAN_THREADS + (nth & (p.quad - 1)), v1 = c.y & 0x1ffffff;
-    r.beam = c.y >> 25;
-    r.token = i * N;
-    const Row<T, ALIGNED> in = {p.logits + (b * p.beams + r.beam) * p.row_bytes, p.vocab};
-    if (i > 0 && i < min(v1, in.inner())) r.v = in.load(i), r.count = -1;
-    else if (i < v1) r.count = min(N, p.vocab - r.token);
-    return r;
-  };
-  auto push = [&](int k, float x, int token) {  // false: there is no room
-    const Cand c = value(k, x, token);
-    if (better(least, c)) return true;
-    const int o = atomicAdd(&count_s, 1);
-    if (o < KEEP) kept[o] = c;
-    return o < KEEP;
-  };
-  auto look = [&]() {  // into the chosen ones; false: more was wanted than is kept
-    const int items = chosen_s * cell_vecs;
-    bool full = false;
-    Item next = fetch(tid, items);
-#pragma unroll 1
-    for (int i0 = 0; i0 < items && !full; i0 += JOIN_THREADS) {
-      const Item now = next;
-      if (i0 + JOIN_THREADS < items) next = fetch(i0 + JOIN_THREADS + tid, items);
-      const float ref_x = near_of[now.beam].y, least_d = floor_of[now.beam];
-      unsigned wanted = 0;  // of its tokens
-      if (now.count < 0) {
-        float x[N];
-        Vec<T>::floats(now.v, x);
+  const int before = count_s;
+  // A vector's tokens that are not below the floor; at an end of the row all of them.
+  auto wanted_of = [&](const Row<T, ALIGNED>& in, int i, bool inside, const uint4& v, float ref_x, float least_d) {
+    unsigned w = 0;
+    if (inside) {
+      float x[N];
+      Vec<T>::floats(v, x);
 #pragma unroll
-        for (int e = 0; e < N; ++e) wanted |= (x[e] - ref_x >= least_d) << e;
-      } else {
-        wanted = (1u << now.count) - 1;
-      }
-      const Row<T, ALIGNED> in = {p.logits + (b * p.beams + now.beam) * p.row_bytes, p.vocab};
+      for (int e = 0; e < N; ++e) w |= (x[e] - ref_x >= least_d) << e;
+    } else {
+      w = (1u << min(N, p.vocab - i * N)) - 1;
+    }
+    return w;
+  };
+  // Into the chosen cells.  False: more was wanted than is kept.
+  auto look = [&]() {
+    const int cells_n = chosen_s, items = cells_n * cell_vecs;
+    bool full = false;
+    if (items <= JOIN_THREADS) {  // a vector each: 0.3 us less than teams would take
+      const int o = tid / cell_vecs;
+      if (o < cells_n) {
+        const int2 c = chosen[o];
+        const int k = c.y >> 25, v1 = c.y & 0x1ffffff, i = vector_of(c.x, tid - o * cell_vecs);
+        const Row<T, ALIGNED> in = {p.logits + (b * p.beams + k) * p.row_bytes, p.vocab};
+        const bool inside = i > 0 && i < min(v1, in.inner());
+        uint4 v = {};
+        if (inside) v = in.load(i);
+        unsigned wanted = i < v1 ? wanted_of(in, i, inside, v, near_of[k].y, floor_of[k]) : 0;
 #pragma unroll 1
-      for (; wanted; wanted &= wanted - 1) {
-        const int token = now.token + __ffs(wanted) - 1;
-        const float x = in.at(token);
-        if (may_be(now.beam, x)) full |= !push(now.beam, x, token);
+        for (; wanted; wanted &= wanted - 1) {
+          const int token = i * N + __ffs(wanted) - 1;
+          const float x = in.at(token);
+          if (!may_be(k, x)) continue;
+          const Cand r = value(k, x, token);
+          const int to = atomicAdd(&count_s, 1);
+          if (to < KEEP) kept[to] = r;
+          else full = true;
+        }
+      }
+      return !__syncthreads_or(full);
+    }
+    // A team of threads a cell, LOOKS vectors of a thread on their way at once.  The
+    // scores wait for the end, a thread each: a 64-bit sum takes some 400 cycles.
+    constexpr int LOOKS = ALIGNED ? 6 : 4;
+    const int least_log = min(4, 32 - __clz(cell_vecs - 1));
+    const int team_log = max(least_log, JOIN_LOG - (32 - __clz(cells_n - 1)));
+    const int team = 1 << team_log, at = tid & (team - 1);
+#pragma unroll 1
+    for (int o = tid >> team_log; o < cells_n && !full; o += JOIN_THREADS >> team_log) {
+      const int2 c = chosen[o];
+      const int k = c.y >> 25, v1 = c.y & 0x1ffffff;
+      const Row<T, ALIGNED> in = {p.logits + (b * p.beams + k) * p.row_bytes, p.vocab};
+      const int inner = min(v1, in.inner());
+      const float ref_x = near_of[k].y, least_d = floor_of[k];
+#pragma unroll 1
+      for (int nth = at; nth < cell_vecs && !full; nth += team * LOOKS) {
+        uint4 v[LOOKS][1];
+#pragma unroll
+        for (int u = 0; u < LOOKS; ++u) {
+          const int i = vector_of(c.x, nth + u * team);
+          if (nth + u * team < cell_vecs && i > 0 && i < inner) v[u][0] = in.load(i);
+        }
+        unsigned hits = 0;  // vectors that may hold one; those at the row's ends are gone through
+#pragma unroll
+        for (int u = 0; u < LOOKS; ++u) {
+          const int i = vector_of(c.x, nth + u * team);
+          const bool inside = i > 0 && i < inner;
+          if (nth + u * team < cell_vecs && i < v1) hits |= (!inside || Vec<T>::top(v[u]) - ref_x >= least_d) << u;
+        }
+#pragma unroll 1
+        for (; hits; hits &= hits - 1) {
+          const int i = vector_of(c.x, nth + (__ffs(hits) - 1) * team);
+          const bool inside = i > 0 && i < inner;
+          uint4 again = {};
+          if (inside) again = in.load(i);
+#pragma unroll 1
+          for (unsigned wanted = wanted_of(in, i, inside, again, ref_x, least_d); wanted; wanted &= wanted - 1) {
+            const int token = i * N + __ffs(wanted) - 1;
+            const float x = in.at(token);
+            if (!may_be(k, x)) continue;
+            const int to = atomicAdd(&count_s, 1);
+            if (to < KEEP) kept[to] = {__float_as_uint(x), (unsigned long long)k << 32 | (unsigned)token};
+            else full = true;
+          }
+        }
       }
     }
-    return !__syncthreads_or(full);
+    if (__syncthreads_or(full)) return false;
+#pragma unroll 1
+    for (int i = before + tid; i < count_s; i += JOIN_THREADS) {
+      const Cand raw = kept[i];
+      kept[i] = value((int)(raw.tie >> 32), __uint_as_float((uint32_t)raw.score), (int)(uint32_t)raw.tie);
+    }
+    __syncthreads();
+    return true;
   };
   // The same, however many are wanted: a token of each thread in turns, pruned
   // between them.
@@ -775,15 +823,21 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_beam_join(const BeamParams p) 
     const int items = chosen_s * cell_vecs;
 #pragma unroll 1
     for (int i0 = 0; i0 < items; i0 += JOIN_THREADS) {
-      const Item now = fetch(i0 + tid, items);
-      const int count = now.count < 0 ? N : now.count;
-      const Row<T, ALIGNED> in = {p.logits + (b * p.beams + now.beam) * p.row_bytes, p.vocab};
+      int k = 0, first = 0, count = 0;  // of a vector: beam, token, tokens
+      if (i0 + tid < items) {
+        const int o = (i0 + tid) / cell_vecs;
+        const int2 c = chosen[o];
+        const int i = vector_of(c.x, i0 + tid - o * cell_vecs);
+        k = c.y >> 25;
+        first = i * N;
+        if (i < (c.y & 0x1ffffff)) count = min(N, p.vocab - first);
+      }
+      const Row<T, ALIGNED> in = {p.logits + (b * p.beams + k) * p.row_bytes, p.vocab};
 #pragma unroll 1
       for (int e = 0; e < N; ++e) {
-        const int token = now.token + e;
+        const int token = first + e;
         const float x = e < count ? in.at(token) : -INF;
-        const bool wanted = may_be(now.beam, x) &&
-                            (x > cut_of[now.beam] || (x == cut_of[now.beam] && token < limit_of[now.beam]));
+        const bool wanted = may_be(k, x) && (x > cut_of[k] || (x == cut_of[k] && token < limit_of[k]));
         const int pushers = __syncthreads_count(wanted);
         if (pushers == 0) continue;
         if (count_s + pushers > KEEP / 2) {  // leaves at most DFLASH_BEAM_MAX_N; looked at by all before it is changed
@@ -791,14 +845,16 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_beam_join(const BeamParams p) 
           cut();
         }
         __syncthreads();
-        if (wanted) push(now.beam, x, token);
+        if (wanted) {
+          const Cand c = value(k, x, token);
+          if (!better(least, c)) put(c);
+        }
         __syncthreads();
       }
     }
   };
   // All of them at once; or, where there is no room for the cells or for what they
   // hold, a load of every thread at a time, in turns.
-  const int before = count_s;
   const bool room = choose(hits);
   if (__syncthreads_or(!room) || !look()) {
 #pragma unroll 1

@@ -477,6 +477,22 @@ def test_selection_of_strided_rows_at_every_alignment(ops, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f16", "f32"])
+@pytest.mark.parametrize("at,n", [(0, 48), (0, 128), (1, 48), (3, 128)])
+def test_selection_from_many_large_cells(ops, dtype, at, n):
+    """More vectors to look into again than the join has threads, candidates at the rows' ends, ended beams between."""
+    batch, beams, vocab = 2, 24, 90001
+    g = gen(n + at)
+    logits = (torch.randn(batch * beams, 90008, generator=g, device="cuda") * 2.5).to(dtype)[:, at:at + vocab]
+    logits[::5, 0] = 14
+    logits[1::7, vocab - 1] = 13
+    logits[3, 700:760] = 12.5  # one after another, equal
+    scores = -2 * torch.rand(batch, beams, generator=g, device="cuda")
+    done = torch.rand(batch, beams, generator=g, device="cuda") < 0.2
+    check_select(ops, logits, scores, n)
+    check_select(ops, logits, scores, n, done, 5)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f16", "f32"])
 def test_ties_go_to_the_lowest_beam_and_token(ops, dtype):
     vocab = 9001
     flat = torch.zeros(4, vocab, dtype=dtype, device="cuda")
