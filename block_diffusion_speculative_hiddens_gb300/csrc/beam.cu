@@ -62,6 +62,9 @@ constexpr int KEEP = 1024;        // candidates that are kept at a time
 constexpr float LOG2E_HI = 1.44269502162933349609f;
 constexpr float LOG2E_LO = 1.92596299112661746887e-8f;
 constexpr double LN2 = 0.693147180559945309417232121458;
+// Logits below it have an integer reference within 2 of their exponent: x * LOG2E_HI
+// is then off by 1 at most, from 2^28 on by tens, and a term could be anything.
+constexpr float EXACT = 0x1p24f;
 
 // What a part of a row leaves: the sum of exp(x - reference).  The reference is
 // q * ln 2 if `base2`, else the part's largest logit (which is too large or too
@@ -361,7 +364,9 @@ __global__ void __launch_bounds__(SCAN_THREADS, SCAN_CTAS) k_beam_scan(const Bea
   float part_top = warp_top[0], part_q = warp_q[0];
 #pragma unroll
   for (int w = 1; w < WARPS; ++w) part_top = fmaxf(part_top, warp_top[w]), part_q = fmaxf(part_q, warp_q[w]);
-  const bool plain = !any_odd && (part_top == -INF || part_q > -1e30f);
+  // Threads without a logit near the part's largest may have references that are off
+  // by more (masks of the type's lowest value): their sums are shifted out.
+  const bool plain = !any_odd && (part_top == -INF || fabsf(part_top) < EXACT);
   if (!plain) {
     // NaN, infinity, or logits whose exponent does not fit: once more, against the largest finite one
     auto clean = [&](float x) { return x <= FLT_MAX ? x : -INF; };
