@@ -28,22 +28,33 @@ DFL_DEV int pages_of(int len, int shift) { return (int)(((unsigned)len + (1u << 
 DFL_DEV bool len_fits(const Pool& p, int len) { return len >= 0 && pages_of(len, p.shift) <= p.max_pages; }
 
 // One holder more and less of each of four entries' pages, those with their bit
-// set.  Whether a page is pinned does not change during a call, and a page given up
-// has a holder until then.
-DFL_DEV void count_entries(const Pool& p, const int (&more)[4], unsigned m, const int (&less)[4], unsigned l) {
-  int rm[4], rl[4];
+// set.  Whether a page is pinned does not change during a call, so it is looked up
+// once; without `pins` none of the pool's pages is.  A page given up has a holder
+// until then, or its count was too low: the value that the subtraction found says so
+// (two entries may both take away the last holder), and the one goes back.
+DFL_DEV void count_entries(const Pool& p, const int (&more)[4], unsigned m, const int (&less)[4], unsigned l, bool pins) {
+  int rm[4], was[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {  // all of them on their way at once; outside the pool: as if nobody held it
+  for (int j = 0; j < 4; ++j)  // all of them on their way at once
     rm[j] = m >> j & 1 && (unsigned)more[j] < (unsigned)p.n_pages ? __ldcg(p.refs + more[j]) : INT_MIN;
-    rl[j] = l >> j & 1 ? (unsigned)less[j] < (unsigned)p.n_pages ? __ldcg(p.refs + less[j]) : 0 : INT_MIN;
+  if (pins) {
+    int rl[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) rl[j] = l >> j & 1 && (unsigned)less[j] < (unsigned)p.n_pages ? __ldcg(p.refs + less[j]) : 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) l &= ~((unsigned)(rl[j] < 0) << j);
   }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)  // outside the pool: as if nobody held it
+    was[j] = l >> j & 1 ? (unsigned)less[j] < (unsigned)p.n_pages ? atomicSub(p.refs + less[j], 1) : 0 : 1;
   bool bad = false;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     if (rm[j] >= 0) atomicAdd(p.refs + more[j], 1);
     bad |= m >> j & 1 && (unsigned)more[j] >= (unsigned)p.n_pages;
-    if (rl[j] > 0) atomicSub(p.refs + less[j], 1);
-    bad |= rl[j] == 0;
+    if (was[j] > 0) continue;
+    if ((unsigned)less[j] < (unsigned)p.n_pages) atomicAdd(p.refs + less[j], 1);
+    bad |= was[j] == 0;  // who finds it below 0 came behind one who found it 0
   }
   if (bad) dev_error(p.status, DFLASH_DEV_PAGE);
 }
@@ -107,7 +118,7 @@ DFL_DEV void change_entries(const Pool& p, int b, int col, const Step& s, const 
   }
   if (!differ) return;
   int* at = p.table + b * p.stride + col;
-  count_entries(p, n, differ & entries_below(s.has - col), w, differ & entries_below(s.had - col));
+  count_entries(p, n, differ & entries_below(s.has - col), w, differ & entries_below(s.had - col), true);
   if (vec && col + 4 <= p.max_pages) {
     *reinterpret_cast<int4*>(at) = make_int4(out[0], out[1], out[2], out[3]);
   } else {
@@ -198,10 +209,10 @@ DFL_DEV uint32_t ld_dsmem_u32(uint32_t addr) {
   return v;
 }
 
-DFL_DEV int4 load_refs(const int* refs, int i, int end, bool vec) {
+// behind: what is read behind the end.
+DFL_DEV int4 load_refs(const int* refs, int i, int end, bool vec, int behind) {
   if (vec && i + 4 <= end) return __ldcg(reinterpret_cast<const int4*>(refs + i));
-  // behind the end: pages that are neither free nor held
-  int4 v = make_int4(-1, -1, -1, -1);
+  int4 v = make_int4(behind, behind, behind, behind);
   if (i < end) v.x = __ldcg(refs + i);
   if (i + 1 < end) v.y = __ldcg(refs + i + 1);
   if (i + 2 < end) v.z = __ldcg(refs + i + 2);
@@ -342,7 +353,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) k_resize(const Pool p, const 
   extern __shared__ __align__(16) char smem[];
   __shared__ unsigned long long sums[SCAN_WARPS + 1];
   __shared__ int counts[SCAN_WARPS + 1];
-  __shared__ int shrinks;
+  __shared__ int shrinks, pinned;
   Change* seq = reinterpret_cast<Change*>(smem);                      // [batch]
   uint32_t* copies = reinterpret_cast<uint32_t*>(seq + p.batch);     // [batch]
   Sharers shared;
@@ -356,10 +367,10 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) k_resize(const Pool p, const 
     shared.page[i] = -1;
     shared.who[i] = 0xffffu;
   }
-  if (threadIdx.x == 0) shrinks = 0;
+  if (threadIdx.x == 0) shrinks = pinned = 0;
   pdl_wait();
   const Part part = scan_part(p.n_pages, ctas, rank);
-  const int4 head = load_refs(p.refs, part.first + 4 * lane, part.end, vec);  // on its way meanwhile
+  const int4 head = load_refs(p.refs, part.first + 4 * lane, part.end, vec, 1);  // on its way meanwhile; behind the end: held
   __syncthreads();
 
   // every CTA goes through the whole batch, a thread a few sequences in a row
@@ -423,14 +434,17 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) k_resize(const Pool p, const 
   }
 
   // the free pages
-  auto refs_at = [&](int i) { return i == part.first ? head : load_refs(p.refs, i + 4 * lane, part.end, vec); };
+  auto refs_at = [&](int i) { return i == part.first ? head : load_refs(p.refs, i + 4 * lane, part.end, vec, 1); };
   int mine = 0;
 #pragma unroll 1
   for (int i = part.first; i < part.end; i += 128) {
     const int4 r = refs_at(i);
     mine += (r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0);
+    if (min(min(r.x, r.y), min(r.z, r.w)) < 0) pinned = 1;
   }
   const Before found = cluster_before(warp_total(mine), counts, ctas, rank);
+  // whether any page of the pool is pinned: if not, what is given up need not be looked up first
+  const bool pins = __any_sync(0xffffffffu, lane < ctas && ld_dsmem_u32(dsmem_addr(smem_u32(&pinned), lane)));
   const bool fits = want <= (unsigned long long)found.total;
 
   // moves: their number, and nothing behind the last
@@ -514,7 +528,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) k_resize(const Pool p, const 
       for (int u = 0; u < ABREAST; ++u) {
         if (!lost[u]) continue;
         const int id[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-        count_entries(p, id, 0, id, lost[u]);
+        count_entries(p, id, 0, id, lost[u], pins);
         if (tvec && lost[u] == 15) {
           *reinterpret_cast<int4*>(row[u]) = make_int4(-1, -1, -1, -1);
         } else {
@@ -527,7 +541,8 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) k_resize(const Pool p, const 
   }
 #pragma unroll 1
   for (int b = tid; b < p.batch; b += ctas * SCAN_THREADS) {
-    if ((copies[b] & COPIED) && (copies[b] & COUNTED)) atomicSub(p.refs + seq[b].page, 1);
+    const int page[4] = {seq[b].page};
+    count_entries(p, page, 0, page, (copies[b] & COPIED) && (copies[b] & COUNTED), false);
     if (seq[b].had >= 0) p.lens[b] = new_lens[b];
   }
 }
@@ -583,8 +598,8 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) k_compact(const Pool p, int* 
   pdl_launch_dependents();
   pdl_wait();
   const Part part = scan_part(p.n_pages, ctas, rank);
-  const int4 head = load_refs(p.refs, part.first + 4 * lane, part.end, vec);
-  auto refs_at = [&](int i) { return i == part.first ? head : load_refs(p.refs, i + 4 * lane, part.end, vec); };
+  const int4 head = load_refs(p.refs, part.first + 4 * lane, part.end, vec, -1);
+  auto refs_at = [&](int i) { return i == part.first ? head : load_refs(p.refs, i + 4 * lane, part.end, vec, -1); };
   int f = 0, h = 0;
 #pragma unroll 1
   for (int i = part.first; i < part.end; i += 128) {

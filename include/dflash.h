@@ -638,8 +638,8 @@ DFLASH_API int dflash_pool_read_status(const dflash_page_pool* pool, uint32_t* o
  * empty and DFLASH_DEV_CAPACITY is set.  A sequence whose new length does not fit
  * its table row (DFLASH_DEV_CAPACITY) or whose old or new length is negative or,
  * the old one, past the row (DFLASH_DEV_ARG) stays as it is, alone.  A held entry
- * outside the pool, or given up where nobody holds it, is left out of the count
- * and sets DFLASH_DEV_PAGE.  batch <= capacity <= 2^30, else DFLASH_ERR_CAPACITY. */
+ * outside the pool, or given up where nobody holds it (any more: counts that are
+ * too low end at 0), is left out of the count and sets DFLASH_DEV_PAGE.  batch <= capacity <= 2^30, else DFLASH_ERR_CAPACITY. */
 DFLASH_API int dflash_pages_resize(const dflash_page_pool* pool, const int32_t* new_lens, int32_t* moves, int32_t capacity,
                                    void* stream);
 
@@ -647,8 +647,10 @@ DFLASH_API int dflash_pages_resize(const dflash_page_pool* pool, const int32_t* 
  * before the call: its pages and length; what it held itself is given up.  -1: it
  * ends and is empty.  Any map: a beam search's, a prompt's row handed to many, a
  * permutation.  A parent outside [-1, batch), or one whose length does not fit
- * the table row, leaves the sequence as it is and sets DFLASH_DEV_ARG.  No page
- * is copied: resize does that for the sequences that grow. */
+ * the table row, leaves the sequence as it is and sets DFLASH_DEV_ARG.  Entries
+ * outside the pool or without a holder as for resize; of counts that are too low
+ * it is open whether new holders come before those that leave.  No page is
+ * copied: resize does that for the sequences that grow. */
 DFLASH_API int dflash_pages_fork(const dflash_page_pool* pool, const int32_t* parents, void* stream);
 
 /* Move pages so that those in use are the first ones of the pools, as far as

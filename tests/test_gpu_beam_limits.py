@@ -1,9 +1,10 @@
 """Selection and page calls at the limits of what they accept: logits too large for
-a shared exponent."""
+a shared exponent, counts that are too low."""
 import pytest
 import torch
 
-from tests.test_gpu_beam import BF16, F32, check_select, gen
+from tests import beam_ref
+from tests.test_gpu_beam import BF16, F32, PAGE, check_select, gen, i32, make_pool, step
 
 pytestmark = pytest.mark.gpu
 
@@ -42,3 +43,79 @@ def test_rows_of_large_logits(ops, dtype, value):
         check_select(ops, flat, torch.zeros(2, 2, device="cuda"), 40, exact=True)
         near = (sign * value * (1 - 0.1 * torch.rand(3, 20011, generator=g, device="cuda"))).to(dtype)
         check_select(ops, near, -torch.rand(1, 3, generator=g, device="cuda"), 10)
+
+
+# ------------------------------------------------------------------ counts that are too low
+
+def shared(ops, batch, held):
+    """A pool whose first `held` rows hold the same three pages, the others nothing."""
+    pool = make_pool(ops, batch, 4, 4 * batch + 8)
+    ref = beam_ref.Pool.of(pool)
+    step(ops, pool, ref, "resize", [40] + [0] * (batch - 1))
+    step(ops, pool, ref, "fork", [0 if b < held else -1 for b in range(batch)])
+    return pool, ref
+
+
+def recount(pool, ref, counts):
+    for p, n in zip(ref.table[0], counts):
+        ref.refs[p] = n
+        pool.refs[p] = n
+
+
+@pytest.mark.parametrize("batch", [2, 3, 40, 600, 1500])
+def test_counts_that_are_too_low_do_not_pin_pages(ops, batch):
+    """More entries give up a page than it has holders: flagged, the count ends at 0, and the page is free."""
+    for counts in ((1, 1, 1), (0, batch - 1, 1)):
+        for what, arg in (("resize", [0] * batch), ("fork", [-1] * batch)):
+            pool, ref = shared(ops, batch, batch)
+            recount(pool, ref, counts)
+            step(ops, pool, ref, what, arg, PAGE)
+            assert not any(ref.refs) and min(pool.refs.tolist()) == 0
+            step(ops, pool, ref, "resize", [b % 60 for b in range(batch)])  # and serves again
+            ref.check()
+
+
+def status_of(ref, what, arg):
+    want = beam_ref.Pool(ref.refs, ref.table, ref.lens, ref.page)
+    getattr(want, what)(arg)
+    return want.status
+
+
+@pytest.mark.parametrize("batch", [3, 4, 40, 600])
+def test_counts_that_are_too_low_and_copies(ops, batch):
+    """All of them grow in a page that has two holders by its count: each but the first gives it up."""
+    pool, ref = shared(ops, batch, batch)
+    recount(pool, ref, (batch, batch, 2))
+    grown = [41] * batch
+    assert status_of(ref, "resize", grown) == (PAGE if batch > 3 else 0)
+    step(ops, pool, ref, "resize", grown, PAGE if batch > 3 else 0)
+
+
+@pytest.mark.parametrize("batch", [6, 64, 1500])
+def test_counts_that_are_too_low_and_new_holders(ops, batch):
+    """In which order a fork counts them is open: the count ends between all that are left and 0."""
+    keeps, first = batch // 2 - 1, batch - batch // 3  # the only row of the old ones that stays; the new ones
+    pool, ref = shared(ops, batch, keeps + 1)
+    recount(pool, ref, (1, 2, keeps))
+    pages = ref.table[0][:3]
+    parents = [keeps if b == keeps or b >= first else -1 for b in range(batch)]
+    ops.fork(pool, i32(parents))
+    status = pool.read_status()
+    ref.fork(parents)
+    assert pool.page_table.tolist() == ref.table and pool.lens.tolist() == ref.lens
+    assert all(ref.refs[p] <= pool.refs[p].item() <= batch - first + 1 for p in pages)
+    assert status == PAGE or (status == ref.status and pool.refs.tolist() == ref.refs)
+
+
+@pytest.mark.parametrize("batch", [3, 600, 1500])
+def test_pins_of_every_size(ops, batch):
+    """Pinned pages that many take and give up in one call keep their counts, the lowest values among them."""
+    pins = (-1, -2 ** 31, -2 ** 31 + 5)
+    pool, ref = shared(ops, batch, 1)
+    recount(pool, ref, pins)
+    some = [0 if b % 3 else -1 for b in range(batch)]
+    some[0] = 0
+    for what, arg in (("fork", [0] * batch), ("fork", some), ("fork", [0] * batch), ("resize", [20 if b % 2 else 40 for b in range(batch)]),
+                      ("fork", [0] * batch), ("resize", [41] * batch), ("resize", [0] * batch)):
+        step(ops, pool, ref, what, arg)
+        assert [ref.refs[p] for p in range(3)] == list(pins)
