@@ -18,6 +18,7 @@ Which sequence holds which page, around a step of the whole model:
 
     pool = PagePool(page_table, n_pages, page_size)        # once a model
     copy_pages(caches, resize(pool, new_lens))             # room for the new tokens; every layer's cache
+    ctx_len = torch.where(pool.lens == new_lens, ctx_len, -2 ** 31)  # for those that got it
     ...                                                    # the layers: append, attention
     resize(pool, confirmed)                                # what was not confirmed is given back
 
@@ -487,7 +488,10 @@ def resize(pool: PagePool, new_lens, *, moves=None, stream=None):
     grows inside a page which others hold gets a copy of it.  Returns the copies to
     make, moves int32 [1 + batch, 3]: their number in row 0, then (source page,
     destination page, positions) -- for copy_pages, ahead of the first append.  Not
-    enough free pages: nothing changes, DEV_CAPACITY in the pool's status."""
+    enough free pages: nothing changes, DEV_CAPACITY in the pool's status.  Nothing may
+    then be appended: a sequence whose pool.lens is not its new length has no room, its
+    positions lie in pages that others hold.  Give append and attention ctx_len -2**31
+    for it, as above, and its rows are not written."""
     raw = _raw_stream(stream, pool.device)
     new = _i32(new_lens, "new_lens", pool.batch, pool.device)
     moves, capacity = _moves(moves, pool.batch, pool, stream)

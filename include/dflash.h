@@ -635,11 +635,18 @@ DFLASH_API int dflash_pool_read_status(const dflash_page_pool* pool, uint32_t* o
  * are free from the next one on.  Run dflash_pages_copy before anything is
  * written to the new lengths.
  * If fewer pages are free than the call takes, nothing changes at all, moves is
- * empty and DFLASH_DEV_CAPACITY is set.  A sequence whose new length does not fit
+ * empty and DFLASH_DEV_CAPACITY is set.  Nothing may then be written at the new
+ * positions: they lie in pages that other sequences hold, or in none that the
+ * sequence holds, and an append goes there all the same.  lens tells on the device:
+ * where it is not new_lens behind the call, hand dflash_paged_append and
+ * dflash_paged_attention INT32_MIN for ctx_len (and 0 for kv_len, if it is given);
+ * the sequence's rows are then not written and see nothing, and the append sets
+ * DFLASH_DEV_PAGE in the cache's status.  A sequence whose new length does not fit
  * its table row (DFLASH_DEV_CAPACITY) or whose old or new length is negative or,
  * the old one, past the row (DFLASH_DEV_ARG) stays as it is, alone.  A held entry
  * outside the pool, or given up where nobody holds it (any more: counts that are
- * too low end at 0), is left out of the count and sets DFLASH_DEV_PAGE.  batch <= capacity <= 2^30, else DFLASH_ERR_CAPACITY. */
+ * too low end at 0), is left out of the count and sets DFLASH_DEV_PAGE.
+ * batch <= capacity <= 2^30, else DFLASH_ERR_CAPACITY. */
 DFLASH_API int dflash_pages_resize(const dflash_page_pool* pool, const int32_t* new_lens, int32_t* moves, int32_t capacity,
                                    void* stream);
 

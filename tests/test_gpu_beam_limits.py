@@ -1,10 +1,10 @@
 """Selection and page calls at the limits of what they accept: logits too large for
-a shared exponent, counts that are too low."""
+a shared exponent, counts that are too low, calls that find no pages."""
 import pytest
 import torch
 
 from tests import beam_ref
-from tests.test_gpu_beam import BF16, F32, PAGE, check_select, gen, i32, make_pool, step
+from tests.test_gpu_beam import BF16, F32, I32, PAGE, check_select, gen, i32, make_pool, step
 
 pytestmark = pytest.mark.gpu
 
@@ -119,3 +119,61 @@ def test_pins_of_every_size(ops, batch):
                       ("fork", [0] * batch), ("resize", [41] * batch), ("resize", [0] * batch)):
         step(ops, pool, ref, what, arg)
         assert [ref.refs[p] for p in range(3)] == list(pins)
+
+
+# ------------------------------------------------------------------ no pages
+
+@pytest.mark.parametrize("n_pages,fail", [(8, 3), (4, 16)])
+def test_nothing_is_appended_to_sequences_without_room(ops, n_pages, fail):
+    """A captured step of beams on shared pages, replayed where their pool is used up, or too small for the copies
+    from the start: its rows have no place, what the cache holds stays as it was, and pages that are given back serve
+    again."""
+    rows, page, hkv, dim = 4, 16, 2, 64
+    g = gen(31)
+    table = torch.zeros(rows, 6, dtype=I32, device="cuda")
+    cache = ops.PagedCache(*(torch.randn(n_pages, page, hkv, dim, generator=g, device="cuda").to(BF16) for _ in range(2)), table)
+    pool = ops.PagePool(table, n_pages, page)
+    ops.resize(pool, i32([20, 0, 0, 0]))
+    ops.fork(pool, i32([0, 0, 0, 0]))  # two pages, the last of them to be copied
+    ref = beam_ref.Pool.of(pool)
+    k, v, q = (torch.randn(rows, hkv, dim, generator=g, device="cuda").to(BF16) for _ in range(3))
+    cu = i32(range(rows + 1))
+    out = torch.empty_like(q)
+
+    def one(step):
+        ctx = pool.lens.clone()
+        new = ctx + step
+        ops.copy_pages(cache, ops.resize(pool, new))
+        ctx = torch.where(pool.lens == new, ctx, -2 ** 31)
+        ops.append(cache, k, v, cu, ctx)
+        ops.attention(cache, q, cu, ctx, out=out)
+
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        one(1)
+
+    def kept():  # what each sequence holds
+        return [torch.cat([p[t].flatten(0, 1)[:n] for p in (cache.k_pool, cache.v_pool)])
+                for t, n in ((table[b].long().clamp(0, n_pages - 1), n) for b, n in enumerate(pool.lens.tolist()))]
+
+    failed = 0
+    for turn in range(16):
+        before, pools = kept(), [cache.k_pool.clone(), cache.v_pool.clone()]
+        new = [n + 1 for n in ref.lens]
+        ref.resize(new)
+        graph.replay()
+        assert pool.lens.tolist() == ref.lens and pool.read_status() == ref.status
+        if ref.status:
+            failed += 1
+            assert torch.equal(cache.k_pool, pools[0]) and torch.equal(cache.v_pool, pools[1])
+            assert cache.read_status() == PAGE and not out.any()
+        else:
+            for b, (x, y, n) in enumerate(zip(before, kept(), ref.lens)):
+                x, y = x.view(2, n - 1, hkv, dim), y.view(2, n, hkv, dim)
+                assert torch.equal(x, y[:, :-1]) and torch.equal(y[0, -1], k[b]) and torch.equal(y[1, -1], v[b])
+            assert cache.read_status() == 0 and out.abs().sum(-1).min() > 0
+        ref.status = 0
+        if turn == 14:  # one ends
+            step(ops, pool, ref, "fork", [-1, 1, 2, 3])
+    assert failed == fail
