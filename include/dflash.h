@@ -686,7 +686,7 @@ DFLASH_API int dflash_pages_copy(const dflash_paged_cache* caches, int32_t n_cac
  *   scores[b][k] + logits[b * beams + k][v] - log sum_w exp(logits[b * beams + k][w]),
  * best first.  Scores are compared in 64 bits; of equal ones the lowest k goes
  * first, of one beam's the larger logit, then the lower token.  The sums of
- * exponentials are held in 32 bits a thread and 64 beyond.
+ * exponentials are held in 32 bits over 256 terms at most and in 64 beyond.
  * A beam with done set offers itself alone: done_token, at its score.  A score of
  * -inf is a beam without continuations, a logit of -inf a token that is not
  * offered; NaN and +inf count as -inf and set DFLASH_DEV_NAN.  Where fewer than n

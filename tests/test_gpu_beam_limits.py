@@ -1,10 +1,11 @@
 """Selection and page calls at the limits of what they accept: logits too large for
-a shared exponent, counts that are too low, calls that find no pages."""
+a shared exponent, the longest sums, counts that are too low, calls that find no
+pages."""
 import pytest
 import torch
 
 from tests import beam_ref
-from tests.test_gpu_beam import BF16, F32, I32, PAGE, check_select, gen, i32, make_pool, step
+from tests.test_gpu_beam import BF16, F16, F32, I32, PAGE, check_select, gen, i32, make_pool, step
 
 pytestmark = pytest.mark.gpu
 
@@ -43,6 +44,32 @@ def test_rows_of_large_logits(ops, dtype, value):
         check_select(ops, flat, torch.zeros(2, 2, device="cuda"), 40, exact=True)
         near = (sign * value * (1 - 0.1 * torch.rand(3, 20011, generator=g, device="cuda"))).to(dtype)
         check_select(ops, near, -torch.rand(1, 3, generator=g, device="cuda"), 10)
+
+
+# ------------------------------------------------------------------ long sums
+
+@pytest.mark.parametrize("dtype,most,tops", [
+    (F16, -0.59375, (3.0, 3.125, 3.25, 3.375, 3.5)), (BF16, 0.4375, (3.0, 3.125, 3.25, 3.375, 3.5)),
+    (F32, -1.46875, (3.0, 3.125, 3.25, 3.375, 3.5)), (F32, 2.0 ** 24 + 2, (2.0 ** 24 + 4,))],
+    ids=["f16", "bf16", "f32", "large"])
+def test_sums_of_the_longest_rows(ops, dtype, most, tops):
+    """320 rows of 2^24 tokens, too many to be split: thousands of equal terms a thread, whose roundings add up in a
+    32-bit sum that takes them all."""
+    vocab, batch, beams, n = 1 << 24, 5, 64, 8
+    row = torch.full((1, vocab), most, dtype=dtype, device="cuda")
+    at = (0, vocab // 3, vocab // 2, vocab - 2, vocab - 1)[:len(tops)]
+    for token, x in zip(at, tops):
+        row[0, token] = x
+    scores = -0.0101 * torch.arange(float(beams), device="cuda").repeat(batch, 1)
+    s, p, t = ops.beam_select(row.expand(batch * beams, vocab), scores, n)
+    lse = torch.logsumexp(row[0].double(), 0).item()
+    want = sorted(((b + x - lse, -k, token) for k, b in enumerate(scores[0].tolist()) for token, x in zip(at, tops)), reverse=True)[:n]
+    for b in range(batch):
+        assert t[b].tolist() == [w[2] for w in want] and p[b].tolist() == [b * beams - w[1] for w in want]
+        for got, (x, _, _) in zip(s[b].tolist(), want):
+            # a thread's two floats take 256 terms each at most before they are added to a 64-bit sum:
+            # units of 2^-34, at most 2^15 roundings of half of one beside a sum above 1/2
+            assert abs(got - x) <= beam_ref.select_tolerance(x, 512) + 2.0 ** -19, (b, got, x)
 
 
 # ------------------------------------------------------------------ counts that are too low
