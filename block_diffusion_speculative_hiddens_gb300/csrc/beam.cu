@@ -388,53 +388,74 @@ __global__ void __launch_bounds__(SCAN_THREADS, SCAN_CTAS) k_beam_scan(const Bea
   if (!plain) {
     // NaN, infinity, or logits whose exponent does not fit: once more, against the largest finite one
     auto clean = [&](float x) { return x <= FLT_MAX ? x : -INF; };
-    auto each = [&](int from, int to, auto&& f) {  // this thread's logits of some rounds
-#pragma unroll 1
-      for (int r = from; r < to; ++r) {
-        const int i = v0 + r * SCAN_THREADS + tid;
-        if (i >= v1) break;
-        if (i > 0 && i < inner) {
-          float x[N];
-          Vec<T>::floats(in.load(i), x);
-#pragma unroll
-          for (int e = 0; e < N; ++e) f(x[e]);
-        } else {
-#pragma unroll 1
-          for (int token = i * N; token < min(p.vocab, (i + 1) * N); ++token) f(in.at(token));
-        }
-      }
-    };
-    bool bad = false;
-    whole = -INF;
     __syncthreads();  // the maxima are read
+    if (any_odd) {  // the cells' maxima without what is not finite
+      auto each = [&](int from, int to, auto&& f) {  // this thread's logits of some rounds
 #pragma unroll 1
-    for (int i = 0; i < p.segments; ++i) {
-      top = -INF;
-      each(i * p.seg_len * AHEAD, (i + 1) * p.seg_len * AHEAD, [&](float x) {
-        bad |= !(x <= FLT_MAX);
-        top = fmaxf(top, clean(x));
-      });
-      __syncwarp();
-      close(i);
-    }
-    if (bad) flag_nan(p.status);
-    whole = warp_max(whole);
-    if (lane == 0) warp_top[warp] = whole, warp_q[warp] = 0.0f;
-    __syncthreads();
-    part_top = warp_top[0];
+        for (int r = from; r < to; ++r) {
+          const int i = v0 + r * SCAN_THREADS + tid;
+          if (i >= v1) break;
+          if (i > 0 && i < inner) {
+            float x[N];
+            Vec<T>::floats(in.load(i), x);
 #pragma unroll
-    for (int w = 1; w < WARPS; ++w) part_top = fmaxf(part_top, warp_top[w]);
+            for (int e = 0; e < N; ++e) f(x[e]);
+          } else {
+#pragma unroll 1
+            for (int token = i * N; token < min(p.vocab, (i + 1) * N); ++token) f(in.at(token));
+          }
+        }
+      };
+      bool bad = false;
+      whole = -INF;
+#pragma unroll 1
+      for (int i = 0; i < p.segments; ++i) {
+        top = -INF;
+        each(i * p.seg_len * AHEAD, (i + 1) * p.seg_len * AHEAD, [&](float x) {
+          bad |= !(x <= FLT_MAX);
+          top = fmaxf(top, clean(x));
+        });
+        __syncwarp();
+        close(i);
+      }
+      if (bad) flag_nan(p.status);
+      whole = warp_max(whole);
+      if (lane == 0) warp_top[warp] = whole;
+      __syncthreads();
+      part_top = warp_top[0];
+#pragma unroll
+      for (int w = 1; w < WARPS; ++w) part_top = fmaxf(part_top, warp_top[w]);
+    }
     part_q = 0.0f;
     unsigned long long f = 0;
+    s = 0.0f;
+    k = v0 + tid;
+    auto term = [&](float x) {
+      const float d = clean(x) - part_top;
+      s += ex2(fmaf(d, LOG2E_HI, d * LOG2E_LO));
+    };
 #pragma unroll 1
-    for (int r = 0; r < batches && part_top > -INF; r += FOLD) {
-      s = 0.0f;
-      each(r * AHEAD, min(r + FOLD, batches) * AHEAD, [&](float x) { s += expf(clean(x) - part_top); });
-      f += fixed(s);
+    for (int b = 0; b < batches && part_top > -INF; ++b) {
+      fetch(even);
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) {
+        float x[N];
+        Vec<T>::floats(even[j], x);
+#pragma unroll
+        for (int e = 0; e < N; ++e) term(x[e]);
+      }
+      if ((b + 1) % FOLD == 0) f += fixed(s), s = 0.0f;
     }
+#pragma unroll 1
+    for (int i = v0 == 0 ? 0 : max(inner, v0); i < v1 && part_top > -INF; i = max(inner, i + 1)) {  // the row's ends
+      if ((i - v0) % SCAN_THREADS != tid) continue;
+#pragma unroll 1
+      for (int token = i * N; token < min(p.vocab, (i + 1) * N); ++token) term(in.at(token));
+    }
+    f += fixed(s);
     __syncwarp();
     f = total(f);
-    if (lane == 0) warp_sum[warp] = f;
+    if (lane == 0) warp_sum[warp] = f, warp_q[warp] = 0.0f;
     __syncthreads();
   }
   const long long at = row * p.splits + part;
