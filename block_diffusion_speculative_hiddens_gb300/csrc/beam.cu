@@ -14,8 +14,8 @@
 // takes a logit goes by its index alone.
 //
 // Sums: exponents are taken to base 2 against an integer reference, so that sums
-// join by exact shifts.  A thread's sum is two floats of 256 terms each at most, then
-// a 64-bit fixed-point number, as a warp's and a row's is (floats that took all of a
+// join by shifts.  A thread's sum is two floats of 256 terms each at most, then a
+// 64-bit fixed-point number, as a warp's and a row's is (floats that took all of a
 // long row's 32,768 terms were off by up to 5e-4).
 //
 // Measured in graphs of six calls (bf16, 151,936 tokens).  64 requests of 8 beams,
@@ -64,21 +64,27 @@ constexpr int KEEP = 1024;        // candidates that are kept at a time
 constexpr float LOG2E_HI = 1.44269502162933349609f;
 constexpr float LOG2E_LO = 1.92596299112661746887e-8f;
 constexpr double LN2 = 0.693147180559945309417232121458;
-// Logits below it have an integer reference within 2 of their exponent: x * LOG2E_HI
-// is then off by 1 at most, from 2^28 on by tens, and a term could be anything.
-constexpr float EXACT = 0x1p24f;
+// Logits below it have references that fit: the rounded x * LOG2E_HI is whole and
+// below 2^31, and within 65 of the logit's exponent (its unit is 128 there).
+constexpr float EXACT = 1.4e9f;
+
+// A sum of exponentials: units of 2^(q - FIX).
+struct Sum {
+  unsigned long long v;
+  int q;
+};
+constexpr int FIX = 34;
 
 // What a part of a row leaves: the sum of exp(x - reference).  The reference is
 // q * ln 2 if `base2`, else the part's largest logit (which is too large or too
 // small for the shared exponent).
 struct PartSum {
   unsigned long long sum;  // units of 2^-FIX
-  float q;
+  int q;
   float top;               // largest logit; -inf: no tokens are offered
   int base2;
   int reserved;
 };
-constexpr int FIX = 34;
 
 struct BeamParams {
   const char* logits;
@@ -242,6 +248,19 @@ DFL_DEV float pow2_or_0(float e) {  // 2^e for whole e <= 0, 0 where it is too s
   return e < -120.0f ? 0.0f : __uint_as_float((uint32_t)(127 + (int)e) << 23);
 }
 
+DFL_DEV unsigned long long shifted(unsigned long long v, unsigned by) { return by < 64 ? v >> by : 0; }
+// s * 2^q, s at or above 0: by its exponent, whatever it is.  Also 0 for an s or a q
+// that a part's largest logit does not leave.
+DFL_DEV Sum scaled(float s, float q) {
+  const uint32_t u = __float_as_uint(s);
+  if (!(s >= FLT_MIN) || fabsf(q) > 2.1e9f) return {0, INT_MIN};
+  return {(unsigned long long)((u & 0x7fffffu) | 0x800000u) << (FIX - 23), (int)q + (int)(u >> 23) - 127};
+}
+DFL_DEV Sum joined(const Sum& a, const Sum& b) {
+  const int q = max(a.q, b.q);
+  return {shifted(a.v, (unsigned)q - (unsigned)a.q) + shifted(b.v, (unsigned)q - (unsigned)b.q), q};
+}
+
 template <int T, bool ALIGNED>
 __global__ void __launch_bounds__(SCAN_THREADS, SCAN_CTAS) k_beam_scan(const BeamParams p) {
   constexpr int N = Vec<T>::N;
@@ -249,10 +268,10 @@ __global__ void __launch_bounds__(SCAN_THREADS, SCAN_CTAS) k_beam_scan(const Bea
   constexpr int BATCH = AHEAD * SCAN_THREADS;  // vectors of AHEAD rounds; a round is a vector a thread
   const float INF = __uint_as_float(0x7f800000u);
   __shared__ uint32_t cell[MAX_SEGMENTS * SCAN_THREADS];  // the part's, in order
-  __shared__ float warp_top[WARPS], warp_q[WARPS];
+  __shared__ float warp_top[WARPS];
+  __shared__ int warp_q[WARPS];
   __shared__ unsigned long long warp_sum[WARPS];
-  __shared__ unsigned long long held[SCAN_THREADS];  // a thread's sum but for its last terms, of units 2^-FIX
-  __shared__ float held_q[SCAN_THREADS];             // and its reference
+  __shared__ Sum held[SCAN_THREADS];  // a thread's sum but for its last terms
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int row = blockIdx.x / p.splits, part = blockIdx.x - row * p.splits;
@@ -297,16 +316,13 @@ __global__ void __launch_bounds__(SCAN_THREADS, SCAN_CTAS) k_beam_scan(const Bea
     unpair(fma2(x2, lo2, fma2(x2, hi2, ref)), a, b);
     sum2 = add2(sum2, pair(ex2(a), ex2(b)));
   };
-  auto fixed = [](float v) { return __float2ull_rn(v * (float)(1ull << FIX)); };
-  auto shifted = [](unsigned long long v, float by) { return by < 63.0f ? v >> (int)by : 0; };
   const bool folds = batches >= FOLD;
-  if (folds) held[tid] = 0, held_q[tid] = q;
+  if (folds) held[tid] = {0, INT_MIN};
   auto fold = [&]() {
     float a, b;
     unpair(sum2, a, b);
-    if (!(a + b < 0x1p29f)) return;  // stays what it is, and is seen below
-    held[tid] = shifted(held[tid], q - held_q[tid]) + fixed(a + b);
-    held_q[tid] = q;
+    if (!(a + b < 1e37f)) return;  // stays what it is, and is seen below
+    held[tid] = joined(held[tid], scaled(a + b, q));
     sum2 = pair(0.0f, 0.0f);
   };
   auto close = [&](int seg) {  // the segment's cells
@@ -372,18 +388,20 @@ __global__ void __launch_bounds__(SCAN_THREADS, SCAN_CTAS) k_beam_scan(const Bea
   s += s1;
   const bool odd = !(s < 1e37f);
   {
-    const float most = warp_max(s > 0.0f || (folds && held[tid]) ? q : -1e30f), m = warp_max(whole);
-    unsigned long long f = fixed(odd ? 0.0f : s * pow2_or_0(q - most));
-    if (folds) f += shifted(held[tid], most - held_q[tid]);
-    f = total(f);
+    Sum mine = scaled(odd ? 0.0f : s, q);
+    if (folds) mine = joined(mine, held[tid]);
+    const int most = __reduce_max_sync(0xffffffffu, mine.q);
+    const float m = warp_max(whole);
+    const unsigned long long f = total(shifted(mine.v, (unsigned)most - (unsigned)mine.q));
     if (lane == 0) warp_top[warp] = m, warp_q[warp] = most, warp_sum[warp] = f;
   }
   const bool any_odd = __syncthreads_or(odd);
-  float part_top = warp_top[0], part_q = warp_q[0];
+  float part_top = warp_top[0];
+  int part_q = warp_q[0];
 #pragma unroll
-  for (int w = 1; w < WARPS; ++w) part_top = fmaxf(part_top, warp_top[w]), part_q = fmaxf(part_q, warp_q[w]);
-  // Threads without a logit near the part's largest may have references that are off
-  // by more (masks of the type's lowest value): their sums are shifted out.
+  for (int w = 1; w < WARPS; ++w) part_top = fmaxf(part_top, warp_top[w]), part_q = max(part_q, warp_q[w]);
+  // Threads without a logit near the part's largest may have references that do not
+  // fit (masks of the type's lowest value): their sums are far below it.
   const bool plain = !any_odd && (part_top == -INF || fabsf(part_top) < EXACT);
   if (!plain) {
     // NaN, infinity, or logits whose exponent does not fit: once more, against the largest finite one
@@ -426,7 +444,8 @@ __global__ void __launch_bounds__(SCAN_THREADS, SCAN_CTAS) k_beam_scan(const Bea
 #pragma unroll
       for (int w = 1; w < WARPS; ++w) part_top = fmaxf(part_top, warp_top[w]);
     }
-    part_q = 0.0f;
+    part_q = 0;
+    auto fixed = [](float v) { return __float2ull_rn(v * (float)(1ull << FIX)); };
     unsigned long long f = 0;
     s = 0.0f;
     k = v0 + tid;
@@ -455,7 +474,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, SCAN_CTAS) k_beam_scan(const Bea
     f += fixed(s);
     __syncwarp();
     f = total(f);
-    if (lane == 0) warp_sum[warp] = f, warp_q[warp] = 0.0f;
+    if (lane == 0) warp_sum[warp] = f, warp_q[warp] = 0;
     __syncthreads();
   }
   const long long at = row * p.splits + part;
@@ -463,7 +482,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, SCAN_CTAS) k_beam_scan(const Bea
     unsigned long long sum = 0;
 #pragma unroll
     for (int w = 0; w < WARPS; ++w)
-      sum += shifted(warp_sum[w], part_q - warp_q[w]);
+      sum += shifted(warp_sum[w], (unsigned)part_q - (unsigned)warp_q[w]);
     const PartSum r = {sum, part_q, part_top, plain, 0};
     p.sums[at] = r;
   }
@@ -591,10 +610,10 @@ __global__ void __launch_bounds__(JOIN_THREADS, 2) k_beam_join(const BeamParams 
     const unsigned group = (W == 32 ? 0xffffffffu : (1u << W) - 1) << (lane & ~(W - 1));
     const bool any = __ballot_sync(0xffffffffu, some) & group;
     const bool bare = __ballot_sync(0xffffffffu, some && !part.base2) & group;
-    float q = some && part.base2 ? part.q : -INF;
-    for (int d = W >> 1; d; d >>= 1) q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, d));
+    int q = some && part.base2 ? part.q : INT_MIN;
+    for (int d = W >> 1; d; d >>= 1) q = max(q, __shfl_xor_sync(0xffffffffu, q, d));
     double r = q * LN2;
-    unsigned long long sum = some && q - part.q < 63.0f ? part.sum >> (int)(q - part.q) : 0;  // shifted to the largest reference
+    unsigned long long sum = some ? shifted(part.sum, (unsigned)q - (unsigned)part.q) : 0;  // shifted to the largest reference
     if (__any_sync(0xffffffffu, bare)) {  // ref is then a logit, or one of the powers of two
       double r2 = 0.0;
       const unsigned long long sum2 = sum_of_any(part, some, W, r2);

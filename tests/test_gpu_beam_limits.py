@@ -35,7 +35,7 @@ def test_one_large_logit_among_ordinary_ones(ops, dtype, value):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
-@pytest.mark.parametrize("value", [1e8, 1e9, 1.8e9, 2.0 ** 31, 2.5e9, 1e10])
+@pytest.mark.parametrize("value", [1.7e7, 6e7, 1e8, 4e8, 7e8, 1e9, 1.39e9, 1.41e9, 1.8e9, 2.0 ** 31, 2.5e9, 1e10])
 def test_rows_of_large_logits(ops, dtype, value):
     """Rows of one large value, of either sign, and of values close to it."""
     g = gen(22)
@@ -44,6 +44,26 @@ def test_rows_of_large_logits(ops, dtype, value):
         check_select(ops, flat, torch.zeros(2, 2, device="cuda"), 40, exact=True)
         near = (sign * value * (1 - 0.1 * torch.rand(3, 20011, generator=g, device="cuda"))).to(dtype)
         check_select(ops, near, -torch.rand(1, 3, generator=g, device="cuda"), 10)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("fill", [-1e4, -3e7, -1e9, -1.5e9, -1e10, -1e30, -3e38])
+def test_masks_of_every_size(ops, dtype, fill):
+    """Rows masked by a large negative value: wholly, but for a token, but for their beginning; more of them wanted
+    than are not masked."""
+    g = gen(23)
+    vocab = 70001
+    for at in (0, 1):
+        logits = (torch.randn(6, vocab + 7, generator=g, device="cuda") * 2).to(dtype)[:, at:at + vocab]
+        logits[0] = fill
+        logits[1, :vocab - 1] = fill
+        logits[2, 20000:] = fill
+        logits[3, torch.rand(vocab, generator=g, device="cuda") < 0.999] = fill
+        logits[4, 3:] = fill
+        scores = -torch.rand(2, 3, generator=g, device="cuda")
+        check_select(ops, logits, scores, 12)
+        check_select(ops, logits[4:5], scores[:1, :1].contiguous(), 8)
+        check_select(ops, logits[:1], scores[:1, :1].contiguous(), 8, exact=True)
 
 
 # ------------------------------------------------------------------ long sums
