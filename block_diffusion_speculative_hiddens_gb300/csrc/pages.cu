@@ -774,8 +774,10 @@ int pool_check(const dflash_page_pool* c) {
 }
 
 Pool pool_of(const dflash_page_pool* c) {
+  // entries that no length reaches are never looked at: at most 2^27, far from where indexes end
+  const int reached = 0x7fffffff / c->page_size + 1;
   return {c->refs, c->page_table, c->table_stride, c->lens, c->status, c->n_pages, page_shift(c->page_size),
-          c->max_pages, c->batch};
+          std::min(c->max_pages, reached), c->batch};
 }
 
 struct PoolParts {
@@ -846,18 +848,19 @@ int dflash_pages_fork(const dflash_page_pool* c, const int32_t* parents, void* s
   if (!apart({w.refs, w.table, w.lens, w.status}, {strided_ints(parents, c->batch)})) return DFLASH_ERR_INVALID_ARG;
   // Columns of a CTA: as many as give every thread one unit of four entries, but
   // no fewer than four: larger batches take several units a thread.
+  const Pool p = pool_of(c);
   int cols = 4;
-  while (cols * 2 * c->batch <= 4 * FORK_THREADS && cols < c->max_pages) cols *= 2;
+  while (cols * 2 * p.batch <= 4 * FORK_THREADS && cols < p.max_pages) cols *= 2;
   DeviceGuard guard(c->device);
   if (!guard.ok) return DFLASH_ERR_CUDA;
-  const dim3 grid((unsigned)((c->max_pages + cols - 1) / cols));
-  const int units = c->batch * (cols / 4);
+  const dim3 grid((unsigned)((p.max_pages + cols - 1) / cols));
+  const int units = p.batch * (cols / 4);
   if (units <= FORK_THREADS)
-    return launch(k_fork<true>, grid, (units + 31) / 32 * 32, 0, 1, stream, pool_of(c), parents, cols, table_vec(c));
+    return launch(k_fork<true>, grid, (units + 31) / 32 * 32, 0, 1, stream, p, parents, cols, table_vec(c));
   if (int e = cuda_status(cudaFuncSetAttribute(k_fork<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                DFLASH_POOL_MAX_BATCH * (int)sizeof(int4))))
     return e;
-  return launch(k_fork<false>, grid, FORK_THREADS, units * sizeof(int4), 1, stream, pool_of(c), parents, cols, table_vec(c));
+  return launch(k_fork<false>, grid, FORK_THREADS, units * sizeof(int4), 1, stream, p, parents, cols, table_vec(c));
 }
 
 int dflash_pages_resize(const dflash_page_pool* c, const int32_t* new_lens, int32_t* moves, int32_t capacity,
@@ -869,7 +872,8 @@ int dflash_pages_resize(const dflash_page_pool* c, const int32_t* new_lens, int3
   if (!apart({w.refs, w.table, w.lens, w.status, strided_ints(moves, 3 + 3ll * capacity)},
              {strided_ints(new_lens, c->batch)}))
     return DFLASH_ERR_INVALID_ARG;
-  if ((long long)c->batch * ((c->max_pages + 127ll) / 128) > 0x7fffffffll) return DFLASH_ERR_CAPACITY;
+  const Pool p = pool_of(c);
+  if ((long long)p.batch * ((p.max_pages + 127) / 128) > 0x7fffffffll) return DFLASH_ERR_CAPACITY;
   const size_t smem = resize_smem(c->batch);
   DeviceGuard guard(c->device);
   if (!guard.ok) return DFLASH_ERR_CUDA;
@@ -878,7 +882,7 @@ int dflash_pages_resize(const dflash_page_pool* c, const int32_t* new_lens, int3
                                                  (int)resize_smem(DFLASH_POOL_MAX_BATCH))))
       return e;
   const int ctas = scan_ctas(c->n_pages);
-  return launch(k_resize, dim3((unsigned)ctas), SCAN_THREADS, smem, ctas, stream, pool_of(c), new_lens, moves, capacity,
+  return launch(k_resize, dim3((unsigned)ctas), SCAN_THREADS, smem, ctas, stream, p, new_lens, moves, capacity,
                 ctas, resize_slots(c->batch), (reinterpret_cast<uintptr_t>(c->refs) & 15) == 0, table_vec(c));
 }
 
@@ -889,21 +893,22 @@ int dflash_pages_compact(const dflash_page_pool* c, int32_t* moves, int32_t capa
   const PoolParts w = pool_parts(c);
   if (!apart({w.refs, w.table, w.status, strided_ints(moves, 3 + 3ll * capacity), strided_ints(remap, c->n_pages)}, {w.lens}))
     return DFLASH_ERR_INVALID_ARG;
-  const int per_row = (c->max_pages + REMAP_THREADS * REMAP_EACH - 1) / (REMAP_THREADS * REMAP_EACH);
-  const long long blocks = (long long)per_row * c->batch;
+  const Pool p = pool_of(c);
+  const int per_row = (p.max_pages + REMAP_THREADS * REMAP_EACH - 1) / (REMAP_THREADS * REMAP_EACH);
+  const long long blocks = (long long)per_row * p.batch;
   if (blocks > 0x7fffffffll) return DFLASH_ERR_CAPACITY;
   DeviceGuard guard(c->device);
   if (!guard.ok) return DFLASH_ERR_CUDA;
   // A table of some pieces a warp is gone through by the same cluster; a larger one
   // by a grid of its own, which takes a launch more and has all SMs.
-  const long long pieces = (long long)((c->max_pages + 32 * REMAP_EACH - 1) / (32 * REMAP_EACH)) * c->batch;
+  const long long pieces = (long long)((p.max_pages + 32 * REMAP_EACH - 1) / (32 * REMAP_EACH)) * p.batch;
   const int ctas = scan_ctas((int)std::min<long long>(DFLASH_POOL_MAX_PAGES, std::max<long long>(c->n_pages, pieces * 128)));
   const bool with_table = pieces <= REMAP_PIECES * SCAN_WARPS * ctas;
-  if (int e = launch(k_compact, dim3((unsigned)ctas), SCAN_THREADS, 0, ctas, stream, pool_of(c), moves, capacity, remap, ctas,
+  if (int e = launch(k_compact, dim3((unsigned)ctas), SCAN_THREADS, 0, ctas, stream, p, moves, capacity, remap, ctas,
                      (reinterpret_cast<uintptr_t>(c->refs) & 15) == 0, with_table))
     return e;
   if (with_table) return DFLASH_OK;
-  return launch(k_remap, dim3((unsigned)blocks), REMAP_THREADS, 0, 1, stream, pool_of(c), remap, per_row);
+  return launch(k_remap, dim3((unsigned)blocks), REMAP_THREADS, 0, 1, stream, p, remap, per_row);
 }
 
 int dflash_pages_copy(const dflash_paged_cache* caches, int32_t n_caches, const int32_t* moves, int32_t capacity,

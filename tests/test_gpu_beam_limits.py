@@ -1,6 +1,6 @@
 """Selection and page calls at the limits of what they accept: logits too large for
 a shared exponent, the longest sums, counts that are too low, calls that find no
-pages."""
+pages, tables wider than any length."""
 import pytest
 import torch
 
@@ -224,3 +224,27 @@ def test_nothing_is_appended_to_sequences_without_room(ops, n_pages, fail):
         if turn == 14:  # one ends
             step(ops, pool, ref, "fork", [-1, 1, 2, 3])
     assert failed == fail
+
+
+# ------------------------------------------------------------------ wide tables
+
+def test_a_table_wider_than_any_length(ops):
+    """One row of 2^31 - 1 entries, most of which no length reaches."""
+    width, page = 2 ** 31 - 1, 16
+    table = torch.empty(1, width, dtype=I32, device="cuda")
+    table[:, :50] = -7
+    pool = ops.PagePool(table, 60, page)
+    new = i32([0])
+    for n in (700, 300, 301, 0, 640):
+        assert ops.resize(pool, new.fill_(n))[0, 0].item() == 0
+        held = -(-n // page)
+        assert pool.lens.item() == n and sorted(table[0, :held].tolist()) == list(range(held))
+        assert pool.refs.tolist() == [1] * held + [0] * (60 - held)
+    pool.refs[40:45] = pool.refs[:5].clone()
+    pool.refs[:5] = 0
+    table[0, :5] = i32([44, 43, 42, 41, 40])
+    moves, remap = ops.compact(pool)
+    assert moves[0, 0].item() == 5 and table[0, :40].tolist() == [4, 3, 2, 1, 0] + list(range(5, 40))
+    ops.fork(pool, i32([0]))
+    ops.fork(pool, i32([-1]))
+    assert not pool.refs.any() and (table[0, :40] == -1).all() and pool.lens.item() == 0 and pool.read_status() == 0
