@@ -471,6 +471,11 @@ class PagePool:
         return v.value
 
 
+def _copies(moves):
+    """Copies that a list has room for, as 32 bits hold them: no call makes more."""
+    return min(moves.shape[0] - 1, 2 ** 31 - 1)
+
+
 def _moves(moves, least, pool, stream):
     """Room for page copies -- the caller's, checked, or new -- and how many it takes."""
     if moves is None:
@@ -479,7 +484,7 @@ def _moves(moves, least, pool, stream):
             moves.shape[1] != 3 or moves.shape[0] < 1 + least or not moves.is_contiguous():
         raise ValueError(f"moves: expected contiguous int32 [at least {1 + least}, 3] on cuda:{pool.device}, got "
                          f"{list(moves.shape)} {moves.dtype} on {moves.device}")
-    return moves, moves.shape[0] - 1
+    return moves, _copies(moves)
 
 
 def resize(pool: PagePool, new_lens, *, moves=None, stream=None):
@@ -544,7 +549,7 @@ def copy_pages(caches, moves, *, stream=None):
         raise ValueError(f"moves: expected contiguous int32 [1 + copies, 3] on cuda:{device}, got {list(moves.shape)} "
                          f"{moves.dtype} on {moves.device}")
     packed = caches[0]._c if len(caches) == 1 else b"".join([c._c for c in caches])
-    code = load().dflash_pages_copy(packed, len(caches), moves.data_ptr(), moves.shape[0] - 1, raw)
+    code = load().dflash_pages_copy(packed, len(caches), moves.data_ptr(), _copies(moves), raw)
     if code:
         raise DflashError("dflash_pages_copy", code)
 
@@ -630,4 +635,4 @@ def beam_workspace(batch: int, beams: int, vocab: int, n: int, dtype) -> int:
     """Bytes of workspace that beam_select() of this shape needs."""
     if dtype not in _LOGITS:
         raise ValueError(f"dtype: expected float16, bfloat16 or float32, got {dtype}")
-    return _beam_bytes(batch, beams, vocab, n, _LOGITS[dtype])
+    return _beam_bytes(_int32(batch, "batch"), _int32(beams, "beams"), _int32(vocab, "vocab"), _int32(n, "n"), _LOGITS[dtype])
