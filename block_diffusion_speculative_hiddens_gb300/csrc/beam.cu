@@ -16,16 +16,19 @@
 // Sums: exponents are taken to base 2 against an integer reference, so that sums
 // join by shifts.  A thread's sum is two floats of 256 terms each at most, then a
 // 64-bit fixed-point number, as a warp's and a row's is (floats that took all of a
-// long row's 32,768 terms were off by up to 5e-4).
+// long row's 32,768 terms were off by up to 5e-4; 0.2 us of the batch below).  Logits
+// that do not fit such a reference, and what is not finite, take a second pass: 3 x 32
+// beams, f32, half of each row masked by the type's lowest value, 28.8 us against 21.7
+// with -1e9 or -inf.
 //
 // Measured in graphs of six calls (bf16, 151,936 tokens).  64 requests of 8 beams,
-// 156 MB: 37.1 us, 23 of them the logits' at the copy rate; the scan alone 29 to 31,
+// 156 MB: 36.5 us, 23 of them the logits' at the copy rate; the scan alone 28 to 30,
 // 512 CTAs of a row each on 608 places (two or three parts a row: 39 to 42 us in all,
 // an odd number of CTAs an SM costs less than the parts' ends), then 4 to 5 of join
-// behind it.  One request of 4 beams 8.7 us: 3.5 of scan, 5 of join, a chain of some
+// behind it.  One request of 4 beams 8.3 us: 3.5 of scan, 5 of join, a chain of some
 // twenty dependent steps of 100 to 1,000 cycles each.  Rows at odd addresses (f16,
-// 100,003 tokens, 11 x 5) 12.0 us; f32, 3 x 32 beams, n 64, 98 % masked 22.7 us, 9 of
-// scan: three CTAs look into 80 cells of 96 vectors each (28.9 with a vector a thread
+// 100,003 tokens, 11 x 5) 11.7 us; where memory binds, 512 x 8 rows of 50,257 tokens 147
+// us, 88 with 50,256.  f32, 3 x 32 beams, n 64, 98 % masked 22.3 us, 9 of scan: three CTAs look into 80 cells of 96 vectors each (28.9 with a vector a thread
 // in turns and scores at once, 24.3 with four vectors on their way, 23.8 with eight,
 // which spill).
 // Tried and left: the n best of every part chosen in the scan, from which the join
@@ -967,7 +970,9 @@ int beam_check(int batch, int beams, int vocab, int n, int dtype) {
   return (long long)batch * beams * MAX_SPLITS > 0x7fffffffll ? DFLASH_ERR_CAPACITY : DFLASH_OK;
 }
 
-// Parts of a row: as many CTAs as run at once, none with less than half a batch.
+// Parts of a row: together no more CTAs than run at once, none with less than half a
+// batch.  From 305 rows on a row is one part, and from 609 on the last ones run behind
+// the others (80 x 8 beams of 151,936 tokens 48 us, 64 x 8 of them 36.5).
 // Cells: a thread's in up to MAX_SEGMENTS segments, but no more of a request than
 // the join holds: fewer segments, then more threads a cell.  That fits: 608 parts of
 // 256 / 32 cells, or 64 of one part each.

@@ -67,9 +67,11 @@ DFL_DEV void count_entries(const Pool& p, const int (&more)[4], unsigned m, cons
 // that stay as they are (a long shared prefix) cost their reads only.  The
 // lengths, which every CTA reads, are written by the last one.
 // Bound by latency: parents, lengths, entries and counts are four loads deep, each
-// 0.4 us.  Four rows of 33 pages 2.2 us; 512 rows of 16 to 512 pages 4 us (counting
-// an entry's two pages one after the other: 5.7; every row's units unrolled, 69 KB
-// of code that each call fetches anew: 7.7).
+// 0.4 us, and the value that a subtraction found.  Four rows of 33 pages 2.4 us; 512
+// rows of 16 to 512 pages 4.4 us (4 without looking at that value; counting an entry's
+// two pages one after the other: 5.7; every row's units unrolled, 69 KB of code that
+// each call fetches anew: 7.7).  Rows of more units than threads, several a thread:
+// 1,025 of up to 32 pages 10 us, 2,048 of up to 64 19, 8,192 of up to 128 72.
 constexpr int FORK_THREADS = 1024;
 
 DFL_DEV int4 load_entries(const Pool& p, int row, int col, bool vec) {
@@ -280,9 +282,11 @@ DFL_DEV Part scan_part(int n_pages, int ctas, int rank) {
 // that does not fit changes nothing.
 // Bound by latency: 64 requests for 16 positions more in a pool of 3,700 pages 4.7
 // us.  512 beams for one more over 24,000 pages, some 140 with a copy of a shared last
-// page, while 104 leave with 27,000 entries: 14.4 us, 6 of them the leavers' counts, which eight
-// SMs take at about an entry a cycle; a second launch with all SMs would cost every
-// other call 3 us of launching and waiting.
+// page, while 104 leave with 27,000 entries: 13.4 us, about 5 of them the leavers' counts,
+// which eight SMs take at about two entries a cycle (16 us in a pool with pins, where each
+// count is read before it is changed); a second launch with all SMs would cost every
+// other call 3 us of launching and waiting.  refs are what a large pool costs: 2^20
+// pages 13 us, 2^24 204.
 
 // Exclusive sum over the block of a value a thread (need in the low 48 bits,
 // copies above).  buf: [SCAN_WARPS + 1].
@@ -552,7 +556,8 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) k_resize(const Pool p, const 
 // The same scan, with free pages ranked below the border and held ones above it.
 // Ranks pair them; moves is the list of pairs, remap their table form.  225 pages with
 // 16 rows of 48 entries 4.5 us, 3,501 pages with 32 rows of 68 7.6 us: three exchanges
-// of counts and two passes over memory behind one another.
+// of counts and two passes over memory behind one another.  Large pools are gone
+// through three times by eight SMs: 2^20 pages 81 us, 2^24 1,364, with nothing to move.
 
 // REMAP_EACH entries of a row, `width` apart, to their pages' new places.
 constexpr int REMAP_THREADS = 256;
@@ -688,6 +693,9 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1) k_compact(const Pool p, int* 
 // a page's chunks next to one another in the round (then whole CTAs have the empty
 // ones) 167, bulk copies through a ring in shared memory 152 to 164 (3 to 8 slots of 8
 // to 32 KB, 64 to 192 KB an SM on their way); four pages in one layer 2.5 us.
+// 400 whole pages of 64 x 8 x 128 in 4 layers (839 MB) 132 us; with heads 136 apart 178;
+// heads 129 apart, which take 2 bytes an access, 606; heads of 127 next to one another,
+// also 2 bytes, 319.
 constexpr int COPY_THREADS = 128;
 constexpr int COPY_AHEAD = 4;
 constexpr int COPY_CTAS = 16;    // of an SM
