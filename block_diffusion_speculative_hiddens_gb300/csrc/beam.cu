@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, SCAN_CTAS) k_beam_scan(const Bea
   auto see = [&](float m) {  // a maximum, before its terms
     top = fmaxf(top, m);
     const float t = m * LOG2E_HI;
-    if (t > q + 2.0f) {  // terms stay below 2^2.5
+    if (t > q + 2.0f) {  // terms stay below 2^2.5 (2^67 where the reference has a unit of 128)
       const float to = rintf(t), f = pow2_or_0(q - to);
       sum2 = fma2(sum2, pair(f, f), pair(0.0f, 0.0f));
       q = to;
