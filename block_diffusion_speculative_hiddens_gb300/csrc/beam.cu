@@ -68,7 +68,8 @@ constexpr float LOG2E_HI = 1.44269502162933349609f;
 constexpr float LOG2E_LO = 1.92596299112661746887e-8f;
 constexpr double LN2 = 0.693147180559945309417232121458;
 // Logits below it have references that fit: the rounded x * LOG2E_HI is whole and
-// below 2^31, and within 65 of the logit's exponent (its unit is 128 there).
+// below 2^31, and within 92 of the logit's exponent (half of its unit, 128 there, and
+// x * LOG2E_LO, 27), which a float's range holds.
 constexpr float EXACT = 1.4e9f;
 
 // A sum of exponentials: units of 2^(q - FIX).
@@ -307,7 +308,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, SCAN_CTAS) k_beam_scan(const Bea
   auto see = [&](float m) {  // a maximum, before its terms
     top = fmaxf(top, m);
     const float t = m * LOG2E_HI;
-    if (t > q + 2.0f) {  // terms stay below 2^2.5 (2^67 where the reference has a unit of 128)
+    if (t > q + 2.0f) {  // terms stay below 2^2.5 (below 2^92 near EXACT)
       const float to = rintf(t), f = pow2_or_0(q - to);
       sum2 = fma2(sum2, pair(f, f), pair(0.0f, 0.0f));
       q = to;
